@@ -36,9 +36,20 @@ GQA_DEV_BAD_SEQ_LEN = 1
 GQA_DEV_WAIT_TIMEOUT = 2
 GQA_DEV_INTERNAL = 4
 GQA_DEV_BAD_BLOCK = 8
+GQA_DEV_BAD_TOKENS = 16
+
+GQA_ROPE_HALF = 0
+GQA_ROPE_PAIRS = 1
+GQA_ROPE_PLAIN = 0
+GQA_ROPE_LINEAR = 1
+GQA_ROPE_WAVELENGTH = 2
+GQA_ROPE_YARN = 3
 
 # every function the header declares, with its C signature
 _VP, _I, _F, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
+_D = ctypes.c_double
+# q .. rope_scale, q_out, k_cache, v_cache of the rotate-and-append calls
+_ROPE = [_VP, _VP, _VP, _LL, _LL, _LL, _VP, _VP, _VP, _VP, _F, _VP, _I, _I, _F, _VP, _VP, _VP]
 SIGNATURES = {
     "gqa_kv_append": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP]),
     "gqa_decode_attn": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _F, _VP, _I, _I, _VP]),
@@ -65,6 +76,15 @@ SIGNATURES = {
     "gqa_decode_plan": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_I),
                              ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_I),
                              ctypes.POINTER(_LL), ctypes.POINTER(_I)]),
+    "gqa_rope_table": (_I, [_I, _D, _I, _D, _D, _D, _D, ctypes.POINTER(ctypes.c_uint64),
+                            ctypes.POINTER(_F)]),
+    "gqa_rope_append": (_I, _ROPE + [_I] * 8 + [_VP]),
+    "gqa_rope_append_paged": (_I, _ROPE + [_VP] + [_I] * 10 + [_VP]),
+    "gqa_rope_append_fp8_paged": (_I, _ROPE + [_VP, _VP, _VP] + [_I] * 10 + [_VP]),
+    "gqa_kv_read_fp8_paged": (_I, [_VP] * 8 + [_I] * 9 + [_VP]),
+    "gqa_chunk_attn": (_I, [_VP] * 5 + [_I] * 6 + [_F, _VP, _I, _I, _VP, _LL, _VP]),
+    "gqa_chunk_attn_paged": (_I, [_VP] * 6 + [_I] * 6 + [_F, _VP] + [_I] * 4 + [_VP, _LL, _VP]),
+    "gqa_chunk_attn_workspace": (_I, [_I] * 6 + [ctypes.POINTER(_LL)]),
     "gqa_device_status": (_I, [_VP, ctypes.POINTER(ctypes.c_uint32)]),
     "gqa_selftest_wait_timeout": (_I, [_LL, _VP]),
     "gqa_status_string": (ctypes.c_char_p, [_I]),
@@ -407,6 +427,245 @@ def gqa_decode_plan(b, n, h, g, d_k, d_v, cap, dtype, num_sms=0, flags=0) -> dic
         ctypes.byref(cl)))
     return {"kernels": k.value, "ctas": c.value, "tile": t.value, "tensor_core": bool(tc.value),
             "workspace_bytes": ws.value, "cluster": cl.value}
+
+
+# ---------------------------------------------------------------------------
+# packed tokens, 8-bit cache
+# ---------------------------------------------------------------------------
+def _tensor(x, name, nbytes, types=None) -> int:
+    """_ptr for the calls on packed tokens: also refuses a tensor of another
+    device than the current one (whose stream the call runs on) and one of
+    another type."""
+    if isinstance(x, torch.Tensor):
+        if types is not None and x.dtype not in types:
+            raise ValueError(f"{name}: must be {' or '.join(map(str, types))}, got {x.dtype}")
+        if x.is_cuda and x.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name}: on {x.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    return _ptr(x, name, nbytes)
+
+
+def _tokens(x, name, total, heads, d, types):
+    """Pointer and token stride (elements) of a packed tensor [total, heads, d]
+    whose heads are contiguous; consecutive tokens may lie further apart."""
+    if not isinstance(x, torch.Tensor):
+        return _ptr(x, name), heads * d
+    if tuple(x.shape) != (total, heads, d):
+        raise ValueError(f"{name}: must be [{total}, {heads}, {d}], got {list(x.shape)}")
+    st = x.stride()
+    if total > 0 and (st[2] != 1 and d > 1 or st[1] != d and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {x.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if x.dtype not in types:
+        raise ValueError(f"{name}: must be {types[0]}, got {x.dtype}")
+    p = x.data_ptr() if x.is_cuda else _HostTensor(name, x.device)
+    return p, st[0] if total > 1 else heads * d
+
+
+_TORCH = {GQA_F32: (torch.float32,), GQA_BF16: (torch.bfloat16,), GQA_F16: (torch.float16,)}
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def gqa_rope_table(rot, theta=10000.0, scaling="none", factor=1.0, original_len=0.0, low=1.0,
+                   high=32.0, device=None):
+    """Position table of gqa_rope_append: (phase, rope_scale), phase an int64
+    tensor [rot / 2] on `device` (the current CUDA device by default; made
+    once, kept by the caller).  scaling: "none", "linear", "wavelength" or
+    "yarn" (or a GQA_ROPE_* code), see include/gqa.h."""
+    codes = {"none": GQA_ROPE_PLAIN, "linear": GQA_ROPE_LINEAR,
+             "wavelength": GQA_ROPE_WAVELENGTH, "yarn": GQA_ROPE_YARN}
+    if isinstance(scaling, str) and scaling not in codes:
+        raise ValueError(f"scaling: one of {sorted(codes)}, got {scaling!r}")
+    host = (ctypes.c_uint64 * max(1, int(rot) // 2))()
+    scale = ctypes.c_float(0.0)
+    _check("gqa_rope_table", lib.gqa_rope_table(
+        int(rot), float(theta), codes[scaling] if isinstance(scaling, str) else int(scaling),
+        float(factor), float(original_len), float(low), float(high), host, ctypes.byref(scale)))
+    phase = torch.tensor([v - (1 << 64) if v >> 63 else v for v in host], dtype=torch.int64)
+    return phase.to("cuda" if device is None else device), float(scale.value)
+
+
+def _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v, rope, rope_scale,
+               layout, q_weight, k_weight, eps, total, dtype):
+    """(dtype code, total, the arguments from q to rope_scale, q_out)."""
+    dt = _dtype(k_new, dtype)
+    ty = _TORCH.get(dt, ())
+    if total is None:
+        total = k_new.shape[0]
+    e = _elt(dt)
+    qp, qs = (0, 0) if q is None else _tokens(q, "q", total, h, d_k, ty)
+    kp, ks = _tokens(k_new, "k_new", total, g, d_k, ty)
+    vp, vs = _tokens(v_new, "v_new", total, g, d_v, ty)
+    rot = 0
+    if isinstance(rope, torch.Tensor):
+        rot = 2 * rope.numel()
+    elif rope is not None:
+        raise ValueError("rope: must be the tensor of gqa_rope_table")
+    return dt, total, (
+        qp, kp, vp, qs, ks, vs, _tensor(cu_tokens, "cu_tokens", _n(b + 1) * 4, _I32),
+        _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32),
+        _tensor(q_weight, "q_weight", d_k * e, ty), _tensor(k_weight, "k_weight", d_k * e, ty),
+        float(eps), _tensor(rope, "rope", 0, (torch.int64,)), rot, int(layout),
+        float(rope_scale), _tensor(q_out, "q_out", _n(total, h, d_k) * e, ty))
+
+
+def gqa_rope_append(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_cache, v_cache, b, h, g, d_k,
+                    d_v, rope=None, rope_scale=1.0, layout=GQA_ROPE_HALF, q_weight=None,
+                    k_weight=None, eps=1e-6, total=None, cap=None, dtype=None,
+                    stream=None) -> None:
+    """Per-head norm (with q_weight and k_weight), rotary positions (rope and
+    rope_scale of gqa_rope_table) and append of packed tokens, in one launch.
+    q, k_new, v_new [total, heads, d] may be slices of one projection's
+    output (heads contiguous, tokens further apart); q_out may be q."""
+    dt, total, args = _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v,
+                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype)
+    if cap is None:
+        cap = k_cache.shape[2]
+    e, ty = _elt(dt), _TORCH.get(dt)
+    _call("gqa_rope_append", lib.gqa_rope_append, *args,
+          _tensor(k_cache, "k_cache", _n(b, g, cap, d_k) * e, ty),
+          _tensor(v_cache, "v_cache", _n(b, g, cap, d_v) * e, ty),
+          int(b), int(total), int(h), int(g), int(d_k), int(d_v), int(cap), dt, _stream(stream))
+
+
+def _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, e, ty):
+    """_paged_ptrs with the checks of _tensor."""
+    nb, _, bs, _ = k_pool.shape
+    mb = block_table.shape[1]
+    return (_tensor(k_pool, "k_pool", _n(nb, g, bs, d_k) * e, ty),
+            _tensor(v_pool, "v_pool", _n(nb, g, bs, d_v) * e, ty),
+            _tensor(block_table, "block_table", _n(b, mb) * 4, _I32), int(bs), int(mb), int(nb))
+
+
+def gqa_rope_append_paged(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_pool, v_pool,
+                          block_table, b, h, g, d_k, d_v, rope=None, rope_scale=1.0,
+                          layout=GQA_ROPE_HALF, q_weight=None, k_weight=None, eps=1e-6,
+                          total=None, dtype=None, stream=None) -> None:
+    """gqa_rope_append into a paged cache (pools [num_blocks, g, block_size,
+    d], block_table [b, max_blocks])."""
+    dt, total, args = _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v,
+                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype)
+    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, _elt(dt),
+                                    _TORCH.get(dt))
+    _call("gqa_rope_append_paged", lib.gqa_rope_append_paged, *args, kp, vp, tp, int(b),
+          int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, _stream(stream))
+
+
+def _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g, d_k, d_v):
+    """_pools of an 8-bit cache, with the pointers of its scales [num_blocks,
+    g, block_size]."""
+    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, 1, _E4M3)
+    n = _n(nb, g, bs) * 4
+    return (kp, vp, _tensor(k_scale, "k_scale", n, _F32), _tensor(v_scale, "v_scale", n, _F32),
+            tp, bs, mb, nb)
+
+
+def gqa_rope_append_fp8_paged(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_pool, v_pool,
+                              k_scale, v_scale, block_table, b, h, g, d_k, d_v, rope=None,
+                              rope_scale=1.0, layout=GQA_ROPE_HALF, q_weight=None, k_weight=None,
+                              eps=1e-6, total=None, dtype=None, stream=None) -> None:
+    """gqa_rope_append into an 8-bit paged cache: e4m3 pools (torch.float8_e4m3fn
+    or uint8) and one fp32 scale per row.  q = q_out = None with rope = None
+    is the plain quantising append."""
+    dt, total, args = _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v,
+                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype)
+    kp, vp, ks, vs, tp, bs, mb, nb = _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g,
+                                             d_k, d_v)
+    _call("gqa_rope_append_fp8_paged", lib.gqa_rope_append_fp8_paged, *args, kp, vp, ks, vs, tp,
+          int(b), int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt,
+          _stream(stream))
+
+
+def gqa_kv_read_fp8_paged(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_cache,
+                          v_cache, b, g, d_k, d_v, cap=None, dtype=None, stream=None) -> None:
+    """Rows [0, seq_lens[i]) of an 8-bit paged cache as contiguous caches
+    [b, g, cap, d] of the caches' type."""
+    dt = _dtype(k_cache, dtype)
+    e, ty = _elt(dt), _TORCH.get(dt)
+    if cap is None:
+        cap = k_cache.shape[2]
+    kp, vp, ks, vs, tp, bs, mb, nb = _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g,
+                                             d_k, d_v)
+    _call("gqa_kv_read_fp8_paged", lib.gqa_kv_read_fp8_paged, kp, vp, ks, vs, tp,
+          _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32),
+          _tensor(k_cache, "k_cache", _n(b, g, cap, d_k) * e, ty),
+          _tensor(v_cache, "v_cache", _n(b, g, cap, d_v) * e, ty), int(b), int(g), int(d_k),
+          int(d_v), bs, mb, nb, int(cap), dt, _stream(stream))
+
+
+def gqa_chunk_attn_workspace(total, h, g, d_k, d_v, num_sms=0) -> int:
+    """Bytes of workspace of gqa_chunk_attn(_paged) for up to `total` packed
+    rows (host only when num_sms > 0)."""
+    n = ctypes.c_longlong(0)
+    _check("gqa_chunk_attn_workspace", lib.gqa_chunk_attn_workspace(
+        int(total), int(h), int(g), int(d_k), int(d_v), int(num_sms), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _workspace(ws, stream, like, size, *shape):
+    """The workspace argument (tensor, bytes): the caller's, or a tensor made
+    for this call on its stream (the allocator orders its next use behind
+    the call)."""
+    if ws is None and isinstance(like, torch.Tensor) and like.is_cuda:
+        n = size(*shape)
+        if stream is None:
+            ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else (
+                torch.cuda.ExternalStream(int(stream), device=like.device))
+            with torch.cuda.stream(s):
+                ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+    if isinstance(ws, torch.Tensor):
+        return _tensor(ws, "workspace", 0), ws.numel() * ws.element_size(), ws
+    if ws is None:
+        return 0, 0, None
+    raise ValueError("workspace: must be a tensor")
+
+
+def gqa_chunk_attn(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, scale, out,
+                   total=None, cap=None, dtype=None, workspace=None, stream=None) -> None:
+    """Causal attention of packed chunks of new tokens (q [total, h, d_k], out
+    [total, h, d_v]) over caches that already hold their rows.  workspace:
+    a uint8 tensor of gqa_chunk_attn_workspace bytes to reuse between calls
+    (by default one is made per call)."""
+    dt = _dtype(q, dtype)
+    e, ty = _elt(dt), _TORCH.get(dt)
+    if total is None:
+        total = q.shape[0]
+    if cap is None:
+        cap = k_cache.shape[2]
+    wp, wn, _keep = _workspace(workspace, stream, q, gqa_chunk_attn_workspace, total, h, g, d_k,
+                               d_v)
+    _call("gqa_chunk_attn", lib.gqa_chunk_attn, _tensor(q, "q", _n(total, h, d_k) * e, ty),
+          _tensor(k_cache, "k_cache", _n(b, g, cap, d_k) * e, ty),
+          _tensor(v_cache, "v_cache", _n(b, g, cap, d_v) * e, ty),
+          _tensor(cu_tokens, "cu_tokens", _n(b + 1) * 4, _I32),
+          _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32), int(b), int(total), int(h), int(g),
+          int(d_k), int(d_v), float(scale), _tensor(out, "out", _n(total, h, d_v) * e, ty),
+          int(cap), dt, wp, wn, _stream(stream))
+
+
+def gqa_chunk_attn_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k, d_v,
+                         scale, out, total=None, dtype=None, workspace=None,
+                         stream=None) -> None:
+    """gqa_chunk_attn over a paged cache."""
+    dt = _dtype(q, dtype)
+    e, ty = _elt(dt), _TORCH.get(dt)
+    if total is None:
+        total = q.shape[0]
+    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, e, ty)
+    wp, wn, _keep = _workspace(workspace, stream, q, gqa_chunk_attn_workspace, total, h, g, d_k,
+                               d_v)
+    _call("gqa_chunk_attn_paged", lib.gqa_chunk_attn_paged,
+          _tensor(q, "q", _n(total, h, d_k) * e, ty), kp, vp, tp,
+          _tensor(cu_tokens, "cu_tokens", _n(b + 1) * 4, _I32),
+          _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32), int(b), int(total), int(h), int(g),
+          int(d_k), int(d_v), float(scale), _tensor(out, "out", _n(total, h, d_v) * e, ty), bs,
+          mb, nb, dt, wp, wn, _stream(stream))
 
 
 def gqa_device_status(stream=None) -> int:

@@ -1,0 +1,994 @@
+// chunk_attn.cu - causal attention of packed chunks of new tokens (prompts,
+// prompt chunks, single tokens, mixed) over a contiguous or paged 16-bit
+// cache, on the tcgen05 tensor cores.
+//
+// A unit is a block of query rows of one (sequence, KV head): the r = h / g
+// query heads of a group share K and V, so rows are packed token-major (row
+// s * r + a), tq = 128 / r tokens to an M = 128 tile and two tiles ("sides" A
+// and B) to a unit.  Per 128 cached positions and side:
+//
+//   S [128 x 128] = Q_side . K_tile^T             (tcgen05.mma, operands in shared memory)
+//   P = exp2(scale*log2e * S - m)                 (CUDA cores; one thread per row)
+//   O [128 x d_v] += P . V_tile                   (tcgen05.mma, P in tensor memory)
+//
+// While one side's softmax runs, the tensor cores work on the other side.
+// m is a row's running maximum, raised only when it grows by more than 2^8
+// in the exponent (P stays below 2^8, so 16-bit P and fp32 sums lose
+// nothing); O is rescaled in tensor memory on those occasions alone.  P is
+// rounded to the cache's type for the product; the row sum adds the fp32
+// values.
+//
+// Roles (384 threads, one persistent CTA per SM):
+//   warps 0-3  softmax of side A, output; thread = query row = TMEM lane
+//   warps 4-7  the same for side B
+//   warp 8     one lane issues every product
+//   warp 9     TMA: the sides' query rows once per unit, K and V tiles into a
+//              ring (64-column boxes, 128-byte swizzle)
+//   (warps 10 and 11 idle: registers are dealt out by warpgroups)
+// TMEM columns: S_A 0-127, S_B 128-255 (each holds P, two 16-bit values a
+// column, once its S has been read), O_A 256.., O_B 384...
+//
+// Work split.  A unit has as many tiles as its last token sees.  All units'
+// tiles are laid end to end, and each CTA takes an equal run of them, so the
+// triangle of a causal prompt, ragged batches and a few long sequences all
+// spread evenly; a run's ends snap to a unit's edge when it is close.  A unit
+// cut by a run's end leaves partial results (row maximum, sum, unnormalised
+// output, all fp32) in the workspace, and a second small kernel joins them.
+//
+// Rows >= L_i: masked out of S, their V rows zeroed in shared memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "../../include/gqa.h"
+#include "gqa_internal.h"
+#include "serve_device.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kM = 128;           // query rows of a side
+constexpr int kN = 128;           // positions of a tile
+constexpr int kThreads = 384;     // two softmax warpgroups, one of single warps
+// registers a thread: launched with 168 (65,536 over three warpgroups), then
+// split unevenly: 2 x 128 x 208 + 128 x 88 = 384 x 168
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kDescInts = 8;      // per CTA, see below
+constexpr int kSegs = 4;          // segments announced ahead
+constexpr int kSegBytes = 48;
+// a row's reference maximum is raised when the new one is this much larger
+// (base 2)
+constexpr float kRaise = 8.f;
+
+template <int DK, int DV>
+struct ChunkCfg {
+  static constexpr int Q_BYTES = kM * DK * 2;  // one side
+  static constexpr int SLOT = kN * (DK > DV ? DK : DV) * 2;
+  // ring slots: K and V tiles by turns
+  static constexpr int NS = DK == 128 ? 5 : (DV == 128 ? 6 : 8);
+  static constexpr int OFF_RING = 2 * Q_BYTES;
+  static constexpr int OFF_BAR = OFF_RING + NS * SLOT;
+  static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
+                       S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
+                       SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
+                       DRAIN = V_EDGE + 1, NBAR = DRAIN + 1;
+  static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
+  static constexpr int OFF_MISC = OFF_SEG + kSegs * kSegBytes;
+  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int T_S = 0, T_O = 256;  // TMEM columns, 128 to a side
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct ChunkParams {
+  const int *cu, *lens, *table;
+  int b, total, h, g, r, tq;
+  long long cap;       // positions a sequence can hold
+  int bsz, max_blocks, num_blocks;
+  float scale_log2;
+  void* out;
+  int* desc;           // [grid][kDescInts]
+  float* part_ml;      // [2 * grid][srows][2]
+  float* part_o;       // [2 * grid][srows][d_v]
+  int srows;
+  unsigned int* status;
+  long long budget;
+};
+
+// sum over k < n of floor((a k + b) / 128), by Euclid's reduction
+__device__ __forceinline__ long long floor_sum128(long long n, int a, long long b) {
+  long long m = 128, aa = a, ans = 0;
+  while (n > 0) {
+    if (aa >= m) {
+      ans += (n - 1) * n / 2 * (aa / m);
+      aa %= m;
+    }
+    if (b >= m) {
+      ans += n * (b / m);
+      b %= m;
+    }
+    const long long y = aa * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long tmp = m;
+    m = aa;
+    aa = tmp;
+  }
+  return ans;
+}
+
+struct ChunkSeg {
+  int i, j;        // sequence, KV head
+  int t0;          // packed row of the unit's first token
+  int pos0;        // its position
+  int ntok;        // tokens of the unit
+  int L;
+  int lt0, lt1;    // tiles of the unit taken here
+  int ti;          // tiles of the unit
+  // tiles each side needs of [lt0, lt1)
+  __device__ int side_tiles(int side, int tq) const {
+    const int nt = min(ntok - side * tq, tq);
+    if (nt <= 0) return 0;
+    const int ext = pos0 + side * tq + nt;
+    return max(0, min(lt1, (ext + kN - 1) / kN) - lt0);
+  }
+};
+
+static_assert(sizeof(ChunkSeg) <= kSegBytes, "segment ring");
+
+// The run of tiles of one CTA, cut into segments of units.  The TMA warp walks
+// (warp-uniform values) and announces each segment to the others through a
+// ring in shared memory.
+struct ChunkWalk {
+  const int *cu, *lens;
+  int b, g, tq2, total;
+  long long cap;
+  long long pos, end;
+  int i, j, qt, lt;       // cursor
+  int t0, n, L, nqt;      // of sequence i
+
+  __device__ bool seq(int k, int& a0, int& nn, int& Lk) const {
+    a0 = nn = Lk = 0;
+    if (k >= b) return false;
+    a0 = __ldg(cu + k);
+    const int a1 = __ldg(cu + k + 1);
+    Lk = __ldg(lens + k);
+    if (packed_errors(a0, a1, Lk, total, cap)) return false;
+    nn = a1 - a0;
+    return nn > 0;
+  }
+  // tiles of the first q units (q <= nqt) of a sequence
+  __device__ long long prefix(int q, int nn, int Lk, int nq) const {
+    const int full = min(q, nq - 1);  // units that hold tq2 tokens
+    long long s = floor_sum128(full, tq2, static_cast<long long>(Lk) - nn + tq2 + kN - 1);
+    if (q == nq) s += (Lk + kN - 1) / kN;
+    return s;
+  }
+  __device__ int units(int nn) const { return (nn + tq2 - 1) / tq2; }
+  __device__ int unit_tiles(int q) const {
+    const int ext = (q == nqt - 1) ? L : L - n + (q + 1) * tq2;
+    return (ext + kN - 1) / kN;
+  }
+
+  __device__ long long total_tiles() const {
+    long long acc = 0;
+    for (int k = threadIdx.x & 31; k < b; k += 32) {
+      int a0, nn, Lk;
+      if (seq(k, a0, nn, Lk)) {
+        const int nq = units(nn);
+        acc += prefix(nq, nn, Lk, nq);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    return acc * g;
+  }
+
+  // put the cursor on global tile x (0 <= x < W)
+  __device__ void locate(long long x) {
+    const int lane = threadIdx.x & 31;
+    long long carry = 0;
+    for (int base = 0; base < b; base += 32) {
+      int a0, nn, Lk;
+      long long f = 0;
+      if (seq(base + lane, a0, nn, Lk)) {
+        const int nq = units(nn);
+        f = prefix(nq, nn, Lk, nq);
+      }
+      long long incl = f * g;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const long long hi = carry + incl, lo = hi - f * g;
+      const unsigned hit = __ballot_sync(0xffffffffu, f > 0 && lo <= x && x < hi);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        i = base + src;
+        t0 = __shfl_sync(0xffffffffu, a0, src);
+        n = __shfl_sync(0xffffffffu, nn, src);
+        L = __shfl_sync(0xffffffffu, Lk, src);
+        nqt = units(n);
+        const long long off = x - __shfl_sync(0xffffffffu, lo, src);
+        const long long fs = __shfl_sync(0xffffffffu, f, src);
+        j = static_cast<int>(off / fs);
+        const long long rem = off - j * fs;
+        // the last unit q with prefix(q) <= rem: 32 probes a round
+        int q0 = 0, cnt = nqt;
+        while (cnt > 1) {
+          const int step = (cnt + 31) >> 5;
+          const int q = q0 + lane * step;
+          const bool le = lane * step < cnt && prefix(q, n, L, nqt) <= rem;
+          const int m = __popc(__ballot_sync(0xffffffffu, le));  // >= 1
+          q0 += (m - 1) * step;
+          cnt = min(step, cnt - (m - 1) * step);
+        }
+        qt = q0;
+        lt = static_cast<int>(rem - prefix(q0, n, L, nqt));
+        return;
+      }
+      carry = __shfl_sync(0xffffffffu, hi, 31);
+    }
+    i = b;  // not reached for x < W
+  }
+
+  // Start of run c: c * W / nc, moved to the edge of the unit it falls into
+  // when that is at most `tol` tiles away.
+  __device__ long long run_start(int c, long long W, int nc, long long tol) {
+    const long long x = W * c / nc;
+    if (tol <= 0 || x <= 0 || x >= W) return x;
+    locate(x);
+    if (i >= b) return x;
+    if (lt <= tol) return x - lt;
+    const int left = unit_tiles(qt) - lt;
+    return left <= tol ? x + left : x;
+  }
+
+  __device__ void init(const ChunkParams& p, int c, int nc) {
+    cu = p.cu;
+    lens = p.lens;
+    b = p.b;
+    g = p.g;
+    tq2 = 2 * p.tq;
+    total = p.total;
+    cap = p.cap;
+    pos = end = 0;
+    const long long W = total_tiles();
+    if (W == 0) return;
+    // at least two tiles a run: a piece of one costs more to join than it saves
+    nc = static_cast<int>(min(static_cast<long long>(nc), (W + 1) / 2));
+    if (c >= nc) return;
+    const long long tol = W / (static_cast<long long>(nc) * 32);
+    end = run_start(c + 1, W, nc, tol);
+    pos = run_start(c, W, nc, tol);
+    if (pos < end) locate(pos);
+  }
+
+  __device__ bool next(ChunkSeg& s, int tq) {
+    if (pos >= end || i >= b) return false;
+    const int ti = unit_tiles(qt);
+    const long long left = end - pos;
+    s.i = i;
+    s.j = j;
+    s.t0 = t0 + qt * tq2;
+    s.pos0 = L - n + qt * tq2;
+    s.ntok = min(n - qt * tq2, tq2);
+    s.L = L;
+    s.ti = ti;
+    s.lt0 = lt;
+    s.lt1 = (ti - lt <= left) ? ti : lt + static_cast<int>(left);
+    pos += s.lt1 - lt;
+    lt = s.lt1;
+    if (lt == ti && pos < end) {
+      lt = 0;
+      if (++qt == nqt) {
+        qt = 0;
+        if (++j == g) {
+          j = 0;
+          do {
+            ++i;
+          } while (i < b && !seq(i, t0, n, L));
+          nqt = units(n);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// desc of CTA c: a unit cut at its run's end (head) or start (tail / middle)
+enum { D_HEAD = 0, D_TOK0 = 1, D_NTOK = 2, D_J = 3, D_END = 4 };
+
+template <typename T16, int DK, int DV, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+  using C = ChunkCfg<DK, DV>;
+  constexpr bool kBf16 = Half16<T16>::kBf16;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t s_base = smem_u32(sm);
+  if (s_base & 1023u) {  // never seen; the swizzled layouts need it
+    if (threadIdx.x == 0) atomicOr(p.status, GQA_DEV_INTERNAL);
+    return;
+  }
+  auto BAR = [&](int k) -> uint32_t { return s_base + C::OFF_BAR + 8u * k; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < C::NBAR; ++k)
+      mbar_init(BAR(k), (k == C::P_READY || k == C::P_READY + 1)              ? 4
+                        : (k >= C::SEG_EMPTY && k < C::SEG_EMPTY + kSegs) ? 9
+                                                                          : 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9 && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait_then_release();
+  if (warp == 9 && blockIdx.x == 0)
+    report_bad_packed(p.cu, p.lens, p.b, p.total, p.cap, p.status);
+
+  auto seg_at = [&](uint32_t k) -> ChunkSeg* {
+    return reinterpret_cast<ChunkSeg*>(sm + C::OFF_SEG + (k % kSegs) * kSegBytes);
+  };
+  auto wait = [&](int k, uint32_t phase) -> bool {
+    return mbar_wait(BAR(k), phase & 1u, abort_flag, p.status, p.budget);
+  };
+
+  if (warp >= 10) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  } else if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    // ============================ TMA producer ============================
+    ChunkWalk w;
+    ChunkSeg seg;
+    w.init(p, blockIdx.x, gridDim.x);
+    const uint64_t pol = policy_evict_last();
+    const int oob_row = PAGED ? p.num_blocks * p.g * p.bsz : 0;
+    const int box = PAGED ? min(p.bsz, kN) : kN;
+    const int sub = kN / box;  // boxes a tile and 64-column half
+    uint32_t slot_n = 0, qn[2] = {0, 0}, edge_n = 0;
+    uint32_t kn = 0;  // segments announced
+    bool ok = true;
+    auto announce = [&](const ChunkSeg& sg) {
+      ok = __all_sync(0xffffffffu, wait(C::SEG_EMPTY + kn % kSegs, ((kn / kSegs) & 1) ^ 1));
+      if (!ok) return;
+      if (lane == 0) {
+        *seg_at(kn) = sg;
+        mbar_arrive(BAR(C::SEG_FULL + kn % kSegs));
+      }
+      __syncwarp();
+      ++kn;
+    };
+    while (ok && w.next(seg, p.tq)) {
+      announce(seg);
+      const int* trow =
+          PAGED ? p.table + static_cast<size_t>(seg.i) * p.max_blocks : nullptr;
+      // lane mm < sub: the pool row of box mm of tile lt
+      auto lookup = [&](int lt) -> int {
+        const int pm = lt * kN + lane * box;
+        if (lane >= sub || pm >= seg.L) return oob_row;
+        const int blk = __ldg(trow + pm / p.bsz);
+        if (blk < 0 || blk >= p.num_blocks) {
+          atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+          return oob_row;
+        }
+        return (blk * p.g + seg.j) * p.bsz + pm % p.bsz;
+      };
+      auto load_q = [&](int side) {
+        if (!ok || seg.side_tiles(side, p.tq) == 0) return;
+        ok = __all_sync(0xffffffffu, wait(C::Q_EMPTY + side, (qn[side] & 1) ^ 1));
+        if (!ok) return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(BAR(C::Q_FULL + side), p.tq * p.r * DK * 2);
+          for (int c = 0; c < DK / 64; ++c)
+            tma_load_3d(s_base + side * C::Q_BYTES + c * (kM * 128), &tm_q, BAR(C::Q_FULL + side),
+                        64 * c, seg.j * p.r, seg.t0 + side * p.tq, pol);
+        }
+        ++qn[side];
+      };
+      auto load_kv = [&](bool is_v, int lt, int prow) {
+        if (!ok) return;
+        const int slot = slot_n % C::NS;
+        ok = __all_sync(0xffffffffu, wait(C::EMPTY + slot, ((slot_n / C::NS) & 1) ^ 1));
+        if (!ok) return;
+        const int nbox = (is_v ? DV : DK) / 64;
+        // a V tile that runs past L_i: its rows there are zeroed first
+        const bool edge = is_v && (lt + 1) * kN > seg.L;
+        const uint32_t bar = BAR(edge ? C::V_EDGE : C::FULL + slot);
+        const uint32_t dst = s_base + C::OFF_RING + slot * C::SLOT;
+        if (lane == 0) mbar_arrive_expect_tx(bar, nbox * kN * 128);
+        __syncwarp();
+        if (PAGED ? lane < sub : lane == 0) {
+          const int row = PAGED ? prow
+                                : static_cast<int>((static_cast<long long>(seg.i) * p.g + seg.j) *
+                                                   p.cap) + lt * kN;
+          for (int c = 0; c < nbox; ++c)
+            tma_load_2d(dst + c * (kN * 128) + lane * box * 128, is_v ? &tm_v : &tm_k, bar, 64 * c,
+                        row, pol);
+        }
+        if (edge) {
+          ok = __all_sync(0xffffffffu, wait(C::V_EDGE, edge_n & 1));
+          ++edge_n;
+          if (ok) {
+            const int first = seg.L - lt * kN;
+            for (int idx = first * 8 + lane; idx < kN * 8; idx += 32)
+              for (int c = 0; c < nbox; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 dst + c * (kN * 128) + idx * 16),
+                             "r"(0u)
+                             : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::FULL + slot));
+          }
+        }
+        ++slot_n;
+      };
+      int row = PAGED ? lookup(seg.lt0) : 0;
+      load_q(0);
+      load_kv(false, seg.lt0, row);
+      load_q(1);
+      for (int lt = seg.lt0; lt < seg.lt1 && ok; ++lt) {
+        const int cur = row;
+        if (PAGED && lt + 1 < seg.lt1) row = lookup(lt + 1);
+        // tile lt's V, then tile lt + 1's K: the order the products need them
+        load_kv(true, lt, cur);
+        if (lt + 1 < seg.lt1) load_kv(false, lt + 1, row);
+      }
+    }
+    if (ok) {
+      seg.lt0 = seg.lt1 = 0;  // no more
+      announce(seg);
+    }
+    if (!ok) {
+      // copies in flight must land before the CTA exits (bounded)
+      const long long t0 = clock64();
+      for (int s = 0; s < C::NS; ++s) {
+        if (slot_n <= static_cast<uint32_t>(s)) continue;
+        const uint32_t last = (slot_n - 1 - s) / C::NS;  // fills of slot s, less one
+        while (!mbar_try_wait(BAR(C::FULL + s), last & 1) && clock64() - t0 < p.budget) {
+        }
+      }
+      for (int s = 0; s < 2; ++s)
+        while (qn[s] > 0 && !mbar_try_wait(BAR(C::Q_FULL + s), (qn[s] - 1) & 1) &&
+               clock64() - t0 < p.budget) {
+        }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    // ============================ MMA issuer ==============================
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_bf16(kM, kN, 0, 0, kBf16);   // both K-major
+      constexpr uint32_t kIdescO = idesc_bf16(kM, DV, 0, 1, kBf16);   // V: MN-major
+      uint32_t slot_n = 0;      // ring position of the segment's first K
+      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
+      bool ok = true;
+      auto slot_full = [&](uint32_t x) -> bool {
+        return wait(C::FULL + x % C::NS, (x / C::NS) & 1);
+      };
+      auto issue_s = [&](int side, uint32_t x) {
+        const uint64_t a0 = smem_desc(s_base + side * C::Q_BYTES, 16, 1024, SWZ_128B);
+        const uint64_t b0 =
+            smem_desc(s_base + C::OFF_RING + (x % C::NS) * C::SLOT, 16, 1024, SWZ_128B);
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+          const uint32_t o = ((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4;
+          mma_bf16(tmem + C::T_S + side * 128, a0 + o, b0 + o, kIdescS, k > 0 ? 1u : 0u);
+        }
+        mma_commit(BAR(C::S_FULL + side));
+      };
+      auto issue_o = [&](int side, uint32_t x, bool first) {
+        const uint64_t b0 =
+            smem_desc(s_base + C::OFF_RING + (x % C::NS) * C::SLOT, kN * 128, 1024, SWZ_128B);
+#pragma unroll
+        for (int k = 0; k < kN / 16; ++k)
+          mma_16_ts(tmem + C::T_O + side * 128, tmem + C::T_S + side * 128 + 8 * k,
+                    b0 + k * (2048 >> 4), kIdescO, (first && k == 0) ? 0u : 1u);
+      };
+      for (uint32_t kn = 0;; ++kn) {
+        ok = ok && wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1);
+        if (!ok) break;
+        const ChunkSeg seg = *seg_at(kn);
+        mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+        if (seg.lt1 == seg.lt0) break;
+        const int nt[2] = {seg.side_tiles(0, p.tq), seg.side_tiles(1, p.tq)};
+        const int T = seg.lt1 - seg.lt0;
+        // ring: K_0, V_0, K_1, V_1, ...
+        auto kx = [&](int t) -> uint32_t { return slot_n + 2 * t; };
+        auto vx = [&](int t) -> uint32_t { return slot_n + 2 * t + 1; };
+        ok = slot_full(kx(0));
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (nt[s] == 0) continue;
+          ok = wait(C::Q_FULL + s, qn[s] & 1);
+          ++qn[s];
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(s, kx(0));
+        }
+        if (!ok) break;
+        mma_commit(BAR(C::EMPTY + kx(0) % C::NS));
+        for (int t = 0; t < T && ok; ++t) {
+          for (int s = 0; s < 2 && ok; ++s) {
+            if (t >= nt[s]) continue;
+            ok = wait(C::P_READY + s, pn[s] & 1) && slot_full(vx(t));
+            ++pn[s];
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(s, vx(t), t == 0);
+            if (t + 1 < nt[s]) {
+              ok = slot_full(kx(t + 1));
+              if (!ok) break;
+              issue_s(s, kx(t + 1));
+            } else {
+              mma_commit(BAR(C::O_DONE + s));
+              mma_commit(BAR(C::Q_EMPTY + s));
+            }
+          }
+          if (!ok) break;
+          // (a tile that no side needs any more is waited for all the same,
+          // so that its slot is not handed back while its copy is in flight)
+          ok = slot_full(vx(t)) && (t + 1 >= T || slot_full(kx(t + 1)));
+          mma_commit(BAR(C::EMPTY + vx(t) % C::NS));
+          if (t + 1 < T) mma_commit(BAR(C::EMPTY + kx(t + 1) % C::NS));
+        }
+        slot_n += 2 * T;
+      }
+      // every product has to be finished before tensor memory is released
+      mma_commit(BAR(C::DRAIN));
+      const long long t0 = clock64();
+      while (!mbar_try_wait(BAR(C::DRAIN), 0) && clock64() - t0 < p.budget) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ======================= softmax, output ==============================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int side = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;  // query row of the side = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::T_S + side * 128;
+    const uint32_t tO = tmem + lane_off + C::T_O + side * 128;
+    const int tok = row / p.r, head = row - tok * p.r;
+    // a scale of zero or below would turn the maximum around: it is applied
+    // to the logits first then
+    const bool pre = !(p.scale_log2 > 0.f);
+    const float sl = pre ? 1.f : p.scale_log2;
+    uint32_t sn = 0, on = 0;
+    int d_head = 0, d_tok0 = 0, d_ntok = 0, d_j = 0, d_end = 0;
+    bool ok = true;
+    for (uint32_t kn = 0;; ++kn) {
+      ok = ok && __all_sync(0xffffffffu, wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1));
+      if (!ok) break;
+      const ChunkSeg seg = *seg_at(kn);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+      if (seg.lt1 == seg.lt0) break;
+      const int nt = seg.side_tiles(side, p.tq);
+      const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
+      const int my_tok = side * p.tq + tok;  // token of the unit
+      const bool live = tok < p.tq && my_tok < seg.ntok;
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0);
+      if (seg.lt0 == 0 && !whole) {
+        d_head = 1;
+        d_tok0 = seg.t0;
+        d_ntok = seg.ntok;
+        d_j = seg.j;
+      } else if (seg.lt0 > 0) {
+        d_end = seg.lt1 == seg.ti;
+      }
+      float m = -INFINITY, l = 0.f;
+      const int my_pos = seg.pos0 + my_tok;
+      const int first_pos = seg.pos0 + side * p.tq;  // the side's first token
+      for (int t = 0; t < nt; ++t) {
+        ok = __all_sync(0xffffffffu, wait(C::S_FULL + side, sn & 1));
+        ++sn;
+        if (!ok) break;
+        tc_fence_after();
+        float x[kN];
+#pragma unroll
+        for (int c = 0; c < kN / 32; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
+        tmem_wait_ld();
+        if (pre) {
+#pragma unroll
+          for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
+        }
+        const int base = (seg.lt0 + t) * kN;
+        if (base + kN - 1 > first_pos) {
+          // positions past this row's token
+          const int lim = my_pos - base;
+#pragma unroll
+          for (int e = 0; e < kN; ++e)
+            if (e > lim) x[e] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < kN; e += 4)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[e + k]);
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        // S_FULL also covers the products issued before it: O is complete
+        // up to the last tile
+        if (__any_sync(0xffffffffu, (mn - m) * sl > kRaise)) {
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          const float alpha = ex2((m - ref) * sl);
+          m = mn;
+          l *= alpha;
+          if (t > 0) {
+#pragma unroll
+            for (int c = 0; c < DV / 8; ++c) {
+              float o[8];
+              tmem_ld8(tO + 8 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= alpha;
+              tmem_st8(tO + 8 * c, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m * sl;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kN / 64; ++c) {
+          uint32_t u[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float p0 = ex2(fmaf(x[64 * c + 2 * e], sl, off));
+            const float p1 = ex2(fmaf(x[64 * c + 2 * e + 1], sl, off));
+            sum[(2 * e) & 3] += p0;
+            sum[(2 * e + 1) & 3] += p1;
+            u[e] = Half16<T16>::pack2(p0, p1);
+          }
+          tmem_st32(tS + 32 * c, u);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      if (!ok) break;
+      if (nt > 0) {
+        ok = __all_sync(0xffffffffu, wait(C::O_DONE + side, on & 1));
+        ++on;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (whole) {
+        const float inv = 1.f / l;
+        T16* dst = static_cast<T16*>(p.out) +
+                   (static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head) * DV;
+#pragma unroll
+        for (int c = 0; c < DV / 32; ++c) {
+          if (nt == 0) break;  // (a side without tokens)
+          float o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              float y[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = o[e + k] * inv;
+              Piece8<T16>::store(dst + 32 * c + e, y);
+            }
+          }
+        }
+      } else {
+        const size_t at = slot * p.srows + side * kM + row;
+        if (live) {
+          p.part_ml[2 * at] = l > 0.f ? m * sl : -INFINITY;
+          p.part_ml[2 * at + 1] = l;
+        }
+#pragma unroll
+        for (int c = 0; c < DV / 32; ++c) {
+          if (nt == 0) break;
+          float o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(p.part_o + at * DV + 32 * c + e) =
+                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+    if (threadIdx.x == 0) {
+      int* d = p.desc + static_cast<size_t>(blockIdx.x) * kDescInts;
+      d[D_HEAD] = ok ? d_head : 0;
+      d[D_TOK0] = d_tok0;
+      d[D_NTOK] = d_ntok;
+      d[D_J] = d_j;
+      d[D_END] = ok ? d_end : 1;
+    }
+  }
+
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the units that a run's end cut: block (c, k) handles
+// rows [32 k, 32 k + 32) of the unit whose first piece is CTA c's, a warp to a
+// row.  With per-piece maxima m, sums l and unnormalised outputs O over
+// disjoint positions: M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, in
+// the pieces' order.
+template <typename T16, int DV>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p, int nc) {
+  pdl_wait_then_release();
+  const int c = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int* d = p.desc + static_cast<size_t>(c) * kDescInts;
+  if (!__ldg(d + D_HEAD)) return;
+  const int tok0 = __ldg(d + D_TOK0), ntok = __ldg(d + D_NTOK), j = __ldg(d + D_J);
+  // the CTA that holds the unit's last piece
+  int last = -1;
+  for (int base = c + 1; base < nc && last < 0; base += 32) {
+    const int k = base + lane;
+    const bool e = k < nc && __ldg(p.desc + static_cast<size_t>(k) * kDescInts + D_END);
+    const unsigned hit = __ballot_sync(0xffffffffu, e);
+    if (hit) last = base + __ffs(hit) - 1;
+  }
+  if (last < 0) return;  // (not reached unless a launch gave up)
+  constexpr int CPL = DV / 32;
+  for (int k = warp; k < 32; k += 8) {
+    const int row = blockIdx.y * 32 + k;
+    const int side = row / kM, rr = row % kM, tok = rr / p.r;
+    const int t = side * p.tq + tok;
+    if (row >= p.srows || tok >= p.tq || t >= ntok) continue;
+    auto at = [&](int x) -> size_t {
+      return static_cast<size_t>(2 * x + (x == c ? 1 : 0)) * p.srows + row;
+    };
+    float M = -INFINITY;
+    for (int x = c + lane; x <= last; x += 32) M = fmaxf(M, __ldg(p.part_ml + 2 * at(x)));
+    M = warp_max(M);
+    float den = 0.f, num[CPL];
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) num[e] = 0.f;
+    for (int x = c; x <= last; ++x) {
+      const float2 ml = __ldg(reinterpret_cast<const float2*>(p.part_ml) + at(x));
+      if (ml.x == -INFINITY) continue;  // a piece this row sees nothing of
+      const float wgt = ex2(ml.x - M);
+      den = fmaf(wgt, ml.y, den);
+      float o[CPL];
+      if constexpr (CPL == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p.part_o + at(x) * DV) + lane);
+        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+      } else {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(p.part_o + at(x) * DV) + lane);
+        o[0] = v.x, o[1] = v.y;
+      }
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) num[e] = fmaf(wgt, o[e], num[e]);
+    }
+    const float inv = 1.f / den;
+    T16* dst = static_cast<T16*>(p.out) +
+               (static_cast<size_t>(tok0 + t) * p.h + j * p.r + (rr - tok * p.r)) * DV +
+               lane * CPL;
+    if constexpr (CPL == 4) {
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(Half16<T16>::pack2(num[0] * inv, num[1] * inv),
+                     Half16<T16>::pack2(num[2] * inv, num[3] * inv));
+    } else {
+      *reinterpret_cast<uint32_t*>(dst) = Half16<T16>::pack2(num[0] * inv, num[1] * inv);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+struct ChunkCall {
+  const void *q, *k, *v;
+  const int *cu, *lens, *table;
+  int b, total, h, g, dk, dv;
+  float scale;
+  void* out;
+  int cap, bsz, max_blocks, num_blocks, dtype;
+  void* ws;
+  long long ws_bytes;
+};
+
+struct ChunkPlan {
+  int srows = 0;
+  size_t ml_at = 0, o_at = 0, bytes = 0;
+};
+
+ChunkPlan chunk_plan(int total, int h, int g, int dv, int num_sms) {
+  ChunkPlan pl;
+  const int r = h / g, tq = kM / r;
+  pl.srows = total <= tq ? kM : 2 * kM;
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  pl.ml_at = up(sizeof(int) * kDescInts * num_sms);
+  const size_t rows = 2 * static_cast<size_t>(num_sms) * pl.srows;
+  pl.o_at = up(pl.ml_at + rows * 2 * sizeof(float));
+  pl.bytes = up(pl.o_at + rows * dv * sizeof(float));
+  return pl;
+}
+
+int chunk_shape_check(int total, int h, int g, int dk, int dv) {
+  if (total < 0 || h < 1 || g < 1 || dk < 1 || dv < 1 || h % g != 0) return GQA_ERR_SHAPE;
+  if (static_cast<long long>(total) * h > 0x7FFFFFFFll) return GQA_ERR_SHAPE;
+  if (h / g > kM || (dk != 64 && dk != 128) || (dv != 64 && dv != 128))
+    return GQA_ERR_UNSUPPORTED;
+  return GQA_OK;
+}
+
+int chunk_check(const ChunkCall& x) {
+  if (!x.k || !x.v || !x.cu || !x.lens || !x.ws) return GQA_ERR_NULL;
+  if (x.total != 0 && (!x.q || !x.out)) return GQA_ERR_NULL;
+  if (x.dtype != GQA_F32 && x.dtype != GQA_BF16 && x.dtype != GQA_F16) return GQA_ERR_DTYPE;
+  if (x.b < 1 || x.cap < 1) return GQA_ERR_SHAPE;
+  if (int e = chunk_shape_check(x.total, x.h, x.g, x.dk, x.dv)) return e;
+  if (x.table == nullptr && static_cast<long long>(x.b) * x.g * x.cap + 256 > 0x7FFFFFFFll)
+    return GQA_ERR_SHAPE;
+  if (x.dtype == GQA_F32 || x.b > 65535) return GQA_ERR_UNSUPPORTED;
+  auto off = [](const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) != 0; };
+  if (off(x.q, 15) || off(x.k, 15) || off(x.v, 15) || off(x.out, 15) || off(x.cu, 3) ||
+      off(x.lens, 3) || off(x.ws, 255))
+    return GQA_ERR_ALIGN;
+  return GQA_OK;
+}
+
+template <typename T16, int DK, int DV, bool PAGED>
+cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
+                         unsigned int* status, cudaStream_t st) {
+  using C = ChunkCfg<DK, DV>;
+  constexpr bool kBf16 = Half16<T16>::kBf16;
+  ChunkParams p;
+  p.cu = x.cu;
+  p.lens = x.lens;
+  p.table = x.table;
+  p.b = x.b;
+  p.total = x.total;
+  p.h = x.h;
+  p.g = x.g;
+  p.r = x.h / x.g;
+  p.tq = kM / p.r;
+  p.cap = PAGED ? static_cast<long long>(x.max_blocks) * x.bsz : x.cap;
+  p.bsz = x.bsz;
+  p.max_blocks = x.max_blocks;
+  p.num_blocks = x.num_blocks;
+  p.scale_log2 = static_cast<float>(static_cast<double>(x.scale) * 1.4426950408889634);
+  p.out = x.out;
+  char* ws = static_cast<char*>(x.ws);
+  p.desc = reinterpret_cast<int*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + pl.ml_at);
+  p.part_o = reinterpret_cast<float*>(ws + pl.o_at);
+  p.srows = pl.srows;
+  p.status = status;
+  p.budget = kKernelWaitBudget;
+
+  CUtensorMap mq, mk, mv;
+  const uint64_t rows = PAGED ? static_cast<uint64_t>(x.num_blocks) * x.g * x.bsz
+                              : static_cast<uint64_t>(x.b) * x.g * x.cap;
+  const uint32_t box_rows = (PAGED && x.bsz < kN) ? x.bsz : kN;
+  const uint64_t qd[3] = {DK, static_cast<uint64_t>(x.h), static_cast<uint64_t>(x.total)};
+  const uint64_t qs[2] = {DK * 2, static_cast<uint64_t>(x.h) * DK * 2};
+  const uint32_t qb[3] = {64u, static_cast<uint32_t>(p.r), static_cast<uint32_t>(p.tq)};
+  const uint64_t kd[2] = {DK, rows}, ks[1] = {DK * 2};
+  const uint64_t vd[2] = {DV, rows}, vs[1] = {DV * 2};
+  const uint32_t kb[2] = {64u, box_rows};
+  if (!encode_bf16_map(&mq, x.q, 3, qd, qs, qb, kBf16) ||
+      !encode_bf16_map(&mk, x.k, 2, kd, ks, kb, kBf16) ||
+      !encode_bf16_map(&mv, x.v, 2, vd, vs, kb, kBf16))
+    return cudaErrorInvalidValue;
+  auto kern = chunk_attn_kernel<T16, DK, DV, PAGED>;
+  static std::atomic<unsigned long long> configured{0};  // devices done, this variant
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!(configured.load() & (1ull << dev))) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(1ull << dev);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p)) return e;
+  cfg.gridDim = dim3(num_sms, (pl.srows + 31) / 32);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T16, DV>, p, num_sms);
+}
+
+template <typename T16, bool PAGED>
+cudaError_t launch_chunk_dims(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
+                              unsigned int* status, cudaStream_t st) {
+  if (x.dk == 128)
+    return x.dv == 128 ? launch_chunk<T16, 128, 128, PAGED>(x, pl, num_sms, status, st)
+                       : launch_chunk<T16, 128, 64, PAGED>(x, pl, num_sms, status, st);
+  return x.dv == 128 ? launch_chunk<T16, 64, 128, PAGED>(x, pl, num_sms, status, st)
+                     : launch_chunk<T16, 64, 64, PAGED>(x, pl, num_sms, status, st);
+}
+
+int chunk_run(const ChunkCall& x, void* stream) {
+  if (int e = chunk_check(x)) return e;
+  int num_sms = 0;
+  unsigned int* status = nullptr;
+  if (int e = device_query(&num_sms, &status)) return e;
+  const ChunkPlan pl = chunk_plan(x.total, x.h, x.g, x.dv, num_sms);
+  if (x.ws_bytes < static_cast<long long>(pl.bytes)) return GQA_ERR_SCRATCH_LIMIT;
+  if (x.total == 0) return GQA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (x.table != nullptr)
+    e = x.dtype == GQA_F16 ? launch_chunk_dims<__half, true>(x, pl, num_sms, status, st)
+                           : launch_chunk_dims<__nv_bfloat16, true>(x, pl, num_sms, status, st);
+  else
+    e = x.dtype == GQA_F16 ? launch_chunk_dims<__half, false>(x, pl, num_sms, status, st)
+                           : launch_chunk_dims<__nv_bfloat16, false>(x, pl, num_sms, status, st);
+  return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" {
+
+int gqa_chunk_attn(const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* cu_tokens, const int32_t* seq_lens, int b, int total, int h,
+                   int g, int d_k, int d_v, float scale, void* out, int cap, int dtype,
+                   void* workspace, long long workspace_bytes, void* stream) {
+  const ChunkCall x = {q, k_cache, v_cache, cu_tokens, seq_lens, nullptr, b, total, h, g, d_k,
+                       d_v, scale, out, cap, 0, 0, 0, dtype, workspace, workspace_bytes};
+  return chunk_run(x, stream);
+}
+
+int gqa_chunk_attn_paged(const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_table, const int32_t* cu_tokens,
+                         const int32_t* seq_lens, int b, int total, int h, int g, int d_k,
+                         int d_v, float scale, void* out, int block_size, int max_blocks,
+                         int num_blocks, int dtype, void* workspace, long long workspace_bytes,
+                         void* stream) {
+  if (int e = paged_args_check(block_table, g, block_size, max_blocks, num_blocks)) return e;
+  const ChunkCall x = {q, k_pool, v_pool, cu_tokens, seq_lens, block_table, b, total, h, g, d_k,
+                       d_v, scale, out, max_blocks * block_size, block_size, max_blocks,
+                       num_blocks, dtype, workspace, workspace_bytes};
+  return chunk_run(x, stream);
+}
+
+int gqa_chunk_attn_workspace(int total, int h, int g, int d_k, int d_v, int num_sms,
+                             long long* bytes) {
+  if (!bytes) return GQA_ERR_NULL;
+  if (num_sms < 0) return GQA_ERR_SHAPE;
+  if (int e = chunk_shape_check(total, h, g, d_k, d_v)) return e;
+  if (num_sms == 0) {
+    unsigned int* status = nullptr;
+    if (int e = device_query(&num_sms, &status)) return e;
+  }
+  *bytes = static_cast<long long>(chunk_plan(total, h, g, d_v, num_sms).bytes);
+  return GQA_OK;
+}
+
+}  // extern "C"

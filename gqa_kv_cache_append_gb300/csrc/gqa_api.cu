@@ -25,7 +25,7 @@ __device__ unsigned int g_status_word;
 
 namespace {
 
-constexpr long long kWaitBudget = 1ll << 31;  // ~1 s of SM cycles per wait
+constexpr long long kWaitBudget = kKernelWaitBudget;  // per wait
 
 // ---------------------------------------------------------------------------
 // KV append: one thread per 16-byte chunk of the new rows.
@@ -487,6 +487,19 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_
              const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int device_query(int* num_sms, unsigned int** status) {
+  DeviceInfo* di = nullptr;
+  if (int e = device_info(&di)) return e;
+  *num_sms = di->num_sms;
+  *status = di->status;
+  return GQA_OK;
+}
+
+int paged_args_check(const int32_t* block_table, int g, int block_size, int max_blocks,
+                     int num_blocks) {
+  return paged_check(block_table, g, block_size, max_blocks, num_blocks);
 }
 
 }  // namespace gqa

@@ -94,4 +94,13 @@ long long proj_work(int mode, int D, int h, int g);   // K chunks of the launch
 int proj_tiles(int mode, int D, int h, int g);
 cudaError_t launch_proj(const ProjLaunch& a);
 
+// The current device for a launch: its SM count and status word (checked and
+// looked up once); GQA_OK or the code to return.
+int device_query(int* num_sms, unsigned int** status);
+// Host checks of a paged cache's arguments (no CUDA call).
+int paged_args_check(const int32_t* block_table, int g, int block_size, int max_blocks,
+                     int num_blocks);
+// Wait limit of the kernels, in SM cycles.
+constexpr long long kKernelWaitBudget = 1ll << 31;  // ~1 s
+
 }  // namespace gqa

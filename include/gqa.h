@@ -88,6 +88,18 @@ extern "C" {
                                    and did nothing (not expected to happen) */
 #define GQA_DEV_BAD_BLOCK    8u /* paged cache: a block-table entry in use was
                                    outside [0, num_blocks) */
+#define GQA_DEV_BAD_TOKENS   16u /* packed tokens: some cu_tokens[i] was outside
+                                   [0, total] or above cu_tokens[i + 1] */
+
+/* gqa_rope_append: which elements of a head form the pairs that turn */
+#define GQA_ROPE_HALF  0  /* (m, m + rot / 2) */
+#define GQA_ROPE_PAIRS 1  /* (2 m, 2 m + 1) */
+
+/* gqa_rope_table: how the angles are scaled for long contexts */
+#define GQA_ROPE_PLAIN      0
+#define GQA_ROPE_LINEAR     1
+#define GQA_ROPE_WAVELENGTH 2
+#define GQA_ROPE_YARN       3
 
 /*
  * gqa_kv_append - write the new token's K and V rows into the caches.
@@ -415,6 +427,158 @@ int gqa_decode_attn_noalloc(const void* q, const void* k_cache, const void* v_ca
 int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int dtype,
                     int flags, int num_sms, int* kernels, int* ctas, int* tile,
                     int* tensor_core, long long* workspace_bytes, int* cluster);
+
+/*
+ * Packed tokens.  The calls below take the new tokens of b sequences packed
+ * on one axis, each sequence with its own number n_i of them (a single token,
+ * a chunk, a whole prompt):
+ *   cu_tokens [b + 1] int32 (device): sequence i's new tokens are rows
+ *             cu_tokens[i] .. cu_tokens[i + 1] - 1 of every packed tensor
+ *   seq_lens  [b] int32 (device): L_i AFTER the n_i tokens are appended;
+ *             token s of sequence i sits at position L_i - n_i + s
+ *   total     rows of the packed tensors.  Rows at or behind cu_tokens[b] (a
+ *             batch padded to a fixed size) are neither used nor written.
+ * n_i = 0 is allowed (the sequence takes no part, whatever its L_i).  A
+ * sequence with n_i > 0 and L_i outside [n_i, cap] is skipped and sets
+ * GQA_DEV_BAD_SEQ_LEN; one whose cu_tokens entries are outside [0, total] or
+ * decrease is skipped and sets GQA_DEV_BAD_TOKENS (rows that the entries give
+ * to two sequences are unspecified; no access leaves the tensors).  Paged caches, block
+ * tables and block sizes are those of the paged calls above.  These calls
+ * keep nothing between them: scratch memory is passed in.
+ *
+ * gqa_rope_table - host only: the position table of gqa_rope_append.
+ *
+ * Pair m < rot / 2 turns by f_m radians per position, f_m = theta^(-2 m / rot)
+ * for GQA_ROPE_PLAIN; phase_out [rot / 2] (HOST memory) receives f_m as a
+ * fraction of a turn in units of 2^-64 and rope_scale_out the factor on sine
+ * and cosine (1 but for GQA_ROPE_YARN).  The caller copies the table to the
+ * device once.  Scalings for long contexts (factor > 0):
+ *   GQA_ROPE_LINEAR      f_m / factor
+ *   GQA_ROPE_WAVELENGTH  with x = clamp((original_len f_m / 2 pi - low) /
+ *                        (high - low), 0, 1): (1 - x) f_m / factor + x f_m
+ *   GQA_ROPE_YARN        with at(t) = rot log(original_len / (2 pi t)) /
+ *                        (2 log theta), the pair that turns t times over the
+ *                        original length, first = max(floor(at(high)), 0),
+ *                        last = min(ceil(at(low)), rot - 1) and x =
+ *                        clamp((m - first) / (last - first), 0, 1):
+ *                        (1 - x) f_m + x f_m / factor; rope_scale =
+ *                        0.1 log(factor) + 1 for factor > 1
+ * (0 < low < high, original_len > 0 for the last two.)
+ *
+ * gqa_rope_append - per-head norm, rotary positions and append in one launch.
+ *
+ * For token row t of sequence i at position P, every query head a and KV head
+ * j:   q_out[t, a, :] = rot(norm(q[t, a, :], q_weight), P)
+ *      k_cache[i, j, P, :] = rot(norm(k_new[t, j, :], k_weight), P)
+ *      v_cache[i, j, P, :] = v_new[t, j, :]                  (bit for bit)
+ *   norm(x, w) = x / sqrt(mean(x^2) + eps) * w, left out when q_weight and
+ *   k_weight are NULL; rot turns the pairs of the first `rot` elements (layout
+ *   GQA_ROPE_HALF or GQA_ROPE_PAIRS) by the table's angles times P, exact for
+ *   every position, and multiplies them by rope_scale; left out when phase is
+ *   NULL (then rot and layout are not looked at).  fp32 throughout, rounded
+ *   once when stored.
+ *   q [total, h, d_k], k_new [total, g, d_k], v_new [total, g, d_v] (read;
+ *     heads contiguous, consecutive tokens q_stride / k_stride / v_stride
+ *     elements apart, so the three may be slices of one projection's output)
+ *   q_weight, k_weight [d_k] (read, both or neither)
+ *   phase [rot / 2] uint64 (device, read)
+ *   q_out [total, h, d_k] (written; may be q itself when q_stride = h * d_k).
+ *     q and q_out both NULL: only the cache is written.
+ *   k_cache [b, g, cap, d_k], v_cache [b, g, cap, d_v] (rows P written)
+ * Supported: GQA_F32, GQA_BF16, GQA_F16; d_k, d_v multiples of 8 up to 256;
+ * rot a multiple of 16 up to d_k; strides that are multiples of 16 bytes.
+ *
+ * gqa_rope_append_paged     - the same into a paged cache.
+ * gqa_rope_append_fp8_paged - into a paged cache of 8-bit rows: k_pool
+ *   [num_blocks, g, block_size, d_k] and v_pool [.., d_v] hold e4m3 values,
+ *   k_scale and v_scale [num_blocks, g, block_size] fp32 one scale per row.
+ *   A row x (in fp32, after norm and rotation) is stored as scale =
+ *   max|x| / 448 and round-to-nearest e4m3(x / scale); a row of zeros has
+ *   scale 0.  d_k and d_v multiples of 16.  Rows that hold infinities or
+ *   NaN are stored as rows that hold NaN.
+ *
+ * gqa_kv_read_fp8_paged - rows [0, L_i) of every sequence of an 8-bit paged
+ *   cache, as scale * value rounded to dtype, into contiguous caches
+ *   k_cache [b, g, cap, d_k] and v_cache [b, g, cap, d_v]; other rows are not
+ *   written.  L_i outside [0, min(cap, max_blocks * block_size)] sets
+ *   GQA_DEV_BAD_SEQ_LEN and the sequence is skipped.
+ */
+int gqa_rope_table(int rot, double theta, int scaling, double factor, double original_len,
+                   double low, double high, uint64_t* phase_out, float* rope_scale_out);
+
+int gqa_rope_append(const void* q, const void* k_new, const void* v_new, long long q_stride,
+                    long long k_stride, long long v_stride, const int32_t* cu_tokens,
+                    const int32_t* seq_lens, const void* q_weight, const void* k_weight,
+                    float eps, const uint64_t* phase, int rot, int layout, float rope_scale,
+                    void* q_out, void* k_cache, void* v_cache, int b, int total, int h, int g,
+                    int d_k, int d_v, int cap, int dtype, void* stream);
+
+int gqa_rope_append_paged(const void* q, const void* k_new, const void* v_new,
+                          long long q_stride, long long k_stride, long long v_stride,
+                          const int32_t* cu_tokens, const int32_t* seq_lens,
+                          const void* q_weight, const void* k_weight, float eps,
+                          const uint64_t* phase, int rot, int layout, float rope_scale,
+                          void* q_out, void* k_pool, void* v_pool, const int32_t* block_table,
+                          int b, int total, int h, int g, int d_k, int d_v, int block_size,
+                          int max_blocks, int num_blocks, int dtype, void* stream);
+
+int gqa_rope_append_fp8_paged(const void* q, const void* k_new, const void* v_new,
+                              long long q_stride, long long k_stride, long long v_stride,
+                              const int32_t* cu_tokens, const int32_t* seq_lens,
+                              const void* q_weight, const void* k_weight, float eps,
+                              const uint64_t* phase, int rot, int layout, float rope_scale,
+                              void* q_out, void* k_pool, void* v_pool, float* k_scale,
+                              float* v_scale, const int32_t* block_table, int b, int total,
+                              int h, int g, int d_k, int d_v, int block_size, int max_blocks,
+                              int num_blocks, int dtype, void* stream);
+
+int gqa_kv_read_fp8_paged(const void* k_pool, const void* v_pool, const float* k_scale,
+                          const float* v_scale, const int32_t* block_table,
+                          const int32_t* seq_lens, void* k_cache, void* v_cache, int b, int g,
+                          int d_k, int d_v, int block_size, int max_blocks, int num_blocks,
+                          int cap, int dtype, void* stream);
+
+/*
+ * gqa_chunk_attn - causal attention of packed chunks of new tokens over the
+ * cache, which already holds their rows (append first).  For token row t of
+ * sequence i at position P and query head a, j = a / (h / g):
+ *     out[t, a, :] = sum_{p <= P} softmax_p(scale * q[t, a, :] . k_cache[i, j, p, :])
+ *                    v_cache[i, j, p, :]
+ * A whole prompt is a chunk with n_i = L_i, a decode step one with n_i = 1;
+ * sequences of a call mix freely.  There is no limit on n_i.
+ *   q [total, h, d_k] (read), out [total, h, d_v] (written)
+ *   k_cache [b, g, cap, d_k], v_cache [b, g, cap, d_v] (read)
+ *   workspace: device memory, 256-byte aligned, of at least the bytes that
+ *   gqa_chunk_attn_workspace gives; what it holds before and after the call
+ *   does not matter.  Calls that overlap on the GPU need one each (so do
+ *   captured graphs that are replayed side by side).
+ * Rows p >= L_i of the caches are never used, whatever they hold; rows p < L_i
+ * hold finite values (a later token's infinity or NaN may reach an earlier
+ * token of the same chunk).  Every element is accumulated in fp32, in an order
+ * that depends on the lengths alone: the same call gives the same bits.
+ * Supported: GQA_BF16 and GQA_F16, d_k and d_v in {64, 128} (they may
+ * differ), h / g <= 128, b <= 65535.  GQA_ERR_SCRATCH_LIMIT: the workspace is
+ * too small.
+ *
+ * gqa_chunk_attn_paged - the same over a paged cache.
+ *
+ * gqa_chunk_attn_workspace - host only (no device access when num_sms > 0; 0:
+ * the current device's): the workspace of a call of up to `total` packed rows.
+ */
+int gqa_chunk_attn(const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* cu_tokens, const int32_t* seq_lens, int b, int total, int h,
+                   int g, int d_k, int d_v, float scale, void* out, int cap, int dtype,
+                   void* workspace, long long workspace_bytes, void* stream);
+
+int gqa_chunk_attn_paged(const void* q, const void* k_pool, const void* v_pool,
+                         const int32_t* block_table, const int32_t* cu_tokens,
+                         const int32_t* seq_lens, int b, int total, int h, int g, int d_k,
+                         int d_v, float scale, void* out, int block_size, int max_blocks,
+                         int num_blocks, int dtype, void* workspace, long long workspace_bytes,
+                         void* stream);
+
+int gqa_chunk_attn_workspace(int total, int h, int g, int d_k, int d_v, int num_sms,
+                             long long* bytes);
 
 /* Name of a return code, for messages. */
 const char* gqa_status_string(int status);
