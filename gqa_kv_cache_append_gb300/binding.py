@@ -432,41 +432,82 @@ def gqa_decode_plan(b, n, h, g, d_k, d_v, cap, dtype, num_sms=0, flags=0) -> dic
 # ---------------------------------------------------------------------------
 # packed tokens, 8-bit cache
 # ---------------------------------------------------------------------------
-def _tensor(x, name, nbytes, types=None) -> int:
-    """_ptr for the calls on packed tokens: also refuses a tensor of another
-    device than the current one (whose stream the call runs on) and one of
-    another type."""
+def _tensor(x, name, n, types, dev) -> int:
+    """Device address of a tensor argument of at least n elements of one of
+    `types` on device `dev` (the current one, whose stream the call runs on);
+    like _ptr otherwise (raw integers pass through unchecked).  The common
+    case takes few calls into torch: at single tokens they are most of a
+    call's time."""
     if isinstance(x, torch.Tensor):
-        if types is not None and x.dtype not in types:
-            raise ValueError(f"{name}: must be {' or '.join(map(str, types))}, got {x.dtype}")
-        if x.is_cuda and x.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: on {x.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-    return _ptr(x, name, nbytes)
+        if (x.dtype in types and x.get_device() == dev and x.is_contiguous()
+                and x.numel() >= n):
+            return x.data_ptr()
+        if x.dtype not in types:
+            raise ValueError(f"{name}: must be {_names(types)}, got {x.dtype}")
+        if x.is_cuda and x.get_device() != dev:
+            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{dev}")
+        return _ptr(x, name, n * x.element_size())
+    return int(x) if x is not None else 0
 
 
-def _tokens(x, name, total, heads, d, types):
+def _tokens(x, name, total, heads, d, types, dev):
     """Pointer and token stride (elements) of a packed tensor [total, heads, d]
     whose heads are contiguous; consecutive tokens may lie further apart."""
     if not isinstance(x, torch.Tensor):
         return _ptr(x, name), heads * d
-    if tuple(x.shape) != (total, heads, d):
+    if x.shape != (total, heads, d):
         raise ValueError(f"{name}: must be [{total}, {heads}, {d}], got {list(x.shape)}")
-    st = x.stride()
-    if total > 0 and (st[2] != 1 and d > 1 or st[1] != d and heads > 1):
+    s0, s1, s2 = x.stride()
+    if total > 0 and (s2 != 1 and d > 1 or s1 != d and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if x.is_cuda and x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {x.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
     if x.dtype not in types:
-        raise ValueError(f"{name}: must be {types[0]}, got {x.dtype}")
-    p = x.data_ptr() if x.is_cuda else _HostTensor(name, x.device)
-    return p, st[0] if total > 1 else heads * d
+        raise ValueError(f"{name}: must be {_names(types)}, got {x.dtype}")
+    at = x.get_device()
+    if at != dev:
+        if x.is_cuda:
+            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{dev}")
+        return _HostTensor(name, x.device), heads * d
+    return x.data_ptr(), s0 if total > 1 else heads * d
+
+
+def _names(types) -> str:
+    return " or ".join(map(str, types or (torch.float32, torch.bfloat16, torch.float16)))
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(x, stream):
+    """(current device, stream handle) of a call whose first tensor is x; no
+    device (-2, which no tensor is on) when that is not a CUDA tensor."""
+    if isinstance(x, torch.Tensor) and not x.is_cuda:
+        return -2, 0
+    dev = torch.cuda.current_device() if isinstance(x, torch.Tensor) else -2
+    if stream is None and dev >= 0 and _raw_stream is not None:
+        return dev, _raw_stream(dev)
+    return dev, _stream(stream)
+
+
+def _launch(fn_name, fn, *args) -> None:
+    """_call without a look at every argument: a host tensor's stand-in is no
+    pointer, so its conversion fails before the library is entered."""
+    try:
+        code = fn(*args)
+    except ctypes.ArgumentError:
+        for a in args:
+            if isinstance(a, _HostTensor):
+                raise ValueError(
+                    f"{a.name}: a CUDA tensor is required, got one on {a.device}") from None
+        raise
+    if code != GQA_OK:
+        raise GqaError(fn_name, code)
 
 
 _TORCH = {GQA_F32: (torch.float32,), GQA_BF16: (torch.bfloat16,), GQA_F16: (torch.float16,)}
 _I32 = (torch.int32,)
+_I64 = (torch.int64,)
 _F32 = (torch.float32,)
+_U8 = (torch.uint8,)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -490,27 +531,26 @@ def gqa_rope_table(rot, theta=10000.0, scaling="none", factor=1.0, original_len=
 
 
 def _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v, rope, rope_scale,
-               layout, q_weight, k_weight, eps, total, dtype):
+               layout, q_weight, k_weight, eps, total, dtype, dev):
     """(dtype code, total, the arguments from q to rope_scale, q_out)."""
     dt = _dtype(k_new, dtype)
     ty = _TORCH.get(dt, ())
     if total is None:
         total = k_new.shape[0]
-    e = _elt(dt)
-    qp, qs = (0, 0) if q is None else _tokens(q, "q", total, h, d_k, ty)
-    kp, ks = _tokens(k_new, "k_new", total, g, d_k, ty)
-    vp, vs = _tokens(v_new, "v_new", total, g, d_v, ty)
+    qp, qs = (0, 0) if q is None else _tokens(q, "q", total, h, d_k, ty, dev)
+    kp, ks = _tokens(k_new, "k_new", total, g, d_k, ty, dev)
+    vp, vs = _tokens(v_new, "v_new", total, g, d_v, ty, dev)
     rot = 0
     if isinstance(rope, torch.Tensor):
         rot = 2 * rope.numel()
     elif rope is not None:
         raise ValueError("rope: must be the tensor of gqa_rope_table")
     return dt, total, (
-        qp, kp, vp, qs, ks, vs, _tensor(cu_tokens, "cu_tokens", _n(b + 1) * 4, _I32),
-        _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32),
-        _tensor(q_weight, "q_weight", d_k * e, ty), _tensor(k_weight, "k_weight", d_k * e, ty),
-        float(eps), _tensor(rope, "rope", 0, (torch.int64,)), rot, int(layout),
-        float(rope_scale), _tensor(q_out, "q_out", _n(total, h, d_k) * e, ty))
+        qp, kp, vp, qs, ks, vs, _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
+        _tensor(seq_lens, "seq_lens", b, _I32, dev),
+        _tensor(q_weight, "q_weight", d_k, ty, dev), _tensor(k_weight, "k_weight", d_k, ty, dev),
+        float(eps), _tensor(rope, "rope", 0, _I64, dev), rot, int(layout),
+        float(rope_scale), _tensor(q_out, "q_out", total * h * d_k, ty, dev))
 
 
 def gqa_rope_append(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_cache, v_cache, b, h, g, d_k,
@@ -521,24 +561,26 @@ def gqa_rope_append(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_cache, v_cach
     rope_scale of gqa_rope_table) and append of packed tokens, in one launch.
     q, k_new, v_new [total, heads, d] may be slices of one projection's
     output (heads contiguous, tokens further apart); q_out may be q."""
+    dev, st = _here(k_new, stream)
     dt, total, args = _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v,
-                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype)
+                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype,
+                                 dev)
     if cap is None:
         cap = k_cache.shape[2]
-    e, ty = _elt(dt), _TORCH.get(dt)
-    _call("gqa_rope_append", lib.gqa_rope_append, *args,
-          _tensor(k_cache, "k_cache", _n(b, g, cap, d_k) * e, ty),
-          _tensor(v_cache, "v_cache", _n(b, g, cap, d_v) * e, ty),
-          int(b), int(total), int(h), int(g), int(d_k), int(d_v), int(cap), dt, _stream(stream))
+    ty = _TORCH.get(dt, ())
+    _launch("gqa_rope_append", lib.gqa_rope_append, *args,
+          _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
+          _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev),
+          int(b), int(total), int(h), int(g), int(d_k), int(d_v), int(cap), dt, st)
 
 
-def _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, e, ty):
+def _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, ty, dev):
     """_paged_ptrs with the checks of _tensor."""
     nb, _, bs, _ = k_pool.shape
     mb = block_table.shape[1]
-    return (_tensor(k_pool, "k_pool", _n(nb, g, bs, d_k) * e, ty),
-            _tensor(v_pool, "v_pool", _n(nb, g, bs, d_v) * e, ty),
-            _tensor(block_table, "block_table", _n(b, mb) * 4, _I32), int(bs), int(mb), int(nb))
+    return (_tensor(k_pool, "k_pool", nb * g * bs * d_k, ty, dev),
+            _tensor(v_pool, "v_pool", nb * g * bs * d_v, ty, dev),
+            _tensor(block_table, "block_table", b * mb, _I32, dev), int(bs), int(mb), int(nb))
 
 
 def gqa_rope_append_paged(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_pool, v_pool,
@@ -547,20 +589,23 @@ def gqa_rope_append_paged(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_pool, v
                           total=None, dtype=None, stream=None) -> None:
     """gqa_rope_append into a paged cache (pools [num_blocks, g, block_size,
     d], block_table [b, max_blocks])."""
+    dev, st = _here(k_new, stream)
     dt, total, args = _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v,
-                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype)
-    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, _elt(dt),
-                                    _TORCH.get(dt))
-    _call("gqa_rope_append_paged", lib.gqa_rope_append_paged, *args, kp, vp, tp, int(b),
-          int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, _stream(stream))
+                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype,
+                                 dev)
+    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v,
+                                    _TORCH.get(dt, ()), dev)
+    _launch("gqa_rope_append_paged", lib.gqa_rope_append_paged, *args, kp, vp, tp, int(b),
+          int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, st)
 
 
-def _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g, d_k, d_v):
+def _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g, d_k, d_v, dev):
     """_pools of an 8-bit cache, with the pointers of its scales [num_blocks,
     g, block_size]."""
-    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, 1, _E4M3)
-    n = _n(nb, g, bs) * 4
-    return (kp, vp, _tensor(k_scale, "k_scale", n, _F32), _tensor(v_scale, "v_scale", n, _F32),
+    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, _E4M3, dev)
+    n = nb * g * bs
+    return (kp, vp, _tensor(k_scale, "k_scale", n, _F32, dev),
+            _tensor(v_scale, "v_scale", n, _F32, dev),
             tp, bs, mb, nb)
 
 
@@ -571,30 +616,32 @@ def gqa_rope_append_fp8_paged(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_poo
     """gqa_rope_append into an 8-bit paged cache: e4m3 pools (torch.float8_e4m3fn
     or uint8) and one fp32 scale per row.  q = q_out = None with rope = None
     is the plain quantising append."""
+    dev, st = _here(k_new, stream)
     dt, total, args = _rope_args(q, k_new, v_new, cu_tokens, seq_lens, q_out, b, h, g, d_k, d_v,
-                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype)
+                                 rope, rope_scale, layout, q_weight, k_weight, eps, total, dtype,
+                                 dev)
     kp, vp, ks, vs, tp, bs, mb, nb = _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g,
-                                             d_k, d_v)
-    _call("gqa_rope_append_fp8_paged", lib.gqa_rope_append_fp8_paged, *args, kp, vp, ks, vs, tp,
-          int(b), int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt,
-          _stream(stream))
+                                             d_k, d_v, dev)
+    _launch("gqa_rope_append_fp8_paged", lib.gqa_rope_append_fp8_paged, *args, kp, vp, ks, vs, tp,
+          int(b), int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, st)
 
 
 def gqa_kv_read_fp8_paged(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_cache,
                           v_cache, b, g, d_k, d_v, cap=None, dtype=None, stream=None) -> None:
     """Rows [0, seq_lens[i]) of an 8-bit paged cache as contiguous caches
     [b, g, cap, d] of the caches' type."""
+    dev, st = _here(k_cache, stream)
     dt = _dtype(k_cache, dtype)
-    e, ty = _elt(dt), _TORCH.get(dt)
+    ty = _TORCH.get(dt, ())
     if cap is None:
         cap = k_cache.shape[2]
     kp, vp, ks, vs, tp, bs, mb, nb = _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g,
-                                             d_k, d_v)
-    _call("gqa_kv_read_fp8_paged", lib.gqa_kv_read_fp8_paged, kp, vp, ks, vs, tp,
-          _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32),
-          _tensor(k_cache, "k_cache", _n(b, g, cap, d_k) * e, ty),
-          _tensor(v_cache, "v_cache", _n(b, g, cap, d_v) * e, ty), int(b), int(g), int(d_k),
-          int(d_v), bs, mb, nb, int(cap), dt, _stream(stream))
+                                             d_k, d_v, dev)
+    _launch("gqa_kv_read_fp8_paged", lib.gqa_kv_read_fp8_paged, kp, vp, ks, vs, tp,
+          _tensor(seq_lens, "seq_lens", b, _I32, dev),
+          _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
+          _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev), int(b), int(g), int(d_k),
+          int(d_v), bs, mb, nb, int(cap), dt, st)
 
 
 def gqa_chunk_attn_workspace(total, h, g, d_k, d_v, num_sms=0) -> int:
@@ -606,7 +653,7 @@ def gqa_chunk_attn_workspace(total, h, g, d_k, d_v, num_sms=0) -> int:
     return int(n.value)
 
 
-def _workspace(ws, stream, like, size, *shape):
+def _workspace(ws, stream, dev, like, size, *shape):
     """The workspace argument (tensor, bytes): the caller's, or a tensor made
     for this call on its stream (the allocator orders its next use behind
     the call)."""
@@ -620,7 +667,7 @@ def _workspace(ws, stream, like, size, *shape):
             with torch.cuda.stream(s):
                 ws = torch.empty(n, dtype=torch.uint8, device=like.device)
     if isinstance(ws, torch.Tensor):
-        return _tensor(ws, "workspace", 0), ws.numel() * ws.element_size(), ws
+        return _tensor(ws, "workspace", 0, _U8, dev), ws.numel() * ws.element_size(), ws
     if ws is None:
         return 0, 0, None
     raise ValueError("workspace: must be a tensor")
@@ -632,40 +679,42 @@ def gqa_chunk_attn(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, 
     [total, h, d_v]) over caches that already hold their rows.  workspace:
     a uint8 tensor of gqa_chunk_attn_workspace bytes to reuse between calls
     (by default one is made per call)."""
+    dev, st = _here(q, stream)
     dt = _dtype(q, dtype)
-    e, ty = _elt(dt), _TORCH.get(dt)
+    ty = _TORCH.get(dt, ())
     if total is None:
         total = q.shape[0]
     if cap is None:
         cap = k_cache.shape[2]
-    wp, wn, _keep = _workspace(workspace, stream, q, gqa_chunk_attn_workspace, total, h, g, d_k,
+    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g, d_k,
                                d_v)
-    _call("gqa_chunk_attn", lib.gqa_chunk_attn, _tensor(q, "q", _n(total, h, d_k) * e, ty),
-          _tensor(k_cache, "k_cache", _n(b, g, cap, d_k) * e, ty),
-          _tensor(v_cache, "v_cache", _n(b, g, cap, d_v) * e, ty),
-          _tensor(cu_tokens, "cu_tokens", _n(b + 1) * 4, _I32),
-          _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32), int(b), int(total), int(h), int(g),
-          int(d_k), int(d_v), float(scale), _tensor(out, "out", _n(total, h, d_v) * e, ty),
-          int(cap), dt, wp, wn, _stream(stream))
+    _launch("gqa_chunk_attn", lib.gqa_chunk_attn, _tensor(q, "q", total * h * d_k, ty, dev),
+          _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
+          _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev),
+          _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
+          _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
+          int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev),
+          int(cap), dt, wp, wn, st)
 
 
 def gqa_chunk_attn_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k, d_v,
                          scale, out, total=None, dtype=None, workspace=None,
                          stream=None) -> None:
     """gqa_chunk_attn over a paged cache."""
+    dev, st = _here(q, stream)
     dt = _dtype(q, dtype)
-    e, ty = _elt(dt), _TORCH.get(dt)
+    ty = _TORCH.get(dt, ())
     if total is None:
         total = q.shape[0]
-    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, e, ty)
-    wp, wn, _keep = _workspace(workspace, stream, q, gqa_chunk_attn_workspace, total, h, g, d_k,
+    kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, ty, dev)
+    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g, d_k,
                                d_v)
-    _call("gqa_chunk_attn_paged", lib.gqa_chunk_attn_paged,
-          _tensor(q, "q", _n(total, h, d_k) * e, ty), kp, vp, tp,
-          _tensor(cu_tokens, "cu_tokens", _n(b + 1) * 4, _I32),
-          _tensor(seq_lens, "seq_lens", _n(b) * 4, _I32), int(b), int(total), int(h), int(g),
-          int(d_k), int(d_v), float(scale), _tensor(out, "out", _n(total, h, d_v) * e, ty), bs,
-          mb, nb, dt, wp, wn, _stream(stream))
+    _launch("gqa_chunk_attn_paged", lib.gqa_chunk_attn_paged,
+          _tensor(q, "q", total * h * d_k, ty, dev), kp, vp, tp,
+          _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
+          _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
+          int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev), bs,
+          mb, nb, dt, wp, wn, st)
 
 
 def gqa_device_status(stream=None) -> int:
