@@ -11,6 +11,7 @@ _BINDING = {
     "gqa_project_qkv", "gqa_project_out", "gqa_decode_layer", "gqa_decode_plan",
     "gqa_rope_table", "gqa_rope_append", "gqa_rope_append_paged", "gqa_rope_append_fp8_paged",
     "gqa_kv_read_fp8_paged", "gqa_chunk_attn", "gqa_chunk_attn_paged", "gqa_chunk_attn_workspace",
+    "gqa_decode_attn_fp8_paged", "gqa_decode_attn_fp8_workspace",
     "gqa_device_status", "gqa_selftest_wait_timeout", "gqa_version", "decode_step", "GqaError",
     "status_string",
 }

@@ -85,6 +85,9 @@ SIGNATURES = {
     "gqa_chunk_attn": (_I, [_VP] * 5 + [_I] * 6 + [_F, _VP, _I, _I, _VP, _LL, _VP]),
     "gqa_chunk_attn_paged": (_I, [_VP] * 6 + [_I] * 6 + [_F, _VP] + [_I] * 4 + [_VP, _LL, _VP]),
     "gqa_chunk_attn_workspace": (_I, [_I] * 6 + [ctypes.POINTER(_LL)]),
+    "gqa_decode_attn_fp8_paged": (_I, [_VP] * 7 + [_I] * 6 + [_F, _VP] + [_I] * 4 +
+                                  [_VP, _LL, _VP]),
+    "gqa_decode_attn_fp8_workspace": (_I, [_I] * 6 + [_LL, _I, ctypes.POINTER(_LL)]),
     "gqa_device_status": (_I, [_VP, ctypes.POINTER(ctypes.c_uint32)]),
     "gqa_selftest_wait_timeout": (_I, [_LL, _VP]),
     "gqa_status_string": (ctypes.c_char_p, [_I]),
@@ -715,6 +718,37 @@ def gqa_chunk_attn_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b,
           _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
           int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev), bs,
           mb, nb, dt, wp, wn, st)
+
+
+def gqa_decode_attn_fp8_workspace(b, n, h, g, d_k, d_v, cap, num_sms=0) -> int:
+    """Bytes of workspace of gqa_decode_attn_fp8_paged, cap = max_blocks *
+    block_size (host only when num_sms > 0)."""
+    out = ctypes.c_longlong(0)
+    _check("gqa_decode_attn_fp8_workspace", lib.gqa_decode_attn_fp8_workspace(
+        int(b), int(n), int(h), int(g), int(d_k), int(d_v), int(cap), int(num_sms),
+        ctypes.byref(out)))
+    return int(out.value)
+
+
+def gqa_decode_attn_fp8_paged(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, b, h,
+                              g, d_k, d_v, scale, out, n=1, dtype=None, workspace=None,
+                              stream=None) -> None:
+    """gqa_decode_attn_paged over an 8-bit paged cache (e4m3 pools, one fp32
+    scale per row).  workspace: a uint8 tensor of
+    gqa_decode_attn_fp8_workspace bytes to reuse between calls (by default
+    one is made per call)."""
+    dev, st = _here(q, stream)
+    dt = _dtype(q, dtype)
+    ty = _TORCH.get(dt, ())
+    kp, vp, ks, vs, tp, bs, mb, nb = _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g,
+                                             d_k, d_v, dev)
+    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_decode_attn_fp8_workspace, b, n, h,
+                               g, d_k, d_v, bs * mb)
+    _launch("gqa_decode_attn_fp8_paged", lib.gqa_decode_attn_fp8_paged,
+            _tensor(q, "q", b * n * h * d_k, ty, dev), kp, vp, ks, vs, tp,
+            _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(n), int(h), int(g),
+            int(d_k), int(d_v), float(scale), _tensor(out, "out", b * n * h * d_v, ty, dev), bs,
+            mb, nb, dt, wp, wn, st)
 
 
 def gqa_device_status(stream=None) -> int:

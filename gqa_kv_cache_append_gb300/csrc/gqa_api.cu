@@ -400,6 +400,28 @@ cudaError_t launch_combine(cudaLaunchConfig_t& cfg, const DecodeLaunch& a, int t
   }
 }
 
+}  // namespace
+
+cudaError_t launch_unit_combine(const DecodeLaunch& a, int tile) {
+  const long long rows = static_cast<long long>(a.b) * a.h * a.nq;  // (unit, query row) pairs
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const float* po = static_cast<const float*>(a.part_o);
+  const float* pml = static_cast<const float*>(a.part_ml);
+  if (a.dtype == GQA_BF16) return launch_combine<__nv_bfloat16>(cfg, a, tile, po, pml);
+  if (a.dtype == GQA_F16) return launch_combine<__half>(cfg, a, tile, po, pml);
+  return launch_combine<float>(cfg, a, tile, po, pml);
+}
+
+namespace {
+
 int launch_all(DecodeLaunch& a, int tile) {
   // (a cluster launch merges its split units itself)
   const bool separate = a.cluster <= 1 && use_combine_kernel(a.nc, a.b, a.g);
@@ -408,26 +430,7 @@ int launch_all(DecodeLaunch& a, int tile) {
                                                 a.block_table != nullptr);
   cudaError_t e = tc ? launch_decode_tc(a) : launch_decode_simt(a);
   if (e != cudaSuccess) return GQA_ERR_CUDA;
-  if (separate) {
-    const long long rows = static_cast<long long>(a.b) * a.h * a.nq;  // (unit, query row) pairs
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows));
-    cfg.blockDim = dim3(32 * kCombineWarps);
-    cfg.stream = a.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const float* po = static_cast<const float*>(a.part_o);
-    const float* pml = static_cast<const float*>(a.part_ml);
-    if (a.dtype == GQA_BF16)
-      e = launch_combine<__nv_bfloat16>(cfg, a, tile, po, pml);
-    else if (a.dtype == GQA_F16)
-      e = launch_combine<__half>(cfg, a, tile, po, pml);
-    else
-      e = launch_combine<float>(cfg, a, tile, po, pml);
-  }
+  if (separate) e = launch_unit_combine(a, tile);
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
@@ -500,6 +503,17 @@ int device_query(int* num_sms, unsigned int** status) {
 int paged_args_check(const int32_t* block_table, int g, int block_size, int max_blocks,
                      int num_blocks) {
   return paged_check(block_table, g, block_size, max_blocks, num_blocks);
+}
+
+bool encode_u8_map(CUtensorMap* map, const void* base, int d, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || (d != 64 && d != 128)) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), rows}, st[1] = {static_cast<cuuint64_t>(d)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(d), box_rows}, es[2] = {1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, st, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace gqa

@@ -50,6 +50,10 @@ struct DecodeLaunch {
 bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides, const uint32_t* box, bool bf16 = true);
 
+// The same over rows of d (64 or 128) bytes, the whole row in a box: 64- or
+// 128-byte swizzle.
+bool encode_u8_map(CUtensorMap* map, const void* base, int d, uint64_t rows, uint32_t box_rows);
+
 // CUDA-core kernel (fp32 and bf16, d_k and d_v in {64, 128}); `cols` = nq * r
 // query rows per KV head
 bool simt_supported(int dtype, int d_k, int d_v, int cols);
@@ -67,6 +71,10 @@ int tc_tile(int d_k, int d_v);  // positions per tile (256 for d_k = d_v = 64, e
 int tc_max_clusters(int csize);
 int tc_ctas_per_sm(int r);
 cudaError_t launch_decode_tc(const DecodeLaunch& a);
+
+// Joins the partials of the units cut between a launch's CTAs (every unit
+// whose tiles the Walker gives to more than one of a.nc CTAs).
+cudaError_t launch_unit_combine(const DecodeLaunch& a, int tile);
 
 // tcgen05 projection GEMMs around the step (bf16, 128-wide heads):
 // mode 0: q / k_new / v_new = x . P_q / P_k / P_v; mode 1: y = o . P_o

@@ -580,6 +580,36 @@ int gqa_chunk_attn_paged(const void* q, const void* k_pool, const void* v_pool,
 int gqa_chunk_attn_workspace(int total, int h, int g, int d_k, int d_v, int num_sms,
                              long long* bytes);
 
+/*
+ * gqa_decode_attn_fp8_paged - gqa_decode_attn_paged over an 8-bit paged cache
+ * (the pools and scales of gqa_rope_append_fp8_paged): n new tokens per
+ * sequence, causal, over rows scale * value of the cache, which already holds
+ * the new rows (append first).
+ *   q [b, n, h, d_k] (read), out [b, n, h, d_v] (written)
+ *   seq_lens, block_table and their errors as for gqa_decode_attn_paged
+ *   workspace: as for gqa_chunk_attn, of the bytes that
+ *   gqa_decode_attn_fp8_workspace gives (cap = max_blocks * block_size)
+ * The cache's bytes go to the tensor cores as they are, with fp32
+ * accumulation; query rows and softmax weights are each split into two e4m3
+ * pieces, which keeps 8 significant bits (bf16's own).  Rows p >= L_i are
+ * never used, whatever they hold.  The same call gives the same bits.
+ * Supported: GQA_BF16; d_k, d_v in {64, 128} (they may differ); n * (h / g)
+ * <= 32; b <= 65535.  (Other types: gqa_kv_read_fp8_paged, then the 16-bit
+ * and fp32 calls.)
+ *
+ * gqa_decode_attn_fp8_workspace - host only when num_sms > 0 (0: the current
+ * device's SM count).
+ */
+int gqa_decode_attn_fp8_paged(const void* q, const void* k_pool, const void* v_pool,
+                              const float* k_scale, const float* v_scale,
+                              const int32_t* block_table, const int32_t* seq_lens, int b,
+                              int n, int h, int g, int d_k, int d_v, float scale, void* out,
+                              int block_size, int max_blocks, int num_blocks, int dtype,
+                              void* workspace, long long workspace_bytes, void* stream);
+
+int gqa_decode_attn_fp8_workspace(int b, int n, int h, int g, int d_k, int d_v, long long cap,
+                                  int num_sms, long long* bytes);
+
 /* Name of a return code, for messages. */
 const char* gqa_status_string(int status);
 
