@@ -21,14 +21,15 @@
 // qs[a] is a power of two that puts the row's largest value into [128, 256),
 // so scaling loses nothing; P's common factor does the same for a tile.
 //
-// Roles (one persistent CTA per SM; 224 or 352 threads):
+// Roles (one persistent CTA per SM; 128 threads and 128 for every eight rows):
 //   warp 0     TMA: K and V rows of a tile (boxes of a block's rows, 128- or
 //              64-byte swizzle) into a three-stage ring, one lane per block
 //   warp 1     issues the S products, warp 2 the O products
-//   warps 3-6  softmax, correction, output (7-10 too for more than 16 rows):
-//              thread x holds positions x and x + 128 of S, column x of O;
-//              at a segment's start they split the query rows into shared
-//              memory
+//   warp 3     splits a segment's query rows into e4m3 pieces in shared
+//              memory, up to two segments ahead
+//   warps 4-7  softmax, correction, output of eight query rows (8-11, ... the
+//              next eight): thread x holds positions x and x + 128 of S,
+//              column x of O
 // P is written over the stage's K rows, which S no longer needs.
 //
 // The tiles of all units are laid end to end and dealt out evenly (Walker); a
@@ -52,11 +53,15 @@ constexpr float kLo = 16.f;  // the low piece's factor
 
 template <int NR, int DK, int DV>
 struct F8Cfg {
-  static constexpr int NWG = NR == 32 ? 2 : 1;
-  static constexpr int HP = NR / NWG;              // query rows of a softmax warpgroup
+  // softmax warpgroups of eight query rows each: a warpgroup's time per tile
+  // (one warp to a sub-partition, long dependent chains) is what bounds the
+  // loop.  Sixteen rows on one warpgroup: 51 us where two take 43 (24 ragged
+  // sequences of 512 to 32,766, g = 4, two tokens of seven heads)
+  static constexpr int HP = 8;
+  static constexpr int NWG = NR / HP;
   static constexpr int RP = NR < 16 ? 16 : NR;     // rows of a piece (padded)
   static constexpr int N = 2 * RP;                 // MMA columns: hi rows, lo rows
-  static constexpr int THREADS = 96 + 128 * NWG;
+  static constexpr int THREADS = 128 + 128 * NWG;
   static constexpr int K_BYTES = kTile * DK, V_BYTES = kTile * DV;
   // (d_v = 64: the O product's upper half reads past the V rows, within the
   // shared memory that follows)
@@ -65,12 +70,14 @@ struct F8Cfg {
   static constexpr int OFF_Q = kRing * STAGE;
   static constexpr int OFF_TAIL = OFF_Q + 2 * Q_BYTES;
   static constexpr int OFF_PAD = OFF_TAIL + (DV == 64 ? V_BYTES : 0);
-  static constexpr int OFF_RED = OFF_PAD;                       // [NWG][2][HP + 1][4]
+  static constexpr int OFF_SC = OFF_PAD;                        // float [kRing][2][kTile]
+  static constexpr int OFF_RED = OFF_SC + kRing * 2 * kTile * 4;  // [NWG][2][HP + 1][4]
   static constexpr int OFF_MAX = OFF_RED + NWG * 2 * (HP + 1) * 16;
   static constexpr int OFF_ALPHA = OFF_MAX + 2 * NR * 4;        // float [2][NR]
   static constexpr int OFF_QS = OFF_ALPHA + 2 * NR * 4;         // float [2][NR]
   static constexpr int OFF_VMAX = OFF_QS + 2 * NR * 4;          // float [2][NWG]
-  static constexpr int OFF_BAR = (OFF_VMAX + 2 * NWG * 4 + 15) / 16 * 16;
+  static constexpr int OFF_COL = (OFF_VMAX + 2 * NWG * 4 + 15) / 16 * 16;  // int [2][NR]
+  static constexpr int OFF_BAR = (OFF_COL + 2 * NR * 4 + 15) / 16 * 16;
   static constexpr int FULL_K = 0, FULL_V = kRing, EMPTY = 2 * kRing, Q_FULL = 3 * kRing,
                        Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, S_FREE = S_FULL + 2,
                        P_READY = S_FREE + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2,
@@ -143,13 +150,20 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < C::NBAR; ++k) {
-      const bool by_warps = (k >= C::Q_FULL && k < C::Q_EMPTY) ||
-                            (k >= C::S_FREE && k < C::O_FULL) ||
-                            (k >= C::O_FREE && k < C::DRAIN);
-      mbar_init(BAR(k), k == C::DRAIN ? 2 : by_warps ? 4 * NWG : 1);
+      const bool by_warps = (k >= C::S_FREE && k < C::O_FULL) || (k >= C::O_FREE && k < C::DRAIN);
+      const bool q_empty = k >= C::Q_EMPTY && k < C::S_FULL;  // softmax warps, last S product
+      mbar_init(BAR(k), k == C::DRAIN ? 2 : by_warps ? 4 * NWG : q_empty ? 4 * NWG + 1 : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
+  }
+  // query row a = s * r + t: its token s, and the offset of its output row
+  int* col_tok = reinterpret_cast<int*>(sm + C::OFF_COL);
+  int* col_off = col_tok + NR;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + NR) {
+    const int a = threadIdx.x - 64, s = a / p.r;
+    col_tok[a] = a < nr ? s : -(1 << 30);  // (a padded row sees nothing)
+    col_off[a] = a < nr ? (s * p.h + (a - s * p.r)) * DV : 0;
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_k);
@@ -161,6 +175,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait_then_release();
   if (warp == 2 && blockIdx.x == 0) report_bad_lengths(p.lens, p.b, p.nq, p.cap, p.status);
+
+  float* qs_sm = reinterpret_cast<float*>(sm + C::OFF_QS);  // the query rows' factors [2][NR]
 
   Walker w;
   w.init(p.lens, p.b, p.g, p.nq, p.cap, kTile, blockIdx.x, gridDim.x);
@@ -194,10 +210,13 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         const int cur = row;
         if (lt + 1 < seg.lt1) row = lookup(lt + 1);
         const int st = n % kRing;
+        // the scales of blocks in use (the others' are taken as 0)
+        const bool has = lane < sub && cur != oob_row;
+        const uint32_t sc_bytes = 8u * box * __popc(__ballot_sync(0xffffffffu, has));
         ok = __all_sync(0xffffffffu, wait(C::EMPTY + st, ((n / kRing) & 1) ^ 1));
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(BAR(C::FULL_K + st), C::K_BYTES);
+          mbar_arrive_expect_tx(BAR(C::FULL_K + st), C::K_BYTES + sc_bytes);
           mbar_arrive_expect_tx(BAR(C::FULL_V + st), C::V_BYTES);
         }
         __syncwarp();
@@ -205,6 +224,11 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         if (lane < sub) {
           tma_load_2d(dst + lane * box * DK, &tm_k, BAR(C::FULL_K + st), 0, cur, pol);
           tma_load_2d(dst + C::K_BYTES + lane * box * DV, &tm_v, BAR(C::FULL_V + st), 0, cur, pol);
+        }
+        if (has) {
+          const uint32_t sc = s_base + C::OFF_SC + (st * 2 * kTile + lane * box) * 4;
+          bulk_load(sc, p.k_scale + cur, box * 4, BAR(C::FULL_K + st));
+          bulk_load(sc + kTile * 4, p.v_scale + cur, box * 4, BAR(C::FULL_K + st));
         }
       }
     }
@@ -284,9 +308,78 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // ============================ query rows ==============================
+    constexpr int EPL = DK / 32;  // elements a lane; a warp to a row, four rows at a time
+    uint32_t k = 0;
+    while (w.next(seg)) {
+      const uint32_t qb = k & 1;
+      if (!__all_sync(0xffffffffu, wait(C::Q_EMPTY + qb, (k >> 1) ^ 1))) break;
+      const __nv_bfloat16* q0 =
+          p.q + (static_cast<size_t>(seg.i) * p.nq * p.h + seg.j * p.r) * DK + lane * EPL;
+      uint8_t* dst = sm + C::OFF_Q + qb * C::Q_BYTES;
+      // K-major rows of DK bytes, 16-byte chunks swizzled by the row
+      auto put = [&](int rr, uint32_t v) {
+        const int byte = lane * EPL, chunk = byte >> 4;
+        const int phys = DK == 128 ? (chunk ^ (rr & 7)) : (chunk ^ ((rr >> 1) & 3));
+        uint8_t* d = dst + rr * DK + phys * 16 + (byte & 15);
+        if constexpr (EPL == 4)
+          *reinterpret_cast<uint32_t*>(d) = v;
+        else
+          *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(v);
+      };
+      for (int a0 = 0; a0 < RP; a0 += 8) {
+        uint32_t raw[8][2];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          raw[t][0] = raw[t][1] = 0u;
+          const int a = a0 + t;
+          if (a < nr) {
+            // (col_off counts rows of DV elements)
+            const __nv_bfloat16* src = q0 + static_cast<size_t>(col_off[a] / DV) * DK;
+            if constexpr (EPL == 4) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+              raw[t][0] = v.x;
+              raw[t][1] = v.y;
+            } else {
+              raw[t][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const int a = a0 + t;
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[2 * e] = __uint_as_float(raw[t][e] << 16);
+            x[2 * e + 1] = __uint_as_float(raw[t][e] & 0xFFFF0000u);
+          }
+          const float amax =
+              warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+          // 2^ke * amax in [128, 256)
+          int ke = 0;
+          if (amax > 0.f && amax < INFINITY) ke = min(max(7 - ilogbf(amax), -126), 126);
+          const float up = ldexpf(1.f, ke);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] *= up;
+          uint32_t hi, lo;
+          split4(x, hi, lo);
+          put(a, hi);
+          put(RP + a, lo);
+          if (lane == 0 && a < NR)
+            qs_sm[qb * NR + a] = ldexpf(1.f, -ke) * p.scale_log2;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::Q_FULL + qb));
+      ++k;
+    }
+    __syncwarp();
   } else {
     // ====================== softmax, correction, output ===================
-    const int wg = (warp - 3) >> 2, wq = (warp - 3) & 3;
+    const int wg = (warp - 4) >> 2, wq = warp & 3;
     const int qd = warp & 3;               // TMEM lane quarter of this warp
     const int row = qd * 32 + lane;        // position (S), column (O)
     const int h0 = wg * HP;                // first query row of the warpgroup
@@ -296,23 +389,12 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     float* red = reinterpret_cast<float*>(sm + C::OFF_RED) + wg * 2 * (HP + 1) * 4;
     float* max_sm = reinterpret_cast<float*>(sm + C::OFF_MAX);
     float* alpha_sm = reinterpret_cast<float*>(sm + C::OFF_ALPHA);
-    float* qs_sm = reinterpret_cast<float*>(sm + C::OFF_QS);
     float* vmax_sm = reinterpret_cast<float*>(sm + C::OFF_VMAX);
     float l[HP], o[HP];
     float m_own = -INFINITY;  // running maximum of query row h0 + row (row < HP)
     uint32_t n = 0, k = 0;
     bool ok = true;
 
-    // scale of position pos of the segment's sequence (0 past its length)
-    auto scales = [&](int pos, float& ks, float& vs) {
-      ks = vs = 0.f;
-      if (pos >= seg.L) return;
-      const int blk = __ldg(p.table + static_cast<size_t>(seg.i) * p.max_blocks + pos / p.bsz);
-      if (blk < 0 || blk >= p.num_blocks) return;
-      const size_t at = (static_cast<size_t>(blk) * p.g + seg.j) * p.bsz + pos % p.bsz;
-      ks = __ldg(p.k_scale + at);
-      vs = __ldg(p.v_scale + at);
-    };
     // o = o * alpha + tile mt's product
     auto correct = [&](uint32_t mt) {
       const uint32_t nb = mt & 1;
@@ -339,63 +421,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     while (ok && w.next(seg)) {
       const uint32_t qb = k & 1;
       const int first_new = seg.L - p.nq;  // position of new token 0
-      float ks[2], vs[2];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) scales(seg.lt0 * kTile + row + hf * kHalf, ks[hf], vs[hf]);
-      // ---- the segment's query rows as e4m3 pieces: a warp to a row ----
-      ok = __all_sync(0xffffffffu, wait(C::Q_EMPTY + qb, (k >> 1) ^ 1));
+      ok = __all_sync(0xffffffffu, wait(C::Q_FULL + qb, k >> 1));  // (the rows' factors)
       if (!ok) break;
-      for (int a = h0 + wq; a < h0 + RP / NWG; a += 4) {
-        constexpr int EPL = DK / 32;  // elements a lane
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (a < nr) {
-          const int s = a / p.r;
-          const __nv_bfloat16* src =
-              p.q + ((static_cast<size_t>(seg.i) * p.nq + s) * p.h + seg.j * p.r + (a - s * p.r)) *
-                        DK + lane * EPL;
-          uint32_t raw[2] = {0u, 0u};
-          if constexpr (EPL == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-            raw[0] = v.x;
-            raw[1] = v.y;
-          } else {
-            raw[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-          }
-#pragma unroll
-          for (int e = 0; e < EPL; e += 2) {
-            x[e] = __uint_as_float(raw[e >> 1] << 16);
-            x[e + 1] = __uint_as_float(raw[e >> 1] & 0xFFFF0000u);
-          }
-        }
-        const float amax =
-            warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-        // 2^ke * amax in [128, 256)
-        int ke = 0;
-        if (amax > 0.f && amax < INFINITY) ke = min(max(7 - ilogbf(amax), -126), 126);
-        const float up = ldexpf(1.f, ke);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= up;
-        uint32_t hi, lo;
-        split4(x, hi, lo);
-        // K-major rows of DK bytes, 16-byte chunks swizzled by the row
-        auto put = [&](int rr, uint32_t v) {
-          const int byte = lane * EPL;
-          const int chunk = byte >> 4;
-          const int phys = DK == 128 ? (chunk ^ (rr & 7)) : (chunk ^ ((rr >> 1) & 3));
-          uint8_t* dst = sm + C::OFF_Q + qb * C::Q_BYTES + rr * DK + phys * 16 + (byte & 15);
-          if constexpr (EPL == 4)
-            *reinterpret_cast<uint32_t*>(dst) = v;
-          else
-            *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(v);
-        };
-        put(a, hi);
-        put(RP + a, lo);
-        if (lane == 0 && a < NR) qs_sm[qb * NR + a] = ldexpf(1.f, -ke) * p.scale_log2;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::Q_FULL + qb));
-      named_bar_sync(bar_id, 128);  // (the rows' factors, for the whole warpgroup)
       m_own = -INFINITY;
 #pragma unroll
       for (int e = 0; e < HP; ++e) l[e] = o[e] = 0.f;
@@ -404,15 +431,20 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         const uint32_t nb = n & 1;
         const int st = n % kRing;
         const int valid = min(kTile, seg.L - lt * kTile);
-        float ksn[2] = {0.f, 0.f}, vsn[2] = {0.f, 0.f};
-        if (lt + 1 < seg.lt1) {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            scales((lt + 1) * kTile + row + hf * kHalf, ksn[hf], vsn[hf]);
-        }
-        ok = __all_sync(0xffffffffu, wait(C::S_FULL + nb, n >> 1));
+        // (S_FULL comes after FULL_K, so the second wait is for the scales'
+        // visibility alone)
+        ok = __all_sync(0xffffffffu, wait(C::S_FULL + nb, n >> 1) &&
+                                         wait(C::FULL_K + st, n / kRing));
         if (!ok) break;
         tc_fence_after();
+        const float* sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + st * 2 * kTile + row;
+        float ks[2], vs[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const bool in = row + hf * kHalf < valid;
+          ks[hf] = in ? sc[hf * kHalf] : 0.f;
+          vs[hf] = in ? sc[kTile + hf * kHalf] : 0.f;
+        }
         float x[2][HP];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -430,16 +462,24 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::S_FREE + nb));
         const float* qs = qs_sm + qb * NR + h0;
-        const bool all_seen = (lt + 1) * kTile <= first_new + 1;
+        if ((lt + 1) * kTile <= first_new + 1) {
+          // (uniform) every query row sees every position of the tile
 #pragma unroll
-        for (int e = 0; e < HP; ++e) {
-          const float f = qs[e];
-          int last = first_new;  // last position that query row h0 + e sees
-          if (!all_seen) last += (h0 + e) / p.r;
+          for (int e = 0; e < HP; ++e) {
+            const float f = qs[e];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const bool seen = h0 + e < nr && (all_seen || lt * kTile + row + hf * kHalf <= last);
-            x[hf][e] = seen ? x[hf][e] * (ks[hf] * f) : -INFINITY;
+            for (int hf = 0; hf < 2; ++hf)
+              x[hf][e] = h0 + e < nr ? x[hf][e] * (ks[hf] * f) : -INFINITY;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < HP; ++e) {
+            const int last = first_new + col_tok[h0 + e];  // last position the row sees
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const bool seen = lt * kTile + row + hf * kHalf <= last;
+              x[hf][e] = seen ? x[hf][e] * (ks[hf] * qs[e]) : -INFINITY;
+            }
           }
         }
         // ---- maxima over the tile's positions, and of the V scales ----
@@ -492,14 +532,26 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
             split4(v, hi[c], lo[c]);
           }
           const uint32_t base = s_base + st * C::STAGE + pr * N;
+          // (one warpgroup: the chunk's rows 8-15 are padding, zeros)
           auto put = [&](int cg, const uint32_t (&v)[4]) {
             const int phys = N == 32 ? (cg ^ ((pr >> 2) & 1)) : (cg ^ ((pr >> 1) & 3));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + phys * 16),
-                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                         : "memory");
+            if constexpr (NWG == 1)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + phys * 16),
+                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                           : "memory");
+            else
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(base + phys * 16 +
+                                                                    (wg & 1) * 8),
+                           "r"(v[0]), "r"(v[1])
+                           : "memory");
           };
-          put(wg, hi);
-          put(RP / 16 + wg, lo);
+          if constexpr (NWG == 1) {
+            put(0, hi);
+            put(1, lo);
+          } else {
+            put(wg >> 1, hi);
+            put(RP / 16 + (wg >> 1), lo);
+          }
         }
         // ---- V rows past L_i hold anything: zero them ----
         if (wg == 0 && valid < kTile) {
@@ -524,27 +576,40 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         if (lt > seg.lt0) correct(n - 1);
         if (lt == seg.lt1 - 1) correct(n);
         if (!ok) break;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          ks[hf] = ksn[hf];
-          vs[hf] = vsn[hf];
-        }
       }
       if (!ok) break;
       ++k;
+      if (lane == 0) mbar_arrive(BAR(C::Q_EMPTY + qb));
       // ---- segment end: the row sums across the warpgroup, then the output
       // or a partial ----
       const uint32_t nb = (n - 1) & 1;
       float* rb = red + nb * (HP + 1) * 4;
+      {
+        // each round trades half of the sums still held with a partner lane;
+        // lane x ends with the warp's sum of row x / (32 / HP)
+        float v[HP];
 #pragma unroll
-      for (int e = 0; e < HP; ++e) {
-        const float sum = warp_sum(l[e]);
-        if (lane == 0) rb[e * 4 + wq] = sum;
+        for (int e = 0; e < HP; ++e) v[e] = l[e];
+#pragma unroll
+        for (int o2 = 16, nv = HP; o2 >= 32 / HP; o2 >>= 1, nv >>= 1) {
+          const bool up = (lane & o2) != 0;
+#pragma unroll
+          for (int e = 0; e < nv / 2; ++e) {
+            const float send = up ? v[e] : v[e + nv / 2];
+            const float keep = up ? v[e + nv / 2] : v[e];
+            v[e] = keep + __shfl_xor_sync(0xffffffffu, send, o2);
+          }
+        }
+#pragma unroll
+        for (int o2 = 16 / HP; o2 > 0; o2 >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o2);
+        if (lane % (32 / HP) == 0) rb[(lane / (32 / HP)) * 4 + wq] = v[0];
       }
       named_bar_sync(bar_id, 128);
       const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
       const int u = seg.i * p.g + seg.j;
       const size_t slot = static_cast<size_t>(u) + blockIdx.x;
+      __nv_bfloat16* obase =
+          p.out + (static_cast<size_t>(seg.i) * p.nq * p.h + seg.j * p.r) * DV + row;
 #pragma unroll
       for (int e = 0; e < HP; ++e) {
         const int a = h0 + e;
@@ -552,10 +617,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           const float4 v = *reinterpret_cast<const float4*>(rb + 4 * e);
           const float sum = (v.x + v.y) + (v.z + v.w);
           if (whole) {
-            const int s = a / p.r;
-            if (row < DV)
-              p.out[((static_cast<size_t>(seg.i) * p.nq + s) * p.h + seg.j * p.r +
-                     (a - s * p.r)) * DV + row] = __float2bfloat16_rn(o[e] / sum);
+            if (row < DV) obase[col_off[a]] = __float2bfloat16_rn(o[e] * (1.f / sum));
           } else {
             const size_t sl = slot * nr + a;
             if (row < DV) p.part_o[sl * DV + row] = o[e];
@@ -630,8 +692,8 @@ int f8_check(const F8Call& x) {
     return e;
   if (x.dtype != GQA_BF16) return GQA_ERR_UNSUPPORTED;
   auto off = [](const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) != 0; };
-  if (off(x.q, 15) || off(x.k, 15) || off(x.v, 15) || off(x.out, 15) || off(x.k_scale, 3) ||
-      off(x.v_scale, 3) || off(x.lens, 3) || off(x.ws, 255))
+  if (off(x.q, 15) || off(x.k, 15) || off(x.v, 15) || off(x.out, 15) || off(x.k_scale, 15) ||
+      off(x.v_scale, 15) || off(x.lens, 3) || off(x.ws, 255))
     return GQA_ERR_ALIGN;
   return GQA_OK;
 }

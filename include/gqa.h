@@ -495,7 +495,8 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  *   A row x (in fp32, after norm and rotation) is stored as scale =
  *   max|x| / 448 and round-to-nearest e4m3(x / scale); a row of zeros has
  *   scale 0.  d_k and d_v multiples of 16.  Rows that hold infinities or
- *   NaN are stored as rows that hold NaN.
+ *   NaN are stored as rows that hold NaN.  The scales are 16-byte aligned for
+ *   gqa_decode_attn_fp8_paged.
  *
  * gqa_kv_read_fp8_paged - rows [0, L_i) of every sequence of an 8-bit paged
  *   cache, as scale * value rounded to dtype, into contiguous caches
