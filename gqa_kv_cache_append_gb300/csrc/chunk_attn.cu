@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float y[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) y[k] = o[e + k] * inv;
-              Piece8<T16>::store(dst + 32 * c + e, y);
+              store8(dst + 32 * c + e, y);
             }
           }
         }

@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/gqa.h"
 #include "gqa_internal.h"
@@ -27,9 +28,6 @@
 
 namespace gqa {
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kMaxRot = 256;
 
 struct RopeLaunch {
   const void *q, *k, *v;                 // [total, heads, d], token strides below
@@ -50,52 +48,81 @@ struct RopeLaunch {
   unsigned int* status;
 };
 
-// One block: `rpp` rows (query, then K, then V heads) of one token; GS lanes
-// hold a row, eight elements each.  Memory-bound: every row is read and
-// written once as 16-byte pieces, all loads of a thread go out before the
-// position is known, and sine and cosine are computed once per block for all
-// its rows.
-template <typename T, bool FP8, int IT>
-__global__ void __launch_bounds__(kThreads)
-    rope_append_kernel(const RopeLaunch a, int parts, int rpp, int gs) {
-  __shared__ float s_cos[kMaxRot / 2], s_sin[kMaxRot / 2];
-  pdl_wait_then_release();
-  if (blockIdx.x == 0 && threadIdx.x < 32)
-    report_bad_packed(a.cu, a.lens, a.b, a.total, a.cap, a.status);
-  const int t = blockIdx.x / parts, part = blockIdx.x - t * parts;
-  const int ngrp = kThreads / gs;
-  const int grp = threadIdx.x / gs, e0 = (threadIdx.x % gs) * 8;
-  const int hq = a.q != nullptr ? a.h : 0;
-  const int rows = hq + 2 * a.g;
-  const int r0 = part * rpp, r1 = min(rows, r0 + rpp);
+constexpr int kRopeThreads = 128;
+constexpr int kBatch = 4;  // rows a lane loads ahead of their use
 
-  Piece8<T> x[IT];
+// One warp: a run of the rows of one token, query, then K, then V heads.  GS
+// lanes hold a row, eight elements each, so 32 / GS rows go side by side.  A
+// lane's eight elements are two pieces of four that hold both elements of
+// every pair it turns: 4 g .. and rot/2 + 4 g .. of the halves layout (lanes
+// past the rotated part, and the pairs layout: 8 g .. 8 g + 7), so rotation
+// needs no exchange between lanes, and either way lane g turns pairs 4 g ..
+// 4 g + 3, whose sines it computes once for all rows, with the norm's weights
+// multiplied in.  Warps do not wait for one another, and the first rows'
+// loads go out before the position is known.
+//
+// Bound by memory (every row read and written once) and by instructions close
+// behind it.  Measured (graph replay): one block per token, sines in shared
+// memory and a shuffle per exchanged element 58 us for 2 x 4096 fp16 tokens
+// and 113 us for 24 ragged sequences (11,290 tokens, h = 28); a warp per
+// token, the kind of a row chosen row by row 47 and 67 us; this form XX, YY.
+enum { ROW_Q = 0, ROW_K = 1, ROW_V = 2 };
+
+template <typename T, bool FP8, int GS>
+__global__ void __launch_bounds__(kRopeThreads, 8)
+    rope_append_kernel(const RopeLaunch a, int parts, int per_part) {
+  constexpr int SIDE = 32 / GS;  // rows side by side
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31;
+  const long long task =
+      static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  if (task == 0) report_bad_packed(a.cu, a.lens, a.b, a.total, a.cap, a.status);
+  const int t = static_cast<int>(task / parts);
+  const int part = static_cast<int>(task - static_cast<long long>(t) * parts);
+  if (t >= a.total) return;
+  const int grp = lane / GS, g8 = lane % GS;
+  // steps of SIDE rows: those of the query heads, then of K, then of V
+  const int hq = a.q != nullptr ? a.h : 0;
+  const int nq = (hq + SIDE - 1) / SIDE, nk = (a.g + SIDE - 1) / SIDE;
+  const int s0 = part * per_part, s1 = min(nq + 2 * nk, s0 + per_part);
+  const bool turns = a.phase != nullptr && 8 * g8 < a.rot;
+  const bool halves = turns && !a.pairs;
+  const int o0 = halves ? 4 * g8 : 8 * g8, o1 = halves ? (a.rot >> 1) + 4 * g8 : 8 * g8 + 4;
+
+  Piece4<T> x[kBatch][2];
+  // rows of kind KIND from its step `st` on
+  auto load = [&](auto kind, int st) {
+    constexpr int KIND = decltype(kind)::value;
+    const int heads = KIND == ROW_Q ? hq : a.g, d = KIND == ROW_V ? a.dv : a.dk;
+    const T* src = KIND == ROW_Q   ? static_cast<const T*>(a.q) + t * a.q_stride
+                   : KIND == ROW_K ? static_cast<const T*>(a.k) + t * a.k_stride
+                                   : static_cast<const T*>(a.v) + t * a.v_stride;
+    const int row = st * SIDE + grp;
+    src += row * d;
+    const int p0 = KIND == ROW_V ? 8 * g8 : o0, p1 = KIND == ROW_V ? 8 * g8 + 4 : o1;
+    const bool in = 8 * g8 < d;
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int row = r0 + grp + it * ngrp;
-    x[it].zero();
-    if (row < r1) {
-      if (row < hq) {
-        if (e0 < a.dk)
-          x[it].load(static_cast<const T*>(a.q) + t * a.q_stride + row * a.dk + e0);
-      } else if (row < hq + a.g) {
-        if (e0 < a.dk)
-          x[it].load(static_cast<const T*>(a.k) + t * a.k_stride + (row - hq) * a.dk + e0);
-      } else if (e0 < a.dv) {
-        x[it].load(static_cast<const T*>(a.v) + t * a.v_stride + (row - hq - a.g) * a.dv + e0);
+    for (int k = 0; k < kBatch; ++k) {
+      if (in && row + k * SIDE < heads) {
+        x[k][0].load(src + k * SIDE * d + p0);
+        x[k][1].load(src + k * SIDE * d + p1);
+      } else {
+        x[k][0].zero();
+        x[k][1].zero();
       }
     }
-  }
-  Piece8<T> wq, wk;
-  if (a.q_w != nullptr && e0 < a.dk) {
-    wq.load(static_cast<const T*>(a.q_w) + e0);
-    wk.load(static_cast<const T*>(a.k_w) + e0);
-  } else {
-    wq.zero();
-    wk.zero();
-  }
+  };
+  using Q = std::integral_constant<int, ROW_Q>;
+  using K = std::integral_constant<int, ROW_K>;
+  using V = std::integral_constant<int, ROW_V>;
+  if (s0 < nq)
+    load(Q{}, s0);
+  else if (s0 < nq + nk)
+    load(K{}, s0 - nq);
+  else
+    load(V{}, s0 - nq - nk);
 
-  // the token's sequence and position (every warp; uniform across the block)
+  // the token's sequence and position (uniform across the warp)
   const int i = packed_sequence(a.cu, a.b, t);
   if (i >= a.b) return;  // behind the last sequence
   const int t0 = __ldg(a.cu + i), t1 = __ldg(a.cu + i + 1), L = __ldg(a.lens + i);
@@ -106,175 +133,235 @@ __global__ void __launch_bounds__(kThreads)
     blk = __ldg(a.table + static_cast<size_t>(i) * a.max_blocks + P / a.bsz);
     prow = P % a.bsz;
     if (blk < 0 || blk >= a.num_blocks) {
-      if (threadIdx.x == 0 && part == 0) atomicOr(a.status, GQA_DEV_BAD_BLOCK);
+      if (lane == 0 && s1 > nq) atomicOr(a.status, GQA_DEV_BAD_BLOCK);
       blk = -1;
     }
   }
-  if (a.phase != nullptr) {
-    for (int m = threadIdx.x; m < a.rot / 2; m += kThreads) {
-      const unsigned long long ph = __ldg(a.phase + m) * static_cast<unsigned long long>(P);
+  float cs[4], sn[4];  // of pairs 4 g8 ..
+  if (turns) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const unsigned long long ph =
+          __ldg(a.phase + 4 * g8 + k) * static_cast<unsigned long long>(P);
       // the angle over pi, in [-1, 1)
-      const float y = static_cast<float>(static_cast<int>(ph >> 32)) * 0x1p-31f;
-      float sn, cs;
-      sincospif(y, &sn, &cs);
-      s_cos[m] = cs * a.rope_scale;
-      s_sin[m] = sn * a.rope_scale;
-    }
-    __syncthreads();
-  }
-  // this thread's eight elements of the rotation: y = x * c + partner * s
-  const bool rotates = a.phase != nullptr && e0 < a.rot;
-  const int half = a.rot >> 1;
-  float c[8], s[8];
-  if (rotates) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int e = e0 + k;
-      const bool second = a.pairs ? (e & 1) : (e >= half);
-      const int m = a.pairs ? (e >> 1) : (second ? e - half : e);
-      c[k] = s_cos[m];
-      s[k] = second ? s_sin[m] : -s_sin[m];
+      sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 0x1p-31f, &sn[k], &cs[k]);
+      cs[k] *= a.rope_scale;
+      sn[k] *= a.rope_scale;
     }
   }
-  // the lane that holds the other halves of this lane's pairs
-  const int lane_g = threadIdx.x % gs;
-  const int mate = (rotates && !a.pairs) ? (e0 < half ? lane_g + (half >> 3) : lane_g - (half >> 3))
-                                         : lane_g;
-#pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int row = r0 + grp + it * ngrp;
-    // (whole groups of lanes take each branch; the shuffles are among the
-    // gs lanes of a row, with every lane of the warp taking part)
-    const bool live = row < r1;
-    const bool is_v = row >= hq + a.g;
-    const int d = is_v ? a.dv : a.dk;
-    float v[8];
-    x[it].get(v);
-    if (a.q_w != nullptr) {
-      float ss = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
-      for (int o = gs >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (!is_v) {
-        const float inv = rsqrtf(ss / static_cast<float>(a.dk) + a.eps);
-        float w[8];
-        if (row < hq)
-          wq.get(w);
-        else
-          wk.get(w);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = v[k] * inv * w[k];
-      }
-    }
-    if (a.phase != nullptr) {
-      float p[8];
-      if (a.pairs) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[k] = v[k ^ 1];
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[k] = __shfl_sync(0xffffffffu, v[k], mate, gs);
-      }
-      if (rotates && !is_v) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = fmaf(v[k], c[k], p[k] * s[k]);
-      }
-    }
-    const bool mine = live && e0 < d;
-    if (row < hq) {
-      if (mine)
-        Piece8<T>::store(
-            static_cast<T*>(a.q_out) + (static_cast<size_t>(t) * a.h + row) * a.dk + e0, v);
-      if (!FP8) continue;
-    }
-    const int j = is_v ? row - hq - a.g : row - hq;
-    const long long dst = (static_cast<long long>(blk) * a.g + j) * a.bsz + prow;
-    if constexpr (FP8) {
-      float amax = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
-      for (int o = gs >> 1; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (mine && row >= hq && blk >= 0) {
-        const float sc = amax / kE4m3Max;
-        const float div = sc > 0.f ? sc : 1.f;
-        uint2 pk;
-        pk.x = e4m3_pack4(v[0] / div, v[1] / div, v[2] / div, v[3] / div);
-        pk.y = e4m3_pack4(v[4] / div, v[5] / div, v[6] / div, v[7] / div);
-        uint8_t* base = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache);
-        *reinterpret_cast<uint2*>(base + dst * d + e0) = pk;
-        if (e0 == 0) (is_v ? a.v_scale : a.k_scale)[dst] = sc;
-      }
-    } else if (mine && blk >= 0) {
-      T* base = static_cast<T*>(is_v ? a.v_cache : a.k_cache);
-      if (is_v)
-        x[it].copy_to(base + dst * d + e0);  // (bit for bit)
-      else
-        Piece8<T>::store(base + dst * d + e0, v);
-    }
-  }
-}
+  const float inv_d = 1.f / static_cast<float>(a.dk);
 
-// ---------------------------------------------------------------------------
-// e4m3 cache -> rows of the call's type: positions [64 x, 64 x + 64) of KV
-// head y of sequence z, 16 elements a thread and step.  Memory-bound: (d + 4)
-// bytes read and d * sizeof(T) written per row.
-// ---------------------------------------------------------------------------
-constexpr int kReadRows = 64;
-
-template <typename T>
-__device__ __forceinline__ void read_rows(const uint8_t* pool, const float* scale, T* cache,
-                                          const int* trow, int p0, int rows, int d, int g, int j,
-                                          int bsz, int num_blocks, long long dst_row,
-                                          unsigned int* status) {
-  const int per = d >> 4;  // 16-byte pieces a row
-  for (int idx = threadIdx.x; idx < rows * per; idx += kThreads) {
-    const int rr = idx / per, c = idx - rr * per;
-    const int p = p0 + rr;
-    const int blk = __ldg(trow + p / bsz);
-    if (blk < 0 || blk >= num_blocks) {
-      if (c == 0) atomicOr(status, GQA_DEV_BAD_BLOCK);
-      continue;
-    }
-    const long long src = (static_cast<long long>(blk) * g + j) * bsz + p % bsz;
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(pool + src * d) + c);
-    const float sc = __ldg(scale + src);
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    T* dst = cache + (dst_row + rr) * d + 16 * c;
+  auto run = [&](auto kind, int from, int to, bool loaded) {
+    constexpr int KIND = decltype(kind)::value;
+    const int heads = KIND == ROW_Q ? hq : a.g, d = KIND == ROW_V ? a.dv : a.dk;
+    const bool in = 8 * g8 < d;
+    const int p0 = KIND == ROW_V ? 8 * g8 : o0, p1 = KIND == ROW_V ? 8 * g8 + 4 : o1;
+    const bool norm = KIND != ROW_V && a.q_w != nullptr;
+    float w[8];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float x[8];
+    for (int k = 0; k < 8; ++k) w[k] = 1.f;
+    if (norm && in) {
+      Piece4<T> r[2];
+      const T* src = static_cast<const T*>(KIND == ROW_Q ? a.q_w : a.k_w);
+      r[0].load(src + o0);
+      r[1].load(src + o1);
+      r[0].get(w);
+      r[1].get(w + 4);
+    }
+    // pair k of the lane: first element e0(k), second e1(k) of the eight;
+    // first' = first * A - second * B, second' = second * C + first * D
+    float A[4], B[4], C[4], D[4];
+    if (KIND != ROW_V && turns) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 f = e4m3_unpack2(w[2 * hf + (k >> 1)] >> (16 * (k & 1)));
-        x[2 * k] = f.x * sc;
-        x[2 * k + 1] = f.y * sc;
+        const float w0 = halves ? w[k] : w[2 * k], w1 = halves ? w[4 + k] : w[2 * k + 1];
+        A[k] = w0 * cs[k];
+        B[k] = w1 * sn[k];
+        C[k] = w1 * cs[k];
+        D[k] = w0 * sn[k];
       }
-      Piece8<T>::store(dst + 8 * hf, x);
     }
-  }
+    for (int st = from; st < to; st += kBatch) {
+      if (!loaded) load(kind, st);
+      loaded = false;
+#pragma unroll
+      for (int it = 0; it < kBatch; ++it) {
+        if (st + it >= to) break;  // (uniform)
+        const int row = (st + it) * SIDE + grp;
+        const bool mine = in && row < heads;
+        float v[8];
+        x[it][0].get(v);
+        x[it][1].get(v + 4);
+        float inv = 1.f;
+        if (norm) {
+          float ss = v[0] * v[0];
+#pragma unroll
+          for (int k = 1; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+#pragma unroll
+          for (int o = GS / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+        }
+        if (KIND != ROW_V) {
+          if (halves) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float p = v[k] * inv, q = v[4 + k] * inv;
+              v[k] = fmaf(p, A[k], -(q * B[k]));
+              v[4 + k] = fmaf(q, C[k], p * D[k]);
+            }
+          } else if (turns) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float p = v[2 * k] * inv, q = v[2 * k + 1] * inv;
+              v[2 * k] = fmaf(p, A[k], -(q * B[k]));
+              v[2 * k + 1] = fmaf(q, C[k], p * D[k]);
+            }
+          } else if (norm) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= inv * w[k];
+          }
+        }
+        if (KIND == ROW_Q) {
+          if (mine) {
+            T* dst = static_cast<T*>(a.q_out) + (static_cast<size_t>(t) * a.h + row) * d;
+            Piece4<T>::store(dst + p0, v);
+            Piece4<T>::store(dst + p1, v + 4);
+          }
+          continue;
+        }
+        const long long dst = (static_cast<long long>(blk) * a.g + row) * a.bsz + prow;
+        if constexpr (FP8) {
+          float amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(v[k]));
+#pragma unroll
+          for (int o = GS / 2; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // (rows so small that the factor would overflow: scaled up first)
+          const bool tiny = amax < 0x1p-100f;
+          const float up = tiny ? 0x1p60f : 1.f;
+          const float f = amax > 0.f ? kE4m3Max / (amax * up) : 0.f;
+          if (mine && blk >= 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = v[k] * up * f;
+            uint8_t* to8 = static_cast<uint8_t*>(KIND == ROW_V ? a.v_cache : a.k_cache) + dst * d;
+            *reinterpret_cast<uint32_t*>(to8 + p0) = e4m3_pack4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint32_t*>(to8 + p1) = e4m3_pack4(v[4], v[5], v[6], v[7]);
+            if (g8 == 0) (KIND == ROW_V ? a.v_scale : a.k_scale)[dst] = amax / kE4m3Max;
+          }
+        } else if (mine && blk >= 0) {
+          T* to16 = static_cast<T*>(KIND == ROW_V ? a.v_cache : a.k_cache) + dst * d;
+          if (KIND == ROW_V) {  // (bit for bit)
+            x[it][0].copy_to(to16 + p0);
+            x[it][1].copy_to(to16 + p1);
+          } else {
+            Piece4<T>::store(to16 + p0, v);
+            Piece4<T>::store(to16 + p1, v + 4);
+          }
+        }
+      }
+    }
+  };
+  if (s0 < nq) run(Q{}, s0, min(s1, nq), true);
+  if (s0 < nq + nk && s1 > nq)
+    run(K{}, max(s0 - nq, 0), min(s1 - nq, nk), s0 >= nq);
+  if (s1 > nq + nk) run(V{}, max(s0 - nq - nk, 0), s1 - nq - nk, s0 >= nq + nk);
 }
 
+// ---------------------------------------------------------------------------
+// e4m3 cache -> rows of the call's type: positions [128 x, 128 x + 128) of KV
+// head y of sequence z.  A thread takes one 16-byte piece of every
+// (256 / pieces)-th row, four rows of K and four of V at a time with their
+// loads side by side (with two in flight 86 MB took 20 us, with eight ZZ).
+// Memory-bound: d + 4 bytes read and d * sizeof(T) written per row.
+// ---------------------------------------------------------------------------
+constexpr int kReadRows = 128;
+constexpr int kReadThreads = 256;
+
+struct ReadRows {  // what a thread reads of one tensor
+  uint4 raw[4];
+  float sc[4];
+  unsigned use;    // bit u: row u is there
+  int c, row0, step, d;
+
+  __device__ void start(int d_) {
+    d = d_;
+    const int per = d >> 4;  // pieces of a row
+    row0 = threadIdx.x / per;
+    c = threadIdx.x - row0 * per;
+    step = kReadThreads / per;
+    if (row0 >= step) row0 = 1 << 30;  // (256 not a multiple of the pieces)
+  }
+  __device__ void load(const uint8_t* __restrict__ pool, const float* __restrict__ scale,
+                       const int* trow, int base, int p0, int rows, int g, int j, int bshift,
+                       int num_blocks, unsigned int* status) {
+    use = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int rr = row0 + base + u * step;
+      if (row0 >= rows || rr >= rows) continue;
+      const int p = p0 + rr;
+      const int blk = __ldg(trow + (p >> bshift));
+      if (blk < 0 || blk >= num_blocks) {
+        atomicOr(status, GQA_DEV_BAD_BLOCK);
+        continue;
+      }
+      const long long src =
+          ((static_cast<long long>(blk) * g + j) << bshift) + (p & ((1 << bshift) - 1));
+      raw[u] = __ldg(reinterpret_cast<const uint4*>(pool + src * d) + c);
+      sc[u] = __ldg(scale + src);
+      use |= 1u << u;
+    }
+  }
+  template <typename T>
+  __device__ void store(T* __restrict__ dst, int base) const {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (!(use & (1u << u))) continue;
+      T* to = dst + static_cast<size_t>(row0 + base + u * step) * d + 16 * c;
+      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = e4m3_unpack2(w[2 * hf + (k >> 1)] >> (16 * (k & 1)));
+          x[2 * k] = f.x * sc[u];
+          x[2 * k + 1] = f.y * sc[u];
+        }
+        store8(to + 8 * hf, x);
+      }
+    }
+  }
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kReadThreads)
     kv_read_fp8_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                        const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                        const int* __restrict__ table, const int* __restrict__ lens,
                        T* __restrict__ k_cache, T* __restrict__ v_cache, int g, int dk, int dv,
-                       int bsz, int max_blocks, int num_blocks, int cap, unsigned int* status) {
+                       int bshift, int max_blocks, int num_blocks, int cap, unsigned int* status) {
   pdl_wait_then_release();
   const int i = blockIdx.z, j = blockIdx.y, p0 = blockIdx.x * kReadRows;
   const int L = __ldg(lens + i);
-  if (L < 0 || L > cap || L > static_cast<long long>(max_blocks) * bsz) {
+  if (L < 0 || L > cap || L > (static_cast<long long>(max_blocks) << bshift)) {
     if (p0 == 0 && j == 0 && threadIdx.x == 0) atomicOr(status, GQA_DEV_BAD_SEQ_LEN);
     return;
   }
   const int rows = min(kReadRows, L - p0);
   if (rows <= 0) return;
   const int* trow = table + static_cast<size_t>(i) * max_blocks;
-  const long long dst_row = (static_cast<long long>(i) * g + j) * cap + p0;
-  read_rows(k_pool, k_scale, k_cache, trow, p0, rows, dk, g, j, bsz, num_blocks, dst_row, status);
-  read_rows(v_pool, v_scale, v_cache, trow, p0, rows, dv, g, j, bsz, num_blocks, dst_row, status);
+  const size_t dst0 = (static_cast<size_t>(i) * g + j) * cap + p0;
+  ReadRows k, v;
+  k.start(dk);
+  v.start(dv);
+  for (int kb = 0, vb = 0; kb < rows || vb < rows; kb += 4 * k.step, vb += 4 * v.step) {
+    k.load(k_pool, k_scale, trow, kb, p0, rows, g, j, bshift, num_blocks, status);
+    v.load(v_pool, v_scale, trow, vb, p0, rows, g, j, bshift, num_blocks, status);
+    k.store(k_cache + dst0 * dk, kb);
+    v.store(v_cache + dst0 * dv, vb);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -295,24 +382,30 @@ cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, int threads, cudaStre
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+template <typename T, bool FP8, int GS>
+cudaError_t launch_rope_gs(const RopeLaunch& a, int num_sms, cudaStream_t st) {
+  constexpr int SIDE = 32 / GS;
+  const int nq = ((a.q != nullptr ? a.h : 0) + SIDE - 1) / SIDE, nk = (a.g + SIDE - 1) / SIDE;
+  const int steps = nq + 2 * nk;
+  // a warp takes a whole token, unless that leaves the SMs short of warps
+  // (16 each): then the token's rows are dealt out to several
+  const long long want = 16ll * num_sms;
+  int parts = static_cast<int>(std::min<long long>((want + a.total - 1) / a.total, steps));
+  const int per_part = (steps + parts - 1) / parts;
+  parts = (steps + per_part - 1) / per_part;
+  constexpr int kWarps = kRopeThreads / 32;
+  const long long blocks = (static_cast<long long>(a.total) * parts + kWarps - 1) / kWarps;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  return launch_pdl(rope_append_kernel<T, FP8, GS>, dim3(static_cast<unsigned>(blocks)),
+                    kRopeThreads, st, a, parts, per_part);
+}
+
 template <typename T, bool FP8>
 cudaError_t launch_rope_t(const RopeLaunch& a, int num_sms, cudaStream_t st) {
-  int gs = 8;
-  while (gs * 8 < a.dk || gs * 8 < a.dv) gs *= 2;
-  const int ngrp = kThreads / gs;
-  const int rows = (a.q != nullptr ? a.h : 0) + 2 * a.g;
-  // few tokens: one row a thread group, so that the rows of a token spread
-  // over several SMs; many: four, which shares the position's sines among
-  // more rows and keeps four loads of a thread in flight
-  const bool small = static_cast<long long>(a.total) * ((rows + ngrp - 1) / ngrp) <= 2 * num_sms;
-  const int it = small ? 1 : 4;
-  const int parts = (rows + ngrp * it - 1) / (ngrp * it);
-  const int rpp = (rows + parts - 1) / parts;
-  const long long blocks = static_cast<long long>(a.total) * parts;
-  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  return small ? launch_pdl(rope_append_kernel<T, FP8, 1>, grid, kThreads, st, a, parts, rpp, gs)
-               : launch_pdl(rope_append_kernel<T, FP8, 4>, grid, kThreads, st, a, parts, rpp, gs);
+  const int d = std::max(a.dk, a.dv);
+  return d <= 64    ? launch_rope_gs<T, FP8, 8>(a, num_sms, st)
+         : d <= 128 ? launch_rope_gs<T, FP8, 16>(a, num_sms, st)
+                    : launch_rope_gs<T, FP8, 32>(a, num_sms, st);
 }
 
 template <bool FP8>
@@ -500,21 +593,23 @@ int gqa_kv_read_fp8_paged(const void* k_pool, const void* v_pool, const float* k
   const dim3 grid(static_cast<unsigned>((rows + kReadRows - 1) / kReadRows), g, b);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const uint8_t *kp = static_cast<const uint8_t*>(k_pool), *vp = static_cast<const uint8_t*>(v_pool);
+  int bshift = 0;  // (block_size is a power of two)
+  while ((1 << bshift) < block_size) ++bshift;
   cudaError_t e;
   if (dtype == GQA_BF16)
-    e = launch_pdl(kv_read_fp8_kernel<__nv_bfloat16>, grid, kThreads, st, kp, vp, k_scale, v_scale,
+    e = launch_pdl(kv_read_fp8_kernel<__nv_bfloat16>, grid, kReadThreads, st, kp, vp, k_scale, v_scale,
                    block_table, seq_lens, static_cast<__nv_bfloat16*>(k_cache),
-                   static_cast<__nv_bfloat16*>(v_cache), g, d_k, d_v, block_size, max_blocks,
+                   static_cast<__nv_bfloat16*>(v_cache), g, d_k, d_v, bshift, max_blocks,
                    num_blocks, cap, status);
   else if (dtype == GQA_F16)
-    e = launch_pdl(kv_read_fp8_kernel<__half>, grid, kThreads, st, kp, vp, k_scale, v_scale,
+    e = launch_pdl(kv_read_fp8_kernel<__half>, grid, kReadThreads, st, kp, vp, k_scale, v_scale,
                    block_table, seq_lens, static_cast<__half*>(k_cache),
-                   static_cast<__half*>(v_cache), g, d_k, d_v, block_size, max_blocks, num_blocks,
+                   static_cast<__half*>(v_cache), g, d_k, d_v, bshift, max_blocks, num_blocks,
                    cap, status);
   else
-    e = launch_pdl(kv_read_fp8_kernel<float>, grid, kThreads, st, kp, vp, k_scale, v_scale,
+    e = launch_pdl(kv_read_fp8_kernel<float>, grid, kReadThreads, st, kp, vp, k_scale, v_scale,
                    block_table, seq_lens, static_cast<float*>(k_cache),
-                   static_cast<float*>(v_cache), g, d_k, d_v, block_size, max_blocks, num_blocks,
+                   static_cast<float*>(v_cache), g, d_k, d_v, bshift, max_blocks, num_blocks,
                    cap, status);
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }

@@ -1,6 +1,6 @@
 // serve_device.cuh - device-side helpers of the kernels around the decode
 // step (rotation and append, 8-bit cache, chunk attention): packed tokens,
-// 8-element row pieces, the e4m3 conversions, wide tensor-memory accesses.
+// row pieces, the e4m3 conversions, wide tensor-memory accesses.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -51,17 +51,17 @@ __device__ __forceinline__ void report_bad_packed(const int* cu, const int* lens
 }
 
 // ---------------------------------------------------------------------------
-// eight consecutive elements of a row
+// four consecutive elements of a row (8 bytes of a 16-bit type, 16 of fp32)
 // ---------------------------------------------------------------------------
 template <typename T>
-struct Piece8 {  // 16-bit types: one 16-byte access
-  uint4 raw;
-  __device__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ void zero() { raw = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+struct Piece4 {
+  uint2 raw;
+  __device__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ void zero() { raw = make_uint2(0u, 0u); }
+  __device__ void get(float* x) const {
+    const uint32_t w[2] = {raw.x, raw.y};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       if constexpr (Half16<T>::kBf16) {
         x[2 * k] = __uint_as_float(w[k] << 16);
         x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
@@ -72,38 +72,39 @@ struct Piece8 {  // 16-bit types: one 16-byte access
       }
     }
   }
-  __device__ static void store(T* p, const float (&x)[8]) {
-    uint4 v;
-    v.x = Half16<T>::pack2(x[0], x[1]);
-    v.y = Half16<T>::pack2(x[2], x[3]);
-    v.z = Half16<T>::pack2(x[4], x[5]);
-    v.w = Half16<T>::pack2(x[6], x[7]);
-    *reinterpret_cast<uint4*>(p) = v;
+  __device__ static void store(T* p, const float* x) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(Half16<T>::pack2(x[0], x[1]), Half16<T>::pack2(x[2], x[3]));
   }
-  __device__ void copy_to(T* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+  __device__ void copy_to(T* p) const { *reinterpret_cast<uint2*>(p) = raw; }
 };
 
 template <>
-struct Piece8<float> {
-  float4 a, b;
-  __device__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+struct Piece4<float> {
+  float4 raw;
+  __device__ void load(const float* p) { raw = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ void zero() { raw = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ void get(float* x) const { x[0] = raw.x, x[1] = raw.y, x[2] = raw.z, x[3] = raw.w; }
+  __device__ static void store(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   }
-  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ void get(float (&x)[8]) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
-  __device__ static void store(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  }
-  __device__ void copy_to(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
+  __device__ void copy_to(float* p) const { *reinterpret_cast<float4*>(p) = raw; }
 };
+
+// eight fp32 values as consecutive elements of T
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  Piece4<float>::store(p, x);
+  Piece4<float>::store(p + 4, x + 4);
+}
+template <typename T16>
+__device__ __forceinline__ void store8(T16* p, const float (&x)[8]) {
+  uint4 v;
+  v.x = Half16<T16>::pack2(x[0], x[1]);
+  v.y = Half16<T16>::pack2(x[2], x[3]);
+  v.z = Half16<T16>::pack2(x[4], x[5]);
+  v.w = Half16<T16>::pack2(x[6], x[7]);
+  *reinterpret_cast<uint4*>(p) = v;
+}
 
 // ---------------------------------------------------------------------------
 // e4m3

@@ -493,7 +493,7 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  *   [num_blocks, g, block_size, d_k] and v_pool [.., d_v] hold e4m3 values,
  *   k_scale and v_scale [num_blocks, g, block_size] fp32 one scale per row.
  *   A row x (in fp32, after norm and rotation) is stored as scale =
- *   max|x| / 448 and round-to-nearest e4m3(x / scale); a row of zeros has
+ *   max|x| / 448 and round-to-nearest e4m3(x * (448 / max|x|)); a row of zeros has
  *   scale 0.  d_k and d_v multiples of 16.  Rows that hold infinities or
  *   NaN are stored as rows that hold NaN.  The scales are 16-byte aligned for
  *   gqa_decode_attn_fp8_paged.
