@@ -22,17 +22,17 @@
 //   warps 0-3  softmax of side A, output; thread = query row = TMEM lane
 //   warps 4-7  the same for side B
 //   warp 8     one lane issues every product
-//   warp 9     TMA: the sides' query rows once per unit, K and V tiles into a
+//   warp 10    TMA: the sides' query rows once per unit, K and V tiles into a
 //              ring (64-column boxes, 128-byte swizzle)
-//   (warps 10 and 11 idle: registers are dealt out by warpgroups)
+//   (warps 9 and 11 idle: registers are dealt out by warpgroups)
 // TMEM columns: S_A 0-127, S_B 128-255 (each holds P, two 16-bit values a
 // column, once its S has been read), O_A 256.., O_B 384...
 //
-// Work split.  A unit has as many tiles as its last token sees.  All units'
-// tiles are laid end to end, and each CTA takes an equal run of them, so the
-// triangle of a causal prompt, ragged batches and a few long sequences all
-// spread evenly; a run's ends snap to a unit's edge when it is close.  A unit
-// cut by a run's end leaves partial results (row maximum, sum, unnormalised
+// Work split.  A unit has as many tiles as its last token sees.  All units are
+// laid end to end, and each CTA takes a run of equal work, so the triangle of
+// a causal prompt, ragged batches and a few long sequences all spread evenly;
+// a run's ends snap to a unit's edge when it is close.  A unit cut by a run's
+// end leaves partial results (row maximum, sum, unnormalised
 // output, all fp32) in the workspace, and a second small kernel joins them.
 //
 // Rows >= L_i: masked out of S, their V rows zeroed in shared memory.
@@ -62,6 +62,7 @@ constexpr int kSegBytes = 48;
 // a row's reference maximum is raised when the new one is this much larger
 // (base 2)
 constexpr float kRaise = 8.f;
+constexpr int kParts = 1;         // parts in which a tile's P is handed over
 
 template <int DK, int DV>
 struct ChunkCfg {
@@ -72,7 +73,7 @@ struct ChunkCfg {
   static constexpr int OFF_RING = 2 * Q_BYTES;
   static constexpr int OFF_BAR = OFF_RING + NS * SLOT;
   static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
-                       S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
+                       S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 4,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
                        DRAIN = V_EDGE + 1, NBAR = DRAIN + 1;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
@@ -97,29 +98,6 @@ struct ChunkParams {
   long long budget;
 };
 
-// sum over k < n of floor((a k + b) / 128), by Euclid's reduction
-__device__ __forceinline__ long long floor_sum128(long long n, int a, long long b) {
-  long long m = 128, aa = a, ans = 0;
-  while (n > 0) {
-    if (aa >= m) {
-      ans += (n - 1) * n / 2 * (aa / m);
-      aa %= m;
-    }
-    if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
-    }
-    const long long y = aa * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const long long tmp = m;
-    m = aa;
-    aa = tmp;
-  }
-  return ans;
-}
-
 struct ChunkSeg {
   int i, j;        // sequence, KV head
   int t0;          // packed row of the unit's first token
@@ -139,16 +117,29 @@ struct ChunkSeg {
 
 static_assert(sizeof(ChunkSeg) <= kSegBytes, "segment ring");
 
-// The run of tiles of one CTA, cut into segments of units.  The TMA warp walks
+// The run of work of one CTA, cut into segments of units.  The TMA warp walks
 // (warp-uniform values) and announces each segment to the others through a
 // ring in shared memory.
+//
+// Work is counted in cached positions: a unit's is the position behind its
+// last token plus kUnitCost for what a unit costs however short it is (query
+// rows in, first logits, output), so the units of a sequence form an
+// arithmetic progression and sums of them a closed form.  All units are laid
+// end to end (sequences, KV heads, blocks of query rows) and run c begins at
+// c * W / nc, moved to a tile's edge, or to the unit's when that is near.
+constexpr int kUnitCost = 256;
+
+struct ChunkPos {  // a place in the order of all tiles
+  int i, j, qt, lt;
+};
+
 struct ChunkWalk {
   const int *cu, *lens;
   int b, g, tq2, total;
   long long cap;
-  long long pos, end;
-  int i, j, qt, lt;       // cursor
-  int t0, n, L, nqt;      // of sequence i
+  ChunkPos at, end;
+  int t0, n, L;  // of sequence at.i
+  bool more;
 
   __device__ bool seq(int k, int& a0, int& nn, int& Lk) const {
     a0 = nn = Lk = 0;
@@ -160,44 +151,25 @@ struct ChunkWalk {
     nn = a1 - a0;
     return nn > 0;
   }
-  // tiles of the first q units (q <= nqt) of a sequence
-  __device__ long long prefix(int q, int nn, int Lk, int nq) const {
-    const int full = min(q, nq - 1);  // units that hold tq2 tokens
-    long long s = floor_sum128(full, tq2, static_cast<long long>(Lk) - nn + tq2 + kN - 1);
-    if (q == nq) s += (Lk + kN - 1) / kN;
-    return s;
-  }
   __device__ int units(int nn) const { return (nn + tq2 - 1) / tq2; }
-  __device__ int unit_tiles(int q) const {
-    const int ext = (q == nqt - 1) ? L : L - n + (q + 1) * tq2;
-    return (ext + kN - 1) / kN;
+  // work of the first q units of a sequence (its last unit counted as full)
+  __device__ long long prefix(long long q, int nn, int Lk) const {
+    return q * (Lk - nn + kUnitCost) + tq2 * (q * (q + 1) / 2);
+  }
+  __device__ static int tiles(int q, int nn, int Lk, int tq2) {
+    const long long ext = min(static_cast<long long>(Lk),
+                              static_cast<long long>(Lk) - nn + (q + 1ll) * tq2);
+    return static_cast<int>((ext + kN - 1) / kN);
   }
 
-  __device__ long long total_tiles() const {
-    long long acc = 0;
-    for (int k = threadIdx.x & 31; k < b; k += 32) {
-      int a0, nn, Lk;
-      if (seq(k, a0, nn, Lk)) {
-        const int nq = units(nn);
-        acc += prefix(nq, nn, Lk, nq);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    return acc * g;
-  }
-
-  // put the cursor on global tile x (0 <= x < W)
-  __device__ void locate(long long x) {
+  // the place of work x (0 <= x < W): every lane gets it; also t0, n, L
+  __device__ ChunkPos locate(long long x, int near) {
     const int lane = threadIdx.x & 31;
     long long carry = 0;
     for (int base = 0; base < b; base += 32) {
       int a0, nn, Lk;
       long long f = 0;
-      if (seq(base + lane, a0, nn, Lk)) {
-        const int nq = units(nn);
-        f = prefix(nq, nn, Lk, nq);
-      }
+      if (seq(base + lane, a0, nn, Lk)) f = prefix(units(nn), nn, Lk);
       long long incl = f * g;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -208,44 +180,32 @@ struct ChunkWalk {
       const unsigned hit = __ballot_sync(0xffffffffu, f > 0 && lo <= x && x < hi);
       if (hit) {
         const int src = __ffs(hit) - 1;
-        i = base + src;
         t0 = __shfl_sync(0xffffffffu, a0, src);
         n = __shfl_sync(0xffffffffu, nn, src);
         L = __shfl_sync(0xffffffffu, Lk, src);
-        nqt = units(n);
         const long long off = x - __shfl_sync(0xffffffffu, lo, src);
         const long long fs = __shfl_sync(0xffffffffu, f, src);
-        j = static_cast<int>(off / fs);
-        const long long rem = off - j * fs;
-        // the last unit q with prefix(q) <= rem: 32 probes a round
-        int q0 = 0, cnt = nqt;
-        while (cnt > 1) {
-          const int step = (cnt + 31) >> 5;
-          const int q = q0 + lane * step;
-          const bool le = lane * step < cnt && prefix(q, n, L, nqt) <= rem;
-          const int m = __popc(__ballot_sync(0xffffffffu, le));  // >= 1
-          q0 += (m - 1) * step;
-          cnt = min(step, cnt - (m - 1) * step);
-        }
-        qt = q0;
-        lt = static_cast<int>(rem - prefix(q0, n, L, nqt));
-        return;
+        ChunkPos r;
+        r.i = base + src;
+        r.j = static_cast<int>(off / fs);
+        const long long rem = off - r.j * fs;
+        // the last unit q with prefix(q) <= rem: the root of the quadratic,
+        // put right by steps of one
+        const int nu = units(n);
+        const double c1 = static_cast<double>(L - n) + kUnitCost + 0.5 * tq2;
+        int q = static_cast<int>((sqrt(c1 * c1 + 2.0 * tq2 * static_cast<double>(rem)) - c1) / tq2);
+        q = min(max(q, 0), nu - 1);
+        while (q > 0 && prefix(q, n, L) > rem) --q;
+        while (q + 1 < nu && prefix(q + 1, n, L) <= rem) ++q;
+        r.qt = q;
+        const int ti = tiles(q, n, L, tq2);
+        const long long lt = (rem - prefix(q, n, L)) / kN;
+        r.lt = lt <= near ? 0 : lt >= ti - near ? ti : static_cast<int>(lt);
+        return r;
       }
       carry = __shfl_sync(0xffffffffu, hi, 31);
     }
-    i = b;  // not reached for x < W
-  }
-
-  // Start of run c: c * W / nc, moved to the edge of the unit it falls into
-  // when that is at most `tol` tiles away.
-  __device__ long long run_start(int c, long long W, int nc, long long tol) {
-    const long long x = W * c / nc;
-    if (tol <= 0 || x <= 0 || x >= W) return x;
-    locate(x);
-    if (i >= b) return x;
-    if (lt <= tol) return x - lt;
-    const int left = unit_tiles(qt) - lt;
-    return left <= tol ? x + left : x;
+    return {b, 0, 0, 0};  // not reached for x < W
   }
 
   __device__ void init(const ChunkParams& p, int c, int nc) {
@@ -256,46 +216,59 @@ struct ChunkWalk {
     tq2 = 2 * p.tq;
     total = p.total;
     cap = p.cap;
-    pos = end = 0;
-    const long long W = total_tiles();
-    if (W == 0) return;
-    // at least two tiles a run: a piece of one costs more to join than it saves
-    nc = static_cast<int>(min(static_cast<long long>(nc), (W + 1) / 2));
-    if (c >= nc) return;
-    const long long tol = W / (static_cast<long long>(nc) * 32);
-    end = run_start(c + 1, W, nc, tol);
-    pos = run_start(c, W, nc, tol);
-    if (pos < end) locate(pos);
+    more = false;
+    long long W = 0;
+    for (int k = threadIdx.x & 31; k < b; k += 32) {
+      int a0, nn, Lk;
+      if (seq(k, a0, nn, Lk)) W += prefix(units(nn), nn, Lk);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+    W *= g;
+    // a run is worth at least the work of a unit and two tiles: less costs
+    // more to join than it saves
+    nc = static_cast<int>(min(static_cast<long long>(nc), W / (kUnitCost + 2 * kN) + 1));
+    if (W == 0 || c >= nc) return;
+    const int near = static_cast<int>(W / nc / (32 * kN));
+    end = c + 1 < nc ? locate(W * (c + 1) / nc, near) : ChunkPos{b, 0, 0, 0};
+    at = locate(W * c / nc, near);
+    if (c == 0) at.lt = 0;
+    more = true;
+    // (a place at its unit's last tile's end is the next unit's start)
+    if (at.i < b && at.lt >= tiles(at.qt, n, L, tq2)) advance();
   }
 
-  __device__ bool next(ChunkSeg& s, int tq) {
-    if (pos >= end || i >= b) return false;
-    const int ti = unit_tiles(qt);
-    const long long left = end - pos;
-    s.i = i;
-    s.j = j;
-    s.t0 = t0 + qt * tq2;
-    s.pos0 = L - n + qt * tq2;
-    s.ntok = min(n - qt * tq2, tq2);
+  __device__ void advance() {  // to the next unit's start
+    at.lt = 0;
+    if (++at.qt < units(n)) return;
+    at.qt = 0;
+    if (++at.j < g) return;
+    at.j = 0;
+    do {
+      ++at.i;
+    } while (at.i < b && !seq(at.i, t0, n, L));
+  }
+
+  __device__ bool next(ChunkSeg& s) {
+    if (!more || at.i >= b) return false;
+    const int ti = tiles(at.qt, n, L, tq2);
+    const bool last = at.i == end.i && at.j == end.j && at.qt == end.qt;
+    const bool past = at.i > end.i || (at.i == end.i && (at.j > end.j ||
+                                       (at.j == end.j && at.qt > end.qt)));
+    if (past || (last && end.lt <= at.lt)) return false;
+    s.i = at.i;
+    s.j = at.j;
+    s.t0 = t0 + at.qt * tq2;
+    s.pos0 = L - n + at.qt * tq2;
+    s.ntok = min(n - at.qt * tq2, tq2);
     s.L = L;
     s.ti = ti;
-    s.lt0 = lt;
-    s.lt1 = (ti - lt <= left) ? ti : lt + static_cast<int>(left);
-    pos += s.lt1 - lt;
-    lt = s.lt1;
-    if (lt == ti && pos < end) {
-      lt = 0;
-      if (++qt == nqt) {
-        qt = 0;
-        if (++j == g) {
-          j = 0;
-          do {
-            ++i;
-          } while (i < b && !seq(i, t0, n, L));
-          nqt = units(n);
-        }
-      }
-    }
+    s.lt0 = at.lt;
+    s.lt1 = last ? end.lt : ti;
+    if (last)
+      more = false;
+    else
+      advance();
     return true;
   }
 };
@@ -323,13 +296,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < C::NBAR; ++k)
-      mbar_init(BAR(k), (k == C::P_READY || k == C::P_READY + 1)              ? 4
-                        : (k >= C::SEG_EMPTY && k < C::SEG_EMPTY + kSegs) ? 9
+      mbar_init(BAR(k), (k >= C::P_READY && k < C::O_DONE)                ? 4   // a side's warps
+                        : (k >= C::SEG_EMPTY && k < C::SEG_EMPTY + kSegs) ? 9  // all its readers
                                                                           : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == 10 && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
@@ -339,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait_then_release();
-  if (warp == 9 && blockIdx.x == 0)
+  if (warp == 11 && blockIdx.x == 0)
     report_bad_packed(p.cu, p.lens, p.b, p.total, p.cap, p.status);
 
   auto seg_at = [&](uint32_t k) -> ChunkSeg* {
@@ -349,9 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return mbar_wait(BAR(k), phase & 1u, abort_flag, p.status, p.budget);
   };
 
-  if (warp >= 10) {
+  if (warp == 9 || warp == 11) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-  } else if (warp == 9) {
+  } else if (warp == 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // ============================ TMA producer ============================
     ChunkWalk w;
@@ -374,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ++kn;
     };
-    while (ok && w.next(seg, p.tq)) {
+    while (ok && w.next(seg)) {
       announce(seg);
       const int* trow =
           PAGED ? p.table + static_cast<size_t>(seg.i) * p.max_blocks : nullptr;
@@ -473,81 +446,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // ============================ MMA issuer ==============================
+    // The sides by turns: P.V of the side's last tile, then S of its next
+    // (of the next unit's first at a unit's end).  One thread issues both
+    // sides' products, so each side's run back to back; with a thread per
+    // side they interleave and both sides wait longer.
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_bf16(kM, kN, 0, 0, kBf16);   // both K-major
       constexpr uint32_t kIdescO = idesc_bf16(kM, DV, 0, 1, kBf16);   // V: MN-major
-      uint32_t slot_n = 0;      // ring position of the segment's first K
-      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};
+      uint32_t slot_n = 0;  // ring position of the segment's K_0
+      uint32_t kn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
       bool ok = true;
       auto slot_full = [&](uint32_t x) -> bool {
         return wait(C::FULL + x % C::NS, (x / C::NS) & 1);
       };
-      auto issue_s = [&](int side, uint32_t x) {
-        const uint64_t a0 = smem_desc(s_base + side * C::Q_BYTES, 16, 1024, SWZ_128B);
+      // the next segment's length and the tiles of each side; 0: no more
+      auto next_seg = [&](int (&nt)[2]) -> int {
+        ok = ok && wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1);
+        if (!ok) return 0;
+        const ChunkSeg seg = *seg_at(kn);
+        mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+        ++kn;
+        nt[0] = seg.side_tiles(0, p.tq);
+        nt[1] = seg.side_tiles(1, p.tq);
+        return seg.lt1 - seg.lt0;
+      };
+      // S of side s with the K tile at ring position x
+      auto issue_s = [&](int s, uint32_t x, bool first, bool last) {
+        if (first) {
+          ok = ok && wait(C::Q_FULL + s, qn[s] & 1);
+          ++qn[s];
+        }
+        ok = ok && slot_full(x);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t a0 = smem_desc(s_base + s * C::Q_BYTES, 16, 1024, SWZ_128B);
         const uint64_t b0 =
             smem_desc(s_base + C::OFF_RING + (x % C::NS) * C::SLOT, 16, 1024, SWZ_128B);
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k) {
           const uint32_t o = ((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4;
-          mma_bf16(tmem + C::T_S + side * 128, a0 + o, b0 + o, kIdescS, k > 0 ? 1u : 0u);
+          mma_bf16(tmem + C::T_S + s * 128, a0 + o, b0 + o, kIdescS, k > 0 ? 1u : 0u);
         }
-        mma_commit(BAR(C::S_FULL + side));
+        mma_commit(BAR(C::S_FULL + s));
+        if (last) mma_commit(BAR(C::Q_EMPTY + s));
       };
-      auto issue_o = [&](int side, uint32_t x, bool first) {
+      auto issue_o = [&](int s, uint32_t x, bool first, bool last) {
         const uint64_t b0 =
             smem_desc(s_base + C::OFF_RING + (x % C::NS) * C::SLOT, kN * 128, 1024, SWZ_128B);
 #pragma unroll
-        for (int k = 0; k < kN / 16; ++k)
-          mma_16_ts(tmem + C::T_O + side * 128, tmem + C::T_S + side * 128 + 8 * k,
-                    b0 + k * (2048 >> 4), kIdescO, (first && k == 0) ? 0u : 1u);
-      };
-      for (uint32_t kn = 0;; ++kn) {
-        ok = ok && wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1);
-        if (!ok) break;
-        const ChunkSeg seg = *seg_at(kn);
-        mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
-        if (seg.lt1 == seg.lt0) break;
-        const int nt[2] = {seg.side_tiles(0, p.tq), seg.side_tiles(1, p.tq)};
-        const int T = seg.lt1 - seg.lt0;
-        // ring: K_0, V_0, K_1, V_1, ...
-        auto kx = [&](int t) -> uint32_t { return slot_n + 2 * t; };
-        auto vx = [&](int t) -> uint32_t { return slot_n + 2 * t + 1; };
-        ok = slot_full(kx(0));
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (nt[s] == 0) continue;
-          ok = wait(C::Q_FULL + s, qn[s] & 1);
-          ++qn[s];
-          if (!ok) break;
+        for (int hf = 0; hf < kParts; ++hf) {
+          ok = ok && wait(C::P_READY + 2 * s + hf, pn[s] & 1);
+          if (hf == 0) ok = ok && slot_full(x);
+          if (!ok) return;
           tc_fence_after();
-          issue_s(s, kx(0));
+#pragma unroll
+          for (int k = 8 / kParts * hf; k < 8 / kParts * (hf + 1); ++k)
+            mma_16_ts(tmem + C::T_O + s * 128, tmem + C::T_S + s * 128 + 8 * k,
+                      b0 + k * (2048 >> 4), kIdescO, (first && k == 0) ? 0u : 1u);
         }
-        if (!ok) break;
-        mma_commit(BAR(C::EMPTY + kx(0) % C::NS));
-        for (int t = 0; t < T && ok; ++t) {
+        ++pn[s];
+        if (last) mma_commit(BAR(C::O_DONE + s));
+      };
+      auto give_back = [&](uint32_t x) {  // (its copy has landed, used or not)
+        ok = ok && slot_full(x);
+        if (ok) mma_commit(BAR(C::EMPTY + x % C::NS));
+      };
+      int nt[2], nx[2];
+      int T = next_seg(nt);
+      if (T > 0) {
+        for (int s = 0; s < 2; ++s)
+          if (nt[s] > 0) issue_s(s, 0, true, nt[s] == 1);
+        give_back(0);
+      }
+      while (T > 0 && ok) {
+        int Tn = 0;
+        for (int t = 1; t <= T && ok; ++t) {
+          const uint32_t v = slot_n + 2 * t - 1, k = slot_n + 2 * t;
+          if (t == T) Tn = next_seg(nx);
           for (int s = 0; s < 2 && ok; ++s) {
-            if (t >= nt[s]) continue;
-            ok = wait(C::P_READY + s, pn[s] & 1) && slot_full(vx(t));
-            ++pn[s];
-            if (!ok) break;
-            tc_fence_after();
-            issue_o(s, vx(t), t == 0);
-            if (t + 1 < nt[s]) {
-              ok = slot_full(kx(t + 1));
-              if (!ok) break;
-              issue_s(s, kx(t + 1));
-            } else {
-              mma_commit(BAR(C::O_DONE + s));
-              mma_commit(BAR(C::Q_EMPTY + s));
+            if (t <= nt[s]) issue_o(s, v, t == 1, t == nt[s]);
+            if (t < T) {
+              if (t < nt[s]) issue_s(s, k, false, t == nt[s] - 1);
+            } else if (Tn > 0 && nx[s] > 0) {
+              issue_s(s, k, true, nx[s] == 1);
             }
           }
-          if (!ok) break;
-          // (a tile that no side needs any more is waited for all the same,
-          // so that its slot is not handed back while its copy is in flight)
-          ok = slot_full(vx(t)) && (t + 1 >= T || slot_full(kx(t + 1)));
-          mma_commit(BAR(C::EMPTY + vx(t) % C::NS));
-          if (t + 1 < T) mma_commit(BAR(C::EMPTY + kx(t + 1) % C::NS));
+          give_back(v);
+          if (t < T || Tn > 0) give_back(k);
         }
         slot_n += 2 * T;
+        T = Tn;
+        nt[0] = nx[0];
+        nt[1] = nx[1];
       }
       // every product has to be finished before tensor memory is released
       mma_commit(BAR(C::DRAIN));
@@ -616,11 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < kN; ++e)
             if (e > lim) x[e] = -INFINITY;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int e = 0; e < kN; e += 4)
+        for (int e = 4; e < kN; e += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[e + k]);
+          for (int k = 0; k < 4; ++k)
+            mx[k] = e + 4 < kN ? max3(mx[k], x[e + k], x[e + 4 + k]) : fmaxf(mx[k], x[e + k]);
         const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         // S_FULL also covers the products issued before it: O is complete
         // up to the last tile
@@ -642,25 +633,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m * sl;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // P in parts: the products over one go out while the next is worked on
 #pragma unroll
-        for (int c = 0; c < kN / 64; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t u[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float p0 = ex2(fmaf(x[64 * c + 2 * e], sl, off));
-            const float p1 = ex2(fmaf(x[64 * c + 2 * e + 1], sl, off));
-            sum[(2 * e) & 3] += p0;
-            sum[(2 * e + 1) & 3] += p1;
-            u[e] = Half16<T16>::pack2(p0, p1);
+            float2 y = fma2(make_float2(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]), sl2, off2);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum[e & 1] = add2(sum[e & 1], y);
+            u[e] = Half16<T16>::pack2(y.x, y.y);
           }
           tmem_st32(tS + 32 * c, u);
+          if (c == 1 || kParts == 2) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * side + (kParts == 2 ? c : 0)));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
       if (nt > 0) {
