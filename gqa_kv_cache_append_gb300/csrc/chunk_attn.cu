@@ -62,7 +62,6 @@ constexpr int kSegBytes = 48;
 // a row's reference maximum is raised when the new one is this much larger
 // (base 2)
 constexpr float kRaise = 8.f;
-constexpr int kParts = 1;         // parts in which a tile's P is handed over
 
 template <int DK, int DV>
 struct ChunkCfg {
@@ -73,7 +72,7 @@ struct ChunkCfg {
   static constexpr int OFF_RING = 2 * Q_BYTES;
   static constexpr int OFF_BAR = OFF_RING + NS * SLOT;
   static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
-                       S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 4,
+                       S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
                        DRAIN = V_EDGE + 1, NBAR = DRAIN + 1;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
@@ -292,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto BAR = [&](int k) -> uint32_t { return s_base + C::OFF_BAR + 8u * k; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (broadcast, so that what depends on it is known to be uniform)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < C::NBAR; ++k)
@@ -310,7 +310,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) tmem_alloc(smem_u32(tmem_slot), 512);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // (all of tensor memory is allocated, so it starts at address 0)
+  constexpr uint32_t tmem = 0;
+  if (*tmem_slot != tmem) {  // never seen
+    if (threadIdx.x == 0) {
+      atomicOr(p.status, GQA_DEV_INTERNAL);
+      *abort_flag = 1;
+    }
+  }
   pdl_wait_then_release();
   if (warp == 11 && blockIdx.x == 0)
     report_bad_packed(p.cu, p.lens, p.b, p.total, p.cap, p.status);
@@ -447,99 +454,124 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // ============================ MMA issuer ==============================
     // The sides by turns: P.V of the side's last tile, then S of its next
-    // (of the next unit's first at a unit's end).  One thread issues both
-    // sides' products, so each side's run back to back; with a thread per
-    // side they interleave and both sides wait longer.
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_bf16(kM, kN, 0, 0, kBf16);   // both K-major
-      constexpr uint32_t kIdescO = idesc_bf16(kM, DV, 0, 1, kBf16);   // V: MN-major
-      uint32_t slot_n = 0;  // ring position of the segment's K_0
-      uint32_t kn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
-      bool ok = true;
-      auto slot_full = [&](uint32_t x) -> bool {
-        return wait(C::FULL + x % C::NS, (x / C::NS) & 1);
-      };
-      // the next segment's length and the tiles of each side; 0: no more
-      auto next_seg = [&](int (&nt)[2]) -> int {
-        ok = ok && wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1);
-        if (!ok) return 0;
-        const ChunkSeg seg = *seg_at(kn);
-        mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
-        ++kn;
-        nt[0] = seg.side_tiles(0, p.tq);
-        nt[1] = seg.side_tiles(1, p.tq);
-        return seg.lt1 - seg.lt0;
-      };
-      // S of side s with the K tile at ring position x
-      auto issue_s = [&](int s, uint32_t x, bool first, bool last) {
-        if (first) {
-          ok = ok && wait(C::Q_FULL + s, qn[s] & 1);
-          ++qn[s];
+    // (of the next unit's first at a unit's end).  One warp issues both sides'
+    // products, so each side's run back to back; with an issuer per side they
+    // interleave and both sides wait longer.  The whole warp walks through
+    // this code with warp-uniform values and one elected lane issues: from a
+    // single lane's branch the operands take a detour into the uniform
+    // registers that costs as long as a product runs.
+    constexpr uint32_t kIdescS = idesc_bf16(kM, kN, 0, 0, kBf16);   // both K-major
+    constexpr uint32_t kIdescO = idesc_bf16(kM, DV, 0, 1, kBf16);   // V: MN-major
+    const uint64_t q0 = smem_desc(s_base, 16, 1024, SWZ_128B);
+    const uint64_t k0 = smem_desc(s_base + C::OFF_RING, 16, 1024, SWZ_128B);
+    const uint64_t v0 = smem_desc(s_base + C::OFF_RING, kN * 128, 1024, SWZ_128B);
+    struct Ring {  // a ring position: slot and phase
+      uint32_t slot = 0, phase = 0;
+      __device__ Ring next() const {
+        Ring r = *this;
+        if (++r.slot == C::NS) {
+          r.slot = 0;
+          r.phase ^= 1;
         }
-        ok = ok && slot_full(x);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t a0 = smem_desc(s_base + s * C::Q_BYTES, 16, 1024, SWZ_128B);
-        const uint64_t b0 =
-            smem_desc(s_base + C::OFF_RING + (x % C::NS) * C::SLOT, 16, 1024, SWZ_128B);
+        return r;
+      }
+    };
+    Ring at;  // of the next tile's V (its K lies one further)
+    uint32_t kn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+    bool ok = true;
+    auto all_wait = [&](int k, uint32_t phase) {
+      ok = __all_sync(0xffffffffu, ok && wait(k, phase));
+    };
+    // the next segment's tiles, and those of each side; 0: no more
+    auto next_seg = [&](int (&nt)[2]) -> int {
+      all_wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1);
+      if (!ok) return 0;
+      const ChunkSeg seg = *seg_at(kn);
+      nt[0] = __shfl_sync(0xffffffffu, seg.side_tiles(0, p.tq), 0);
+      nt[1] = __shfl_sync(0xffffffffu, seg.side_tiles(1, p.tq), 0);
+      const int T = __shfl_sync(0xffffffffu, seg.lt1 - seg.lt0, 0);
+      if (elect_one()) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+      ++kn;
+      return T;
+    };
+    // S of side s with the K tile at ring position x
+    auto issue_s = [&](int s, Ring x, bool first, bool last) {
+      if (first) {
+        all_wait(C::Q_FULL + s, qn[s] & 1);
+        ++qn[s];
+      }
+      all_wait(C::FULL + x.slot, x.phase);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t a0 = q0 + ((s * C::Q_BYTES) >> 4);
+      const uint64_t b0 = k0 + x.slot * (C::SLOT >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k) {
           const uint32_t o = ((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4;
-          mma_bf16(tmem + C::T_S + s * 128, a0 + o, b0 + o, kIdescS, k > 0 ? 1u : 0u);
+          mma_bf16(C::T_S + s * 128, a0 + o, b0 + o, kIdescS, k > 0 ? 1u : 0u);
         }
         mma_commit(BAR(C::S_FULL + s));
         if (last) mma_commit(BAR(C::Q_EMPTY + s));
-      };
-      auto issue_o = [&](int s, uint32_t x, bool first, bool last) {
-        const uint64_t b0 =
-            smem_desc(s_base + C::OFF_RING + (x % C::NS) * C::SLOT, kN * 128, 1024, SWZ_128B);
+      }
+      __syncwarp();
+    };
+    auto issue_o = [&](int s, Ring x, bool first, bool last) {
+      const uint64_t b0 = v0 + x.slot * (C::SLOT >> 4);
+      all_wait(C::FULL + x.slot, x.phase);
+      all_wait(C::P_READY + s, pn[s] & 1);
+      ++pn[s];
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-        for (int hf = 0; hf < kParts; ++hf) {
-          ok = ok && wait(C::P_READY + 2 * s + hf, pn[s] & 1);
-          if (hf == 0) ok = ok && slot_full(x);
-          if (!ok) return;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 8 / kParts * hf; k < 8 / kParts * (hf + 1); ++k)
-            mma_16_ts(tmem + C::T_O + s * 128, tmem + C::T_S + s * 128 + 8 * k,
-                      b0 + k * (2048 >> 4), kIdescO, (first && k == 0) ? 0u : 1u);
-        }
-        ++pn[s];
+        for (int k = 0; k < kN / 16; ++k)
+          mma_16_ts(C::T_O + s * 128, C::T_S + s * 128 + 8 * k, b0 + k * (2048 >> 4), kIdescO,
+                    (first && k == 0) ? 0u : 1u);
         if (last) mma_commit(BAR(C::O_DONE + s));
-      };
-      auto give_back = [&](uint32_t x) {  // (its copy has landed, used or not)
-        ok = ok && slot_full(x);
-        if (ok) mma_commit(BAR(C::EMPTY + x % C::NS));
-      };
-      int nt[2], nx[2];
-      int T = next_seg(nt);
-      if (T > 0) {
-        for (int s = 0; s < 2; ++s)
-          if (nt[s] > 0) issue_s(s, 0, true, nt[s] == 1);
-        give_back(0);
       }
-      while (T > 0 && ok) {
-        int Tn = 0;
-        for (int t = 1; t <= T && ok; ++t) {
-          const uint32_t v = slot_n + 2 * t - 1, k = slot_n + 2 * t;
-          if (t == T) Tn = next_seg(nx);
-          for (int s = 0; s < 2 && ok; ++s) {
-            if (t <= nt[s]) issue_o(s, v, t == 1, t == nt[s]);
-            if (t < T) {
-              if (t < nt[s]) issue_s(s, k, false, t == nt[s] - 1);
-            } else if (Tn > 0 && nx[s] > 0) {
-              issue_s(s, k, true, nx[s] == 1);
-            }
+      __syncwarp();
+    };
+    auto give_back = [&](Ring x) {  // (some side has waited for its copy)
+      if (elect_one()) mma_commit(BAR(C::EMPTY + x.slot));
+      __syncwarp();
+    };
+    int nt[2], nx[2] = {0, 0};
+    int T = next_seg(nt);
+    if (T > 0) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (nt[s] > 0) issue_s(s, at, true, nt[s] == 1);
+      give_back(at);
+      at = at.next();
+    }
+    while (T > 0 && ok) {
+      int Tn = 0;
+      for (int t = 1; t <= T && ok; ++t) {
+        const Ring v = at, k = at.next();
+        if (t == T) Tn = next_seg(nx);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (t <= nt[s]) issue_o(s, v, t == 1, t == nt[s]);
+          if (t < T) {
+            if (t < nt[s]) issue_s(s, k, false, t == nt[s] - 1);
+          } else if (Tn > 0 && nx[s] > 0) {
+            issue_s(s, k, true, nx[s] == 1);
           }
-          give_back(v);
-          if (t < T || Tn > 0) give_back(k);
         }
-        slot_n += 2 * T;
-        T = Tn;
-        nt[0] = nx[0];
-        nt[1] = nx[1];
+        give_back(v);
+        at = k;
+        if (t < T || Tn > 0) {
+          give_back(k);
+          at = k.next();
+        }
       }
-      // every product has to be finished before tensor memory is released
+      T = Tn;
+      nt[0] = nx[0];
+      nt[1] = nx[1];
+    }
+    // every product has to be finished before tensor memory is released
+    if (elect_one()) {
       mma_commit(BAR(C::DRAIN));
       const long long t0 = clock64();
       while (!mbar_try_wait(BAR(C::DRAIN), 0) && clock64() - t0 < p.budget) {
@@ -635,7 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float off = m == -INFINITY ? 0.f : -m * sl;
         const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // P in parts: the products over one go out while the next is worked on
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t u[32];
@@ -648,13 +679,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             u[e] = Half16<T16>::pack2(y.x, y.y);
           }
           tmem_st32(tS + 32 * c, u);
-          if (c == 1 || kParts == 2) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::P_READY + 2 * side + (kParts == 2 ? c : 0)));
-          }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
@@ -719,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 8) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*tmem_slot, 512);
   }
 }
 

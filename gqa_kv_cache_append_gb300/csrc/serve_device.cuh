@@ -9,6 +9,17 @@
 
 namespace gqa {
 
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---------------------------------------------------------------------------
 // packed tokens: sequence i's new tokens are rows cu[i] .. cu[i + 1] - 1
 // ---------------------------------------------------------------------------
@@ -194,9 +205,6 @@ __device__ __forceinline__ void mma_16_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 // fp32 arithmetic on pairs, and the largest of three
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-#ifdef NOPACK
-  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
-#endif
   float2 d;
   asm("{\n\t.reg .b64 a, b, c, d;\n\t"
       "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
@@ -208,9 +216,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
-#ifdef NOPACK
-  return make_float2(a.x + b.x, a.y + b.y);
-#endif
   float2 d;
   asm("{\n\t.reg .b64 a, b, d;\n\t"
       "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
