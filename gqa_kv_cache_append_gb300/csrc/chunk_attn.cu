@@ -74,9 +74,10 @@ struct ChunkCfg {
   static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
                        S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
-                       DRAIN = V_EDGE + 1, NBAR = DRAIN + 1;
+                       TWIN = V_EDGE + 1, DRAIN = TWIN + 2, NBAR = DRAIN + 1;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
-  static constexpr int OFF_MISC = OFF_SEG + kSegs * kSegBytes;
+  static constexpr int OFF_ML = OFF_SEG + kSegs * kSegBytes;  // float2 [2][kM]: twins' maxima, sums
+  static constexpr int OFF_MISC = OFF_ML + 2 * kM * 8;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr int T_S = 0, T_O = 256;  // TMEM columns, 128 to a side
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -105,10 +106,13 @@ struct ChunkSeg {
   int L;
   int lt0, lt1;    // tiles of the unit taken here
   int ti;          // tiles of the unit
-  // tiles each side needs of [lt0, lt1)
+  // A unit whose rows fit side A alone runs as twins: both sides hold the same
+  // rows and take the tiles by turns, and their results are joined at the end.
+  __device__ bool twin(int tq) const { return ntok <= tq; }
+  // tiles that each side works on of [lt0, lt1)
   __device__ int side_tiles(int side, int tq) const {
+    if (twin(tq)) return (lt1 - lt0 + 1 - side) >> 1;
     const int nt = min(ntok - side * tq, tq);
-    if (nt <= 0) return 0;
     const int ext = pos0 + side * tq + nt;
     return max(0, min(lt1, (ext + kN - 1) / kN) - lt0);
   }
@@ -191,8 +195,9 @@ struct ChunkWalk {
         // the last unit q with prefix(q) <= rem: the root of the quadratic,
         // put right by steps of one
         const int nu = units(n);
-        const double c1 = static_cast<double>(L - n) + kUnitCost + 0.5 * tq2;
-        int q = static_cast<int>((sqrt(c1 * c1 + 2.0 * tq2 * static_cast<double>(rem)) - c1) / tq2);
+        const float c1 = static_cast<float>(L - n) + (kUnitCost + 0.5f * tq2);
+        const float rf = static_cast<float>(rem);
+        int q = static_cast<int>(2.f * rf / (sqrtf(c1 * c1 + 2.f * tq2 * rf) + c1));
         q = min(max(q, 0), nu - 1);
         while (q > 0 && prefix(q, n, L) > rem) --q;
         while (q + 1 < nu && prefix(q + 1, n, L) <= rem) ++q;
@@ -298,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < C::NBAR; ++k)
       mbar_init(BAR(k), (k >= C::P_READY && k < C::O_DONE)                ? 4   // a side's warps
                         : (k >= C::SEG_EMPTY && k < C::SEG_EMPTY + kSegs) ? 9  // all its readers
+                        : (k == C::TWIN || k == C::TWIN + 1)              ? 8  // both sides' warps
                                                                           : 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(BAR(C::Q_FULL + side), p.tq * p.r * DK * 2);
           for (int c = 0; c < DK / 64; ++c)
             tma_load_3d(s_base + side * C::Q_BYTES + c * (kM * 128), &tm_q, BAR(C::Q_FULL + side),
-                        64 * c, seg.j * p.r, seg.t0 + side * p.tq, pol);
+                        64 * c, seg.j * p.r, seg.t0 + (seg.twin(p.tq) ? 0 : side * p.tq), pol);
         }
         ++qn[side];
       };
@@ -476,23 +482,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         return r;
       }
     };
-    Ring at;  // of the next tile's V (its K lies one further)
+    Ring at;  // next position to be used
     uint32_t kn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
     bool ok = true;
     auto all_wait = [&](int k, uint32_t phase) {
       ok = __all_sync(0xffffffffu, ok && wait(k, phase));
     };
-    // the next segment's tiles, and those of each side; 0: no more
-    auto next_seg = [&](int (&nt)[2]) -> int {
+    // the next segment: its tiles (0: no more), and the sides'
+    struct Todo {
+      int T, nt[2];
+      bool twin;
+    };
+    auto next_seg = [&]() -> Todo {
+      Todo r = {0, {0, 0}, false};
       all_wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1);
-      if (!ok) return 0;
+      if (!ok) return r;
       const ChunkSeg seg = *seg_at(kn);
-      nt[0] = __shfl_sync(0xffffffffu, seg.side_tiles(0, p.tq), 0);
-      nt[1] = __shfl_sync(0xffffffffu, seg.side_tiles(1, p.tq), 0);
-      const int T = __shfl_sync(0xffffffffu, seg.lt1 - seg.lt0, 0);
+      r.nt[0] = __shfl_sync(0xffffffffu, seg.side_tiles(0, p.tq), 0);
+      r.nt[1] = __shfl_sync(0xffffffffu, seg.side_tiles(1, p.tq), 0);
+      r.T = __shfl_sync(0xffffffffu, seg.lt1 - seg.lt0, 0);
+      r.twin = __shfl_sync(0xffffffffu, seg.twin(p.tq) ? 1 : 0, 0) != 0;
       if (elect_one()) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
       ++kn;
-      return T;
+      return r;
     };
     // S of side s with the K tile at ring position x
     auto issue_s = [&](int s, Ring x, bool first, bool last) {
@@ -536,39 +548,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) mma_commit(BAR(C::EMPTY + x.slot));
       __syncwarp();
     };
-    int nt[2], nx[2] = {0, 0};
-    int T = next_seg(nt);
-    if (T > 0) {
+    Todo cur = next_seg();
+    bool primed = false;  // the segment's first S are out already
+    while (cur.T > 0 && ok) {
+      if (cur.twin) {
+        // (K, V of tile t at positions 2 t, 2 t + 1; tile t is side t & 1's)
+        Ring k = at;
+        issue_s(0, k, true, cur.nt[0] == 1);
+        give_back(k);
+        if (cur.nt[1] > 0) {
+          k = at.next().next();
+          issue_s(1, k, true, cur.nt[1] == 1);
+          give_back(k);
+        }
+        for (int t = 0; t < cur.T && ok; t += 2) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (nt[s] > 0) issue_s(s, at, true, nt[s] == 1);
-      give_back(at);
-      at = at.next();
-    }
-    while (T > 0 && ok) {
-      int Tn = 0;
-      for (int t = 1; t <= T && ok; ++t) {
+          for (int s = 0; s < 2; ++s) {
+            if (t + s >= cur.T) break;
+            at = at.next();
+            issue_o(s, at, t == 0, t + s + 2 >= cur.T);
+            give_back(at);
+            at = at.next();
+            k = at.next().next();
+            if (t + s + 2 < cur.T) {
+              issue_s(s, k, false, t + s + 4 >= cur.T);
+              give_back(k);
+            }
+          }
+        }
+        cur = next_seg();
+        continue;
+      }
+      if (!primed) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (cur.nt[s] > 0) issue_s(s, at, true, cur.nt[s] == 1);
+        give_back(at);
+        at = at.next();
+      }
+      Todo nx = {0, {0, 0}, false};
+      for (int t = 1; t <= cur.T && ok; ++t) {
         const Ring v = at, k = at.next();
-        if (t == T) Tn = next_seg(nx);
+        if (t == cur.T) {
+          nx = next_seg();
+          primed = nx.T > 0 && !nx.twin;
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (t <= nt[s]) issue_o(s, v, t == 1, t == nt[s]);
-          if (t < T) {
-            if (t < nt[s]) issue_s(s, k, false, t == nt[s] - 1);
-          } else if (Tn > 0 && nx[s] > 0) {
-            issue_s(s, k, true, nx[s] == 1);
+          if (t <= cur.nt[s]) issue_o(s, v, t == 1, t == cur.nt[s]);
+          if (t < cur.T) {
+            if (t < cur.nt[s]) issue_s(s, k, false, t == cur.nt[s] - 1);
+          } else if (primed && nx.nt[s] > 0) {
+            issue_s(s, k, true, nx.nt[s] == 1);
           }
         }
         give_back(v);
         at = k;
-        if (t < T || Tn > 0) {
+        if (t < cur.T || primed) {
           give_back(k);
           at = k.next();
         }
       }
-      T = Tn;
-      nt[0] = nx[0];
-      nt[1] = nx[1];
+      cur = nx;
     }
     // every product has to be finished before tensor memory is released
     if (elect_one()) {
@@ -582,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ======================= softmax, output ==============================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int side = warp >> 2;
+    float2* const ml_sm = reinterpret_cast<float2*>(sm + C::OFF_ML);
     const int row = (warp & 3) * 32 + lane;  // query row of the side = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::T_S + side * 128;
@@ -591,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // to the logits first then
     const bool pre = !(p.scale_log2 > 0.f);
     const float sl = pre ? 1.f : p.scale_log2;
-    uint32_t sn = 0, on = 0;
+    uint32_t sn = 0, on = 0, tn = 0;
     int d_head = 0, d_tok0 = 0, d_ntok = 0, d_j = 0, d_end = 0;
     bool ok = true;
     for (uint32_t kn = 0;; ++kn) {
@@ -603,7 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seg.lt1 == seg.lt0) break;
       const int nt = seg.side_tiles(side, p.tq);
       const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
-      const int my_tok = side * p.tq + tok;  // token of the unit
+      const bool twin = seg.twin(p.tq);
+      const int tok0 = twin ? 0 : side * p.tq;
+      const int my_tok = tok0 + tok;  // token of the unit
       const bool live = tok < p.tq && my_tok < seg.ntok;
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0);
       if (seg.lt0 == 0 && !whole) {
@@ -616,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, l = 0.f;
       const int my_pos = seg.pos0 + my_tok;
-      const int first_pos = seg.pos0 + side * p.tq;  // the side's first token
+      const int first_pos = seg.pos0 + tok0;  // the side's first token
       for (int t = 0; t < nt; ++t) {
         ok = __all_sync(0xffffffffu, wait(C::S_FULL + side, sn & 1));
         ++sn;
@@ -630,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
         }
-        const int base = (seg.lt0 + t) * kN;
+        const int base = (seg.lt0 + (twin ? 2 * t + side : t)) * kN;
         if (base + kN - 1 > first_pos) {
           // positions past this row's token
           const int lim = my_pos - base;
@@ -687,53 +731,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
+      // ---- unit's end: O / l, or a partial (maximum, sum, O) ----
+      // (twins: each side joins and writes half of the columns of both)
+      const int other = twin ? seg.side_tiles(side ^ 1, p.tq) : 0;
       if (nt > 0) {
         ok = __all_sync(0xffffffffu, wait(C::O_DONE + side, on & 1));
         ++on;
         if (!ok) break;
         tc_fence_after();
       }
-      if (whole) {
-        const float inv = 1.f / l;
-        T16* dst = static_cast<T16*>(p.out) +
-                   (static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head) * DV;
-#pragma unroll
-        for (int c = 0; c < DV / 32; ++c) {
-          if (nt == 0) break;  // (a side without tokens)
-          float o[32];
+      float ms = l > 0.f ? m * sl : -INFINITY;  // base 2
+      float wo = 1.f, wt = 0.f;                 // factors of this side's O, of its twin's
+      if (twin) {
+        // (a bounded wait, as every wait here; then the other side's O is
+        // complete too)
+        ml_sm[side * kM + row] = make_float2(ms, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::TWIN));
+        ok = __all_sync(0xffffffffu, wait(C::TWIN, tn & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const float2 t2 = ml_sm[(side ^ 1) * kM + row];
+        const float mj = fmaxf(ms, t2.x);
+        const float ref = mj == -INFINITY ? 0.f : mj;
+        wo = ex2(ms - ref);
+        wt = ex2(t2.x - ref);
+        l = l * wo + t2.y * wt;
+        ms = mj;
+      }
+      const int c0 = twin ? side * (DV / 64) : 0, c1 = twin ? c0 + DV / 64 : DV / 32;
+      const float inv = 1.f / l;
+      T16* dst = static_cast<T16*>(p.out) +
+                 (static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head) * DV;
+      const size_t at = slot * p.srows + (twin ? 0 : side * kM) + row;
+      if (!whole && live && (!twin || side == 0)) {
+        p.part_ml[2 * at] = ms;
+        p.part_ml[2 * at + 1] = l;
+      }
+      for (int c = c0; c < c1; ++c) {
+        if (nt == 0 && other == 0) break;  // (a side without tokens)
+        float o[32];
+        if (nt > 0) {
           tmem_ld32(tO + 32 * c, o);
           tmem_wait_ld();
-          if (live) {
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float y[8];
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (twin) {
+          float o2[32];
+          if (other > 0) {
+            tmem_ld32(tO + (side ? -128 : 128) + 32 * c, o2);
+            tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = o[e + k] * inv;
-              store8(dst + 32 * c + e, y);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * wo + o2[e] * wt;
           }
         }
-      } else {
-        const size_t at = slot * p.srows + side * kM + row;
-        if (live) {
-          p.part_ml[2 * at] = l > 0.f ? m * sl : -INFINITY;
-          p.part_ml[2 * at + 1] = l;
-        }
+        if (!live) continue;
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < DV / 32; ++c) {
-          if (nt == 0) break;
-          float o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-          if (live) {
+          for (int e = 0; e < 32; e += 8) {
+            float y[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(p.part_o + at * DV + 32 * c + e) =
-                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int k = 0; k < 8; ++k) y[k] = o[e + k] * inv;
+            store8(dst + 32 * c + e, y);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(p.part_o + at * DV + 32 * c + e) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       tc_fence_before();
+      if (twin) {  // both O and ml_sm are free again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::TWIN + 1));
+        ok = __all_sync(0xffffffffu, wait(C::TWIN + 1, tn & 1));
+        ++tn;
+      }
     }
     if (threadIdx.x == 0) {
       int* d = p.desc + static_cast<size_t>(blockIdx.x) * kDescInts;
