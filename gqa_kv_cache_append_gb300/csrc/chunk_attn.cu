@@ -68,9 +68,11 @@ struct ChunkCfg {
   static constexpr int Q_BYTES = kM * DK * 2;  // one side
   static constexpr int SLOT = kN * (DK > DV ? DK : DV) * 2;
   // ring slots: K and V tiles by turns
-  static constexpr int NS = DK == 128 ? 5 : (DV == 128 ? 6 : 8);
+  static constexpr int NS = DK == 128 ? 4 : (DV == 128 ? 5 : 8);
   static constexpr int OFF_RING = 2 * Q_BYTES;
-  static constexpr int OFF_BAR = OFF_RING + NS * SLOT;
+  // a softmax warp's 32 rows x 32 columns on their way out
+  static constexpr int OFF_STAGE = OFF_RING + NS * SLOT;
+  static constexpr int OFF_BAR = OFF_STAGE + 8 * 32 * 128;
   static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
                        S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
@@ -125,24 +127,35 @@ static_assert(sizeof(ChunkSeg) <= kSegBytes, "segment ring");
 // ring in shared memory.
 //
 // Work is counted in cached positions: a unit's is the position behind its
-// last token plus kUnitCost for what a unit costs however short it is (query
-// rows in, first logits, output), so the units of a sequence form an
-// arithmetic progression and sums of them a closed form.  All units are laid
-// end to end (sequences, KV heads, blocks of query rows) and run c begins at
-// c * W / nc, moved to a tile's edge, or to the unit's when that is near.
+// last token (half of it where it runs as twins) plus kUnitCost for what a
+// unit costs however short it is (query rows in, first logits, output), so
+// the units of a sequence but the last form an arithmetic progression and sums
+// of them a closed form.  All units are laid end to end (sequences, KV heads,
+// blocks of query rows) and run c begins at c * W / nc, moved to a tile's
+// edge, or to the unit's when that is near.
 constexpr int kUnitCost = 256;
 
 struct ChunkPos {  // a place in the order of all tiles
   int i, j, qt, lt;
 };
 
+__device__ __forceinline__ long long div_pos(long long a, long long b) {  // a >= 0, b > 0
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return static_cast<long long>(static_cast<unsigned long long>(a) /
+                                static_cast<unsigned long long>(b));
+}
+
 struct ChunkWalk {
   const int *cu, *lens;
-  int b, g, tq2, total;
+  int b, g, tq, total;
   long long cap;
   ChunkPos at, end;
   int t0, n, L;  // of sequence at.i
   bool more;
+  // sequence `lane` of the batch's first 32: its rows and work, and the work
+  // up to its end (of one KV head)
+  int c_t0, c_n, c_L;
+  long long c_f, c_incl;
 
   __device__ bool seq(int k, int& a0, int& nn, int& Lk) const {
     a0 = nn = Lk = 0;
@@ -154,32 +167,42 @@ struct ChunkWalk {
     nn = a1 - a0;
     return nn > 0;
   }
-  __device__ int units(int nn) const { return (nn + tq2 - 1) / tq2; }
-  // work of the first q units of a sequence (its last unit counted as full)
+  __device__ int units(int nn) const { return (nn + 2 * tq - 1) / (2 * tq); }
+  // is the sequence's last unit one of twins?
+  __device__ bool last_twin(int nn, int nu) const { return nn - (nu - 1) * 2 * tq <= tq; }
+  // work of the first q units, all of them full
   __device__ long long prefix(long long q, int nn, int Lk) const {
-    return q * (Lk - nn + kUnitCost) + tq2 * (q * (q + 1) / 2);
+    return q * (Lk - nn + kUnitCost) + tq * (q * (q + 1));
   }
-  __device__ static int tiles(int q, int nn, int Lk, int tq2) {
+  __device__ long long work(int nn, int Lk) const {
+    const int nu = units(nn);
+    return last_twin(nn, nu) ? prefix(nu - 1, nn, Lk) + (Lk >> 1) + kUnitCost
+                             : prefix(nu, nn, Lk);
+  }
+  __device__ int tiles(int q, int nn, int Lk) const {
     const long long ext = min(static_cast<long long>(Lk),
-                              static_cast<long long>(Lk) - nn + (q + 1ll) * tq2);
-    return static_cast<int>((ext + kN - 1) / kN);
+                              static_cast<long long>(Lk) - nn + (q + 1ll) * 2 * tq);
+    return static_cast<int>((ext + kN - 1) >> 7);
+  }
+
+  // work f of each lane's sequence, and its sum up to the lane
+  __device__ void scan(int base, int& a0, int& nn, int& Lk, long long& f, long long& incl) const {
+    f = seq(base + (threadIdx.x & 31), a0, nn, Lk) ? work(nn, Lk) : 0;
+    incl = f;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((threadIdx.x & 31) >= o) incl += y;
+    }
   }
 
   // the place of work x (0 <= x < W): every lane gets it; also t0, n, L
   __device__ ChunkPos locate(long long x, int near) {
-    const int lane = threadIdx.x & 31;
     long long carry = 0;
     for (int base = 0; base < b; base += 32) {
-      int a0, nn, Lk;
-      long long f = 0;
-      if (seq(base + lane, a0, nn, Lk)) f = prefix(units(nn), nn, Lk);
-      long long incl = f * g;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const long long hi = carry + incl, lo = hi - f * g;
+      int a0 = c_t0, nn = c_n, Lk = c_L;
+      long long f = c_f, incl = c_incl;
+      if (base > 0) scan(base, a0, nn, Lk, f, incl);
+      const long long hi = (carry + incl) * g, lo = hi - f * g;
       const unsigned hit = __ballot_sync(0xffffffffu, f > 0 && lo <= x && x < hi);
       if (hit) {
         const int src = __ffs(hit) - 1;
@@ -190,24 +213,25 @@ struct ChunkWalk {
         const long long fs = __shfl_sync(0xffffffffu, f, src);
         ChunkPos r;
         r.i = base + src;
-        r.j = static_cast<int>(off / fs);
+        r.j = static_cast<int>(div_pos(off, fs));
         const long long rem = off - r.j * fs;
         // the last unit q with prefix(q) <= rem: the root of the quadratic,
         // put right by steps of one
         const int nu = units(n);
-        const float c1 = static_cast<float>(L - n) + (kUnitCost + 0.5f * tq2);
+        const float c1 = static_cast<float>(L - n) + (kUnitCost + tq);
         const float rf = static_cast<float>(rem);
-        int q = static_cast<int>(2.f * rf / (sqrtf(c1 * c1 + 2.f * tq2 * rf) + c1));
+        int q = static_cast<int>(2.f * rf / (sqrtf(c1 * c1 + 4.f * tq * rf) + c1));
         q = min(max(q, 0), nu - 1);
         while (q > 0 && prefix(q, n, L) > rem) --q;
         while (q + 1 < nu && prefix(q + 1, n, L) <= rem) ++q;
         r.qt = q;
-        const int ti = tiles(q, n, L, tq2);
-        const long long lt = (rem - prefix(q, n, L)) / kN;
-        r.lt = lt <= near ? 0 : lt >= ti - near ? ti : static_cast<int>(lt);
+        const int ti = tiles(q, n, L);
+        const bool tw = q == nu - 1 && last_twin(n, nu);
+        const int lt = static_cast<int>((rem - prefix(q, n, L)) >> (tw ? 6 : 7));
+        r.lt = lt <= near ? 0 : lt >= ti - near ? ti : lt;
         return r;
       }
-      carry = __shfl_sync(0xffffffffu, hi, 31);
+      carry += __shfl_sync(0xffffffffu, incl, 31);
     }
     return {b, 0, 0, 0};  // not reached for x < W
   }
@@ -217,29 +241,32 @@ struct ChunkWalk {
     lens = p.lens;
     b = p.b;
     g = p.g;
-    tq2 = 2 * p.tq;
+    tq = p.tq;
     total = p.total;
     cap = p.cap;
     more = false;
-    long long W = 0;
-    for (int k = threadIdx.x & 31; k < b; k += 32) {
+    scan(0, c_t0, c_n, c_L, c_f, c_incl);
+    long long W = __shfl_sync(0xffffffffu, c_incl, 31);
+    for (int base = 32; base < b; base += 32) {
       int a0, nn, Lk;
-      if (seq(k, a0, nn, Lk)) W += prefix(units(nn), nn, Lk);
+      long long f, incl;
+      scan(base, a0, nn, Lk, f, incl);
+      W += __shfl_sync(0xffffffffu, incl, 31);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
     W *= g;
     // a run is worth at least the work of a unit and two tiles: less costs
     // more to join than it saves
     nc = static_cast<int>(min(static_cast<long long>(nc), W / (kUnitCost + 2 * kN) + 1));
     if (W == 0 || c >= nc) return;
-    const int near = static_cast<int>(W / nc / (32 * kN));
-    end = c + 1 < nc ? locate(W * (c + 1) / nc, near) : ChunkPos{b, 0, 0, 0};
-    at = locate(W * c / nc, near);
+    const long long run = div_pos(W, nc);
+    const int near = static_cast<int>(run / (32 * kN));
+    const int left = static_cast<int>(W - run * nc);  // the first `left` runs are one longer
+    end = c + 1 < nc ? locate(run * (c + 1) + min(c + 1, left), near) : ChunkPos{b, 0, 0, 0};
+    at = locate(run * c + min(c, left), near);
     if (c == 0) at.lt = 0;
     more = true;
     // (a place at its unit's last tile's end is the next unit's start)
-    if (at.i < b && at.lt >= tiles(at.qt, n, L, tq2)) advance();
+    if (at.i < b && at.lt >= tiles(at.qt, n, L)) advance();
   }
 
   __device__ void advance() {  // to the next unit's start
@@ -255,16 +282,16 @@ struct ChunkWalk {
 
   __device__ bool next(ChunkSeg& s) {
     if (!more || at.i >= b) return false;
-    const int ti = tiles(at.qt, n, L, tq2);
+    const int ti = tiles(at.qt, n, L);
     const bool last = at.i == end.i && at.j == end.j && at.qt == end.qt;
     const bool past = at.i > end.i || (at.i == end.i && (at.j > end.j ||
                                        (at.j == end.j && at.qt > end.qt)));
     if (past || (last && end.lt <= at.lt)) return false;
     s.i = at.i;
     s.j = at.j;
-    s.t0 = t0 + at.qt * tq2;
-    s.pos0 = L - n + at.qt * tq2;
-    s.ntok = min(n - at.qt * tq2, tq2);
+    s.t0 = t0 + at.qt * 2 * tq;
+    s.pos0 = L - n + at.qt * 2 * tq;
+    s.ntok = min(n - at.qt * 2 * tq, 2 * tq);
     s.L = L;
     s.ti = ti;
     s.lt0 = at.lt;
@@ -761,13 +788,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int c0 = twin ? side * (DV / 64) : 0, c1 = twin ? c0 + DV / 64 : DV / 32;
       const float inv = 1.f / l;
-      T16* dst = static_cast<T16*>(p.out) +
-                 (static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head) * DV;
-      const size_t at = slot * p.srows + (twin ? 0 : side * kM) + row;
+      // A thread holds a row; rows leave through shared memory, 32 columns of
+      // the warp's 32 rows at a time, so that neighbouring lanes write
+      // neighbouring addresses.
+      const size_t at = slot * p.srows + (twin ? 0 : side * kM);
       if (!whole && live && (!twin || side == 0)) {
-        p.part_ml[2 * at] = ms;
-        p.part_ml[2 * at + 1] = l;
+        p.part_ml[2 * (at + row)] = ms;
+        p.part_ml[2 * (at + row) + 1] = l;
       }
+      // output row of each lane's query row, from the unit's first (-1: none)
+      const int orow = live ? my_tok * p.h + head : -1;
+      T16* const obase =
+          static_cast<T16*>(p.out) + (static_cast<size_t>(seg.t0) * p.h + seg.j * p.r) * DV;
+      uint8_t* const stage = sm + C::OFF_STAGE + warp * (32 * 128);
       for (int c = c0; c < c1; ++c) {
         if (nt == 0 && other == 0) break;  // (a side without tokens)
         float o[32];
@@ -778,30 +811,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (twin) {
+        if (other > 0) {
           float o2[32];
-          if (other > 0) {
-            tmem_ld32(tO + (side ? -128 : 128) + 32 * c, o2);
-            tmem_wait_ld();
+          tmem_ld32(tO + (side ? -128 : 128) + 32 * c, o2);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = o[e] * wo + o2[e] * wt;
-          }
+          for (int e = 0; e < 32; ++e) o[e] = o[e] * wo + o2[e] * wt;
         }
-        if (!live) continue;
+        // 16-byte pieces of a row, their order turned by the row
         if (whole) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
+          for (int k = 0; k < 4; ++k) {
             float y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = o[e + k] * inv;
-            store8(dst + 32 * c + e, y);
+            for (int e = 0; e < 8; ++e) y[e] = o[8 * k + e] * inv;
+            store8(reinterpret_cast<T16*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)), y);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 8 * k + (lane >> 2), pc = lane & 3;
+            const int to = __shfl_sync(0xffffffffu, orow, rr);
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(stage + rr * 64 + ((pc ^ ((rr >> 1) & 3)) << 4));
+            if (to >= 0)
+              *reinterpret_cast<uint4*>(obase + static_cast<size_t>(to) * DV + 32 * c + 8 * pc) = v;
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(p.part_o + at * DV + 32 * c + e) =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          __syncwarp();
+          const size_t row0 = at + (warp & 3) * 32;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 4 * k + (lane >> 3), pc = lane & 7;
+            const int to = __shfl_sync(0xffffffffu, orow, rr);
+            const float4 v =
+                *reinterpret_cast<const float4*>(stage + rr * 128 + ((pc ^ (rr & 7)) << 4));
+            if (to >= 0)
+              *reinterpret_cast<float4*>(p.part_o + (row0 + rr) * DV + 32 * c + 4 * pc) = v;
+          }
         }
+        __syncwarp();
       }
       tc_fence_before();
       if (twin) {  // both O and ml_sm are free again
