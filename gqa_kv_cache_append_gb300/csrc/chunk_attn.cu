@@ -68,11 +68,9 @@ struct ChunkCfg {
   static constexpr int Q_BYTES = kM * DK * 2;  // one side
   static constexpr int SLOT = kN * (DK > DV ? DK : DV) * 2;
   // ring slots: K and V tiles by turns
-  static constexpr int NS = DK == 128 ? 4 : (DV == 128 ? 5 : 8);
+  static constexpr int NS = DK == 128 ? 5 : (DV == 128 ? 6 : 10);
   static constexpr int OFF_RING = 2 * Q_BYTES;
-  // a softmax warp's 32 rows x 32 columns on their way out
-  static constexpr int OFF_STAGE = OFF_RING + NS * SLOT;
-  static constexpr int OFF_BAR = OFF_STAGE + 8 * 32 * 128;
+  static constexpr int OFF_BAR = OFF_RING + NS * SLOT;
   static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
                        S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
@@ -254,9 +252,8 @@ struct ChunkWalk {
       W += __shfl_sync(0xffffffffu, incl, 31);
     }
     W *= g;
-    // a run is worth at least the work of a unit and two tiles: less costs
-    // more to join than it saves
-    nc = static_cast<int>(min(static_cast<long long>(nc), W / (kUnitCost + 2 * kN) + 1));
+    // a run is worth at least two tiles: less costs more to join than it saves
+    nc = static_cast<int>(min(static_cast<long long>(nc), W / (2 * kN) + 1));
     if (W == 0 || c >= nc) return;
     const long long run = div_pos(W, nc);
     const int near = static_cast<int>(run / (32 * kN));
@@ -788,73 +785,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int c0 = twin ? side * (DV / 64) : 0, c1 = twin ? c0 + DV / 64 : DV / 32;
       const float inv = 1.f / l;
-      // A thread holds a row; rows leave through shared memory, 32 columns of
-      // the warp's 32 rows at a time, so that neighbouring lanes write
-      // neighbouring addresses.
       const size_t at = slot * p.srows + (twin ? 0 : side * kM);
       if (!whole && live && (!twin || side == 0)) {
         p.part_ml[2 * (at + row)] = ms;
         p.part_ml[2 * (at + row) + 1] = l;
       }
-      // output row of each lane's query row, from the unit's first (-1: none)
+      // O is read with eight rows to a block of columns, four lanes to a row,
+      // so that neighbouring lanes write neighbouring addresses (a row per
+      // lane spreads each store over 32 lines).  Of this warp's rows a lane
+      // gets lane / 4 + 8 k, k < 4: their factors and output rows (-1: none).
       const int orow = live ? my_tok * p.h + head : -1;
+      int to[4];
+      float fo[4], ft[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int src = 8 * k + (lane >> 2);
+        to[k] = __shfl_sync(0xffffffffu, orow, src);
+        fo[k] = __shfl_sync(0xffffffffu, whole ? wo * inv : wo, src);
+        ft[k] = __shfl_sync(0xffffffffu, whole ? wt * inv : wt, src);
+      }
       T16* const obase =
           static_cast<T16*>(p.out) + (static_cast<size_t>(seg.t0) * p.h + seg.j * p.r) * DV;
-      uint8_t* const stage = sm + C::OFF_STAGE + warp * (32 * 128);
+      float* const pbase = p.part_o + (at + (warp & 3) * 32) * DV;
       for (int c = c0; c < c1; ++c) {
         if (nt == 0 && other == 0) break;  // (a side without tokens)
-        float o[32];
-        if (nt > 0) {
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-        } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
-        if (other > 0) {
-          float o2[32];
-          tmem_ld32(tO + (side ? -128 : 128) + 32 * c, o2);
-          tmem_wait_ld();
+        for (int hh = 0; hh < 2; ++hh) {  // rows 0-15, 16-31 of the warp
+          const uint32_t ta = tO + (static_cast<uint32_t>(16 * hh) << 16) + 32 * c;
+          float v[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = o[e] * wo + o2[e] * wt;
-        }
-        // 16-byte pieces of a row, their order turned by the row
-        if (whole) {
+          for (int e = 0; e < 16; ++e) v[e] = 0.f;
+          if (nt > 0) {
+            tmem_ld_blocks(ta, v);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = o[8 * k + e] * inv;
-            store8(reinterpret_cast<T16*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)), y);
+            for (int e = 0; e < 16; ++e) v[e] *= fo[2 * hh + ((e >> 1) & 1)];
           }
-          __syncwarp();
+          if (other > 0) {
+            float v2[16];
+            tmem_ld_blocks(ta + (side ? -128 : 128), v2);
+            tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = 8 * k + (lane >> 2), pc = lane & 3;
-            const int to = __shfl_sync(0xffffffffu, orow, rr);
-            const uint4 v =
-                *reinterpret_cast<const uint4*>(stage + rr * 64 + ((pc ^ ((rr >> 1) & 3)) << 4));
-            if (to >= 0)
-              *reinterpret_cast<uint4*>(obase + static_cast<size_t>(to) * DV + 32 * c + 8 * pc) = v;
+            for (int e = 0; e < 16; ++e) v[e] = fmaf(v2[e], ft[2 * hh + ((e >> 1) & 1)], v[e]);
           }
-        } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          __syncwarp();
-          const size_t row0 = at + (warp & 3) * 32;
+          for (int hi = 0; hi < 2; ++hi) {  // rows lane / 4, + 8
+            const int k = 2 * hh + hi;
+            if (whole) {
+              uint32_t u[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = 4 * k + (lane >> 3), pc = lane & 7;
-            const int to = __shfl_sync(0xffffffffu, orow, rr);
-            const float4 v =
-                *reinterpret_cast<const float4*>(stage + rr * 128 + ((pc ^ (rr & 7)) << 4));
-            if (to >= 0)
-              *reinterpret_cast<float4*>(p.part_o + (row0 + rr) * DV + 32 * c + 4 * pc) = v;
+              for (int blk = 0; blk < 4; ++blk)
+                u[blk] = Half16<T16>::pack2(v[4 * blk + 2 * hi], v[4 * blk + 2 * hi + 1]);
+              quad_transpose(u);
+              if (to[k] >= 0)
+                *reinterpret_cast<uint4*>(obase + static_cast<size_t>(to[k]) * DV + 32 * c +
+                                          8 * (lane & 3)) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else if (to[k] >= 0) {
+              float* dst = pbase + (8 * k + (lane >> 2)) * DV + 32 * c + 2 * (lane & 3);
+#pragma unroll
+              for (int blk = 0; blk < 4; ++blk)
+                *reinterpret_cast<float2*>(dst + 8 * blk) =
+                    make_float2(v[4 * blk + 2 * hi], v[4 * blk + 2 * hi + 1]);
+            }
           }
         }
-        __syncwarp();
       }
       tc_fence_before();
       if (twin) {  // both O and ml_sm are free again
