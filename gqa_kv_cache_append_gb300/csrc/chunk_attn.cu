@@ -90,6 +90,7 @@ struct ChunkParams {
   int bsz, max_blocks, num_blocks;
   float scale_log2;
   void* out;
+  bool out_sectors;    // out is aligned to 32 bytes
   int* desc;           // [grid][kDescInts]
   float* part_ml;      // [2 * grid][srows][2]
   float* part_o;       // [2 * grid][srows][d_v]
@@ -700,11 +701,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int base = (seg.lt0 + (twin ? 2 * t + side : t)) * kN;
         if (base + kN - 1 > first_pos) {
-          // positions past this row's token
+          // positions past this row's token, 32 at a time (those that the
+          // side's first token sees need no mask)
           const int lim = my_pos - base;
 #pragma unroll
-          for (int e = 0; e < kN; ++e)
-            if (e > lim) x[e] = -INFINITY;
+          for (int c = 0; c < kN / 32; ++c) {
+            if (base + 32 * c + 31 <= first_pos) continue;  // (uniform)
+            const int see = lim + 1 - 32 * c;
+            const uint32_t bits = see >= 32 ? ~0u : see <= 0 ? 0u : (1u << see) - 1u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
+          }
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -790,64 +798,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.part_ml[2 * (at + row)] = ms;
         p.part_ml[2 * (at + row) + 1] = l;
       }
-      // O is read with eight rows to a block of columns, four lanes to a row,
-      // so that neighbouring lanes write neighbouring addresses (a row per
-      // lane spreads each store over 32 lines).  Of this warp's rows a lane
-      // gets lane / 4 + 8 k, k < 4: their factors and output rows (-1: none).
-      const int orow = live ? my_tok * p.h + head : -1;
-      int to[4];
-      float fo[4], ft[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int src = 8 * k + (lane >> 2);
-        to[k] = __shfl_sync(0xffffffffu, orow, src);
-        fo[k] = __shfl_sync(0xffffffffu, whole ? wo * inv : wo, src);
-        ft[k] = __shfl_sync(0xffffffffu, whole ? wt * inv : wt, src);
-      }
-      T16* const obase =
-          static_cast<T16*>(p.out) + (static_cast<size_t>(seg.t0) * p.h + seg.j * p.r) * DV;
-      float* const pbase = p.part_o + (at + (warp & 3) * 32) * DV;
+      // A thread writes its own row, in whole 32-byte sectors where the output
+      // is aligned to them.  (Rows turned in shared memory or by shuffles
+      // between four lanes touch fewer lines a store but cost more
+      // instructions: XX and YY us for the mixed batch against ZZ.)
+      T16* const dst = static_cast<T16*>(p.out) +
+                       (static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head) * DV;
+      float* const pdst = p.part_o + (at + row) * DV;
+      const float fo = whole ? wo * inv : wo, ft = whole ? wt * inv : wt;
       for (int c = c0; c < c1; ++c) {
         if (nt == 0 && other == 0) break;  // (a side without tokens)
+        float o[32];
+        if (nt > 0) {
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {  // rows 0-15, 16-31 of the warp
-          const uint32_t ta = tO + (static_cast<uint32_t>(16 * hh) << 16) + 32 * c;
-          float v[16];
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0.f;
-          if (nt > 0) {
-            tmem_ld_blocks(ta, v);
-            tmem_wait_ld();
+        for (int e = 0; e < 32; ++e) o[e] *= fo;
+        if (other > 0) {
+          float o2[32];
+          tmem_ld32(tO + (side ? -128 : 128) + 32 * c, o2);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= fo[2 * hh + ((e >> 1) & 1)];
-          }
-          if (other > 0) {
-            float v2[16];
-            tmem_ld_blocks(ta + (side ? -128 : 128), v2);
-            tmem_wait_ld();
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], ft, o[e]);
+        }
+        if (!live) continue;
+        if (whole) {
+          uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = fmaf(v2[e], ft[2 * hh + ((e >> 1) & 1)], v[e]);
-          }
+          for (int e = 0; e < 16; ++e) u[e] = Half16<T16>::pack2(o[2 * e], o[2 * e + 1]);
+          store_sectors<2>(dst + 32 * c, u, p.out_sectors);
+        } else {
+          uint32_t u[32];
 #pragma unroll
-          for (int hi = 0; hi < 2; ++hi) {  // rows lane / 4, + 8
-            const int k = 2 * hh + hi;
-            if (whole) {
-              uint32_t u[4];
-#pragma unroll
-              for (int blk = 0; blk < 4; ++blk)
-                u[blk] = Half16<T16>::pack2(v[4 * blk + 2 * hi], v[4 * blk + 2 * hi + 1]);
-              quad_transpose(u);
-              if (to[k] >= 0)
-                *reinterpret_cast<uint4*>(obase + static_cast<size_t>(to[k]) * DV + 32 * c +
-                                          8 * (lane & 3)) = make_uint4(u[0], u[1], u[2], u[3]);
-            } else if (to[k] >= 0) {
-              float* dst = pbase + (8 * k + (lane >> 2)) * DV + 32 * c + 2 * (lane & 3);
-#pragma unroll
-              for (int blk = 0; blk < 4; ++blk)
-                *reinterpret_cast<float2*>(dst + 8 * blk) =
-                    make_float2(v[4 * blk + 2 * hi], v[4 * blk + 2 * hi + 1]);
-            }
-          }
+          for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e]);
+          store_sectors<4>(pdst + 32 * c, u, true);
         }
       }
       tc_fence_before();
@@ -1018,6 +1006,7 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   p.num_blocks = x.num_blocks;
   p.scale_log2 = static_cast<float>(static_cast<double>(x.scale) * 1.4426950408889634);
   p.out = x.out;
+  p.out_sectors = (reinterpret_cast<uintptr_t>(x.out) & 31) == 0;
   char* ws = static_cast<char*>(x.ws);
   p.desc = reinterpret_cast<int*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + pl.ml_at);

@@ -185,40 +185,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
       : "memory");
 }
 
-// 16 lanes x 32 columns in blocks of eight: thread t holds, of block k, lane
-// (base + t / 4) columns 2 (t % 4), + 1 in v[4 k], v[4 k + 1] and lane
-// (base + t / 4 + 8) the same columns in v[4 k + 2], v[4 k + 3]
-__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-#pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
-}
-
-// 4 x 4 transposition among four neighbouring lanes: lane q's v[k] becomes
-// lane k's v[q]
-__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4]) {
-  const int lane = threadIdx.x;
-#pragma unroll
-  for (int bit = 1; bit <= 2; bit <<= 1) {
-    const bool up = (lane & bit) != 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k & bit) continue;
-      const uint32_t send = up ? v[k] : v[k | bit];
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, send, bit);
-      if (up)
-        v[k] = got;
-      else
-        v[k | bit] = got;
-    }
-  }
-}
-
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -264,6 +230,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// N x 32 bytes to consecutive addresses, as whole sectors (dst aligned to 32
+// bytes) or in 16-byte pieces
+template <int N>
+__device__ __forceinline__ void store_sectors(void* dst, const uint32_t* v, bool sectors) {
+  char* d = static_cast<char*>(dst);
+  if (sectors) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + 32 * k),
+                   "r"(v[8 * k]), "r"(v[8 * k + 1]), "r"(v[8 * k + 2]), "r"(v[8 * k + 3]),
+                   "r"(v[8 * k + 4]), "r"(v[8 * k + 5]), "r"(v[8 * k + 6]), "r"(v[8 * k + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2 * N; ++k)
+      *reinterpret_cast<uint4*>(d + 16 * k) =
+          make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  }
 }
 
 }  // namespace gqa
