@@ -24,7 +24,8 @@
 //   warp 8     one lane issues every product
 //   warp 10    TMA: the sides' query rows once per unit, K and V tiles into a
 //              ring (64-column boxes, 128-byte swizzle)
-//   (warps 9 and 11 idle: registers are dealt out by warpgroups)
+//   warp 11    the run's end (the TMA warp finds its start meanwhile)
+//   (warp 9 checks the lengths: registers are dealt out by warpgroups)
 // TMEM columns: S_A 0-127, S_B 128-255 (each holds P, two 16-bit values a
 // column, once its S has been read), O_A 256.., O_B 384...
 //
@@ -74,11 +75,11 @@ struct ChunkCfg {
   static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
                        S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
-                       TWIN = V_EDGE + 1, DRAIN = TWIN + 2, NBAR = DRAIN + 1;
+                       TWIN = V_EDGE + 1, RUN_END = TWIN + 2, DRAIN = RUN_END + 1, NBAR = DRAIN + 1;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
   static constexpr int OFF_ML = OFF_SEG + kSegs * kSegBytes;  // float2 [2][kM]: twins' maxima, sums
-  static constexpr int OFF_MISC = OFF_ML + 2 * kM * 8;
-  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int OFF_MISC = OFF_ML + 2 * kM * 8;  // TMEM address, abort flag; the run's end
+  static constexpr int SMEM = OFF_MISC + 32;
   static constexpr int T_S = 0, T_O = 256;  // TMEM columns, 128 to a side
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -132,7 +133,7 @@ static_assert(sizeof(ChunkSeg) <= kSegBytes, "segment ring");
 // of them a closed form.  All units are laid end to end (sequences, KV heads,
 // blocks of query rows) and run c begins at c * W / nc, moved to a tile's
 // edge, or to the unit's when that is near.
-constexpr int kUnitCost = 256;
+constexpr int kUnitCost = 192;
 
 struct ChunkPos {  // a place in the order of all tiles
   int i, j, qt, lt;
@@ -235,7 +236,9 @@ struct ChunkWalk {
     return {b, 0, 0, 0};  // not reached for x < W
   }
 
-  __device__ void init(const ChunkParams& p, int c, int nc) {
+  // Run c's start: false when the launch has fewer runs than that (c = their
+  // number: the end of the last one, behind every sequence).
+  __device__ bool start(const ChunkParams& p, int c, int nc, ChunkPos& r) {
     cu = p.cu;
     lens = p.lens;
     b = p.b;
@@ -243,7 +246,6 @@ struct ChunkWalk {
     tq = p.tq;
     total = p.total;
     cap = p.cap;
-    more = false;
     scan(0, c_t0, c_n, c_L, c_f, c_incl);
     long long W = __shfl_sync(0xffffffffu, c_incl, 31);
     for (int base = 32; base < b; base += 32) {
@@ -253,18 +255,26 @@ struct ChunkWalk {
       W += __shfl_sync(0xffffffffu, incl, 31);
     }
     W *= g;
+    r = {b, 0, 0, 0};
     // a run is worth at least two tiles: less costs more to join than it saves
     nc = static_cast<int>(min(static_cast<long long>(nc), W / (2 * kN) + 1));
-    if (W == 0 || c >= nc) return;
+    if (W == 0 || c > nc) return false;
+    if (c == nc) return true;
     const long long run = div_pos(W, nc);
     const int near = static_cast<int>(run / (32 * kN));
     const int left = static_cast<int>(W - run * nc);  // the first `left` runs are one longer
-    end = c + 1 < nc ? locate(run * (c + 1) + min(c + 1, left), near) : ChunkPos{b, 0, 0, 0};
-    at = locate(run * c + min(c, left), near);
-    if (c == 0) at.lt = 0;
-    more = true;
+    r = locate(run * c + min(c, left), near);
+    if (c == 0) r.lt = 0;
+    return true;
+  }
+
+  // Begin run c, whose end is e.
+  __device__ void begin(const ChunkPos& from, const ChunkPos& e) {
+    at = from;
+    end = e;
+    more = at.i < b;
     // (a place at its unit's last tile's end is the next unit's start)
-    if (at.i < b && at.lt >= tiles(at.qt, n, L)) advance();
+    if (more && at.lt >= tiles(at.qt, n, L)) advance();
   }
 
   __device__ void advance() {  // to the next unit's start
@@ -350,8 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   pdl_wait_then_release();
-  if (warp == 11 && blockIdx.x == 0)
-    report_bad_packed(p.cu, p.lens, p.b, p.total, p.cap, p.status);
 
   auto seg_at = [&](uint32_t k) -> ChunkSeg* {
     return reinterpret_cast<ChunkSeg*>(sm + C::OFF_SEG + (k % kSegs) * kSegBytes);
@@ -360,21 +368,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     return mbar_wait(BAR(k), phase & 1u, abort_flag, p.status, p.budget);
   };
 
-  if (warp == 9 || warp == 11) {
+  ChunkPos* const run_end = reinterpret_cast<ChunkPos*>(sm + C::OFF_MISC + 16);
+  if (warp == 9) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (blockIdx.x == 0) report_bad_packed(p.cu, p.lens, p.b, p.total, p.cap, p.status);
+  } else if (warp == 11) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    // the run's end, beside the TMA warp's look for its start
+    ChunkWalk w;
+    ChunkPos e;
+    w.start(p, blockIdx.x + 1, gridDim.x, e);
+    if (lane == 0) {
+      *run_end = e;
+      mbar_arrive(BAR(C::RUN_END));
+    }
+    __syncwarp();
   } else if (warp == 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // ============================ TMA producer ============================
     ChunkWalk w;
     ChunkSeg seg;
-    w.init(p, blockIdx.x, gridDim.x);
+    ChunkPos from;
+    const bool any = w.start(p, blockIdx.x, gridDim.x, from);
     const uint64_t pol = policy_evict_last();
     const int oob_row = PAGED ? p.num_blocks * p.g * p.bsz : 0;
     const int box = PAGED ? min(p.bsz, kN) : kN;
     const int sub = kN / box;  // boxes a tile and 64-column half
     uint32_t slot_n = 0, qn[2] = {0, 0}, edge_n = 0;
     uint32_t kn = 0;  // segments announced
-    bool ok = true;
+    bool ok = __all_sync(0xffffffffu, wait(C::RUN_END, 0));
+    w.begin(any ? from : ChunkPos{p.b, 0, 0, 0}, ok ? *run_end : ChunkPos{p.b, 0, 0, 0});
     auto announce = [&](const ChunkSeg& sg) {
       ok = __all_sync(0xffffffffu, wait(C::SEG_EMPTY + kn % kSegs, ((kn / kSegs) & 1) ^ 1));
       if (!ok) return;

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
   auto BAR = [&](int k) -> uint32_t { return s_base + C::OFF_BAR + 8u * k; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (broadcast, so that what depends on it is known to be uniform)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int nr = p.nq * p.r;
 
   if (threadIdx.x == 0) {
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::NCOLS);
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait_then_release();
   if (warp == 2 && blockIdx.x == 0) report_bad_lengths(p.lens, p.b, p.nq, p.cap, p.status);
 
@@ -246,62 +247,70 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ============================ MMA issuers =============================
-    // (each walks with the whole warp, lane 0 waits and issues)
+    // (the whole warp walks with warp-uniform values and one elected lane
+    // issues: from a single lane's branch the operands take a detour into the
+    // uniform registers that costs several times what a product runs)
     constexpr uint32_t kIdescS = idesc_e4m3(128, N, 0, 0);
     constexpr uint32_t kIdescO = idesc_e4m3(128, N, 1, 1);
-    uint32_t n = 0, k = 0;
+    const bool s_role = warp == 1;
+    const uint64_t dq = smem_desc(s_base + C::OFF_Q, 16, 8 * DK, C::K_SWZ);
+    const uint64_t dk = smem_desc(s_base, 16, 8 * DK, C::K_SWZ);
+    // A = V^T: 128 head-dim columns contiguous; B = P^T: N columns contiguous,
+    // over the stage's K rows
+    const uint64_t dv = smem_desc(s_base + C::K_BYTES, C::V_BYTES, 8 * DV, C::V_SWZ);
+    const uint64_t dp = smem_desc(s_base, kTile * N, 8 * N, C::P_SWZ);
+    uint32_t nb = 0, nph = 0;           // tile's buffer, and its phase
+    uint32_t st = 0, sph = 0;           // ring slot, and its phase
+    uint32_t qb = 0, qph = 0;
     bool ok = true;
-    while (w.next(seg)) {
-      if (lane == 0) {
-        if (warp == 1) ok = ok && wait(C::Q_FULL + (k & 1), k >> 1);
-        for (int lt = seg.lt0; lt < seg.lt1; ++lt, ++n) {
-          const int st = n % kRing;
-          const uint32_t nb = n & 1;
-          const uint32_t kbase = s_base + st * C::STAGE;
-          if (warp == 1) {
-            ok = ok && wait(C::FULL_K + st, n / kRing);
-            ok = ok && wait(C::S_FREE + nb, (n >> 1) ^ 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b0 =
-                smem_desc(s_base + C::OFF_Q + (k & 1) * C::Q_BYTES, 16, 8 * DK, C::K_SWZ);
+    while (ok && w.next(seg)) {
+      const int T = __shfl_sync(0xffffffffu, seg.lt1 - seg.lt0, 0);
+      if (s_role) ok = __all_sync(0xffffffffu, wait(C::Q_FULL + qb, qph));
+      for (int t = 0; t < T && ok; ++t) {
+        const uint32_t at = st * (C::STAGE >> 4);
+        if (s_role) {
+          ok = __all_sync(0xffffffffu,
+                          wait(C::FULL_K + st, sph) && wait(C::S_FREE + nb, nph ^ 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b0 = dq + qb * (C::Q_BYTES >> 4), a0 = dk + at;
+          if (elect_one()) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint64_t a0 = smem_desc(kbase + hf * kHalf * DK, 16, 8 * DK, C::K_SWZ);
+            for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int kk = 0; kk < DK / 32; ++kk)  // 32 head-dim columns a step
-                mma_f8(tmem + C::T_S + (nb * 2 + hf) * N, a0 + ((kk * 32) >> 4),
+                mma_f8(tmem + C::T_S + (nb * 2 + hf) * N, a0 + ((hf * kHalf * DK + kk * 32) >> 4),
                        b0 + ((kk * 32) >> 4), kIdescS, kk > 0 ? 1u : 0u);
-            }
             mma_commit(BAR(C::S_FULL + nb));
-            if (lt == seg.lt1 - 1) mma_commit(BAR(C::Q_EMPTY + (k & 1)));
-          } else {
-            ok = ok && wait(C::P_READY + nb, n >> 1);
-            ok = ok && wait(C::FULL_V + st, n / kRing);
-            ok = ok && wait(C::O_FREE + nb, (n >> 1) ^ 1);
-            if (!ok) break;
-            tc_fence_after();
-            // A = V^T: 128 head-dim columns contiguous, 32 positions a step;
-            // B = P^T: N columns contiguous, over the stage's K rows
-            const uint64_t a0 = smem_desc(kbase + C::K_BYTES, C::V_BYTES, 8 * DV, C::V_SWZ);
-            const uint64_t b0 = smem_desc(kbase, kTile * N, 8 * N, C::P_SWZ);
+            if (t == T - 1) mma_commit(BAR(C::Q_EMPTY + qb));
+          }
+        } else {
+          ok = __all_sync(0xffffffffu, wait(C::FULL_V + st, sph) &&
+                                           wait(C::O_FREE + nb, nph ^ 1) &&
+                                           wait(C::P_READY + nb, nph));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a0 = dv + at, b0 = dp + at;
+          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTile / 32; ++kk)
+            for (int kk = 0; kk < kTile / 32; ++kk)  // 32 positions a step
               mma_f8(tmem + C::T_O + nb * N, a0 + ((kk * 32 * DV) >> 4), b0 + ((kk * 32 * N) >> 4),
                      kIdescO, kk > 0 ? 1u : 0u);
             mma_commit(BAR(C::O_FULL + nb));
             mma_commit(BAR(C::EMPTY + st));
           }
         }
+        __syncwarp();
+        if (nb ^= 1; nb == 0) nph ^= 1;
+        if (++st == kRing) {
+          st = 0;
+          sph ^= 1;
+        }
       }
-      __syncwarp();
-      ++k;
-      n = __shfl_sync(0xffffffffu, n, 0);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
+      if (qb ^= 1; qb == 0) qph ^= 1;
     }
-    if (lane == 0) {
-      // every product has to be finished before tensor memory is released
+    // every product has to be finished before tensor memory is released
+    if (elect_one()) {
       mma_commit(BAR(C::DRAIN));
       const long long t0 = clock64();
       while (!mbar_try_wait(BAR(C::DRAIN), 0) && clock64() - t0 < p.budget) {

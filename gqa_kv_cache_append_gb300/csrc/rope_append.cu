@@ -269,13 +269,13 @@ __global__ void __launch_bounds__(kRopeThreads, 8)
 }
 
 // ---------------------------------------------------------------------------
-// e4m3 cache -> rows of the call's type: positions [128 x, 128 x + 128) of KV
+// e4m3 cache -> rows of the call's type: positions [64 x, 64 x + 64) of KV
 // head y of sequence z.  A thread takes one 16-byte piece of every
-// (256 / pieces)-th row, four rows of K and four of V at a time with their
-// loads side by side (with two in flight 86 MB took 20 us, with eight ZZ).
+// (256 / pieces)-th row, up to four rows of K and of V at a time with their
+// loads side by side.
 // Memory-bound: d + 4 bytes read and d * sizeof(T) written per row.
 // ---------------------------------------------------------------------------
-constexpr int kReadRows = 128;
+constexpr int kReadRows = 64;
 constexpr int kReadThreads = 256;
 
 struct ReadRows {  // what a thread reads of one tensor
@@ -314,23 +314,26 @@ struct ReadRows {  // what a thread reads of one tensor
     }
   }
   template <typename T>
-  __device__ void store(T* __restrict__ dst, int base) const {
+  __device__ void store(T* __restrict__ dst, int base, bool sectors) const {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (!(use & (1u << u))) continue;
       T* to = dst + static_cast<size_t>(row0 + base + u * step) * d + 16 * c;
       const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      uint32_t y[4 * sizeof(T)];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = e4m3_unpack2(w[2 * hf + (k >> 1)] >> (16 * (k & 1)));
-          x[2 * k] = f.x * sc[u];
-          x[2 * k + 1] = f.y * sc[u];
+      for (int k = 0; k < 8; ++k) {
+        float2 f = e4m3_unpack2(w[k >> 1] >> (16 * (k & 1)));
+        f.x *= sc[u];
+        f.y *= sc[u];
+        if constexpr (sizeof(T) == 2) {
+          y[k] = Half16<T>::pack2(f.x, f.y);
+        } else {
+          y[2 * k] = __float_as_uint(f.x);
+          y[2 * k + 1] = __float_as_uint(f.y);
         }
-        store8(to + 8 * hf, x);
       }
+      store_sectors<sizeof(T) / 2>(to, y, sectors);
     }
   }
 };
@@ -353,14 +356,16 @@ __global__ void __launch_bounds__(kReadThreads)
   if (rows <= 0) return;
   const int* trow = table + static_cast<size_t>(i) * max_blocks;
   const size_t dst0 = (static_cast<size_t>(i) * g + j) * cap + p0;
+  const bool sectors = ((reinterpret_cast<uintptr_t>(k_cache) |
+                         reinterpret_cast<uintptr_t>(v_cache)) & 31) == 0;
   ReadRows k, v;
   k.start(dk);
   v.start(dv);
   for (int kb = 0, vb = 0; kb < rows || vb < rows; kb += 4 * k.step, vb += 4 * v.step) {
     k.load(k_pool, k_scale, trow, kb, p0, rows, g, j, bshift, num_blocks, status);
     v.load(v_pool, v_scale, trow, vb, p0, rows, g, j, bshift, num_blocks, status);
-    k.store(k_cache + dst0 * dk, kb);
-    v.store(v_cache + dst0 * dv, vb);
+    k.store(k_cache + dst0 * dk, kb, sectors);
+    v.store(v_cache + dst0 * dv, vb, sectors);
   }
 }
 
