@@ -824,7 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A thread writes its own row, in whole 32-byte sectors where the output
       // is aligned to them.  (Rows turned in shared memory or by shuffles
       // between four lanes touch fewer lines a store but cost more
-      // instructions: XX and YY us for the mixed batch against ZZ.)
+      // instructions: 155 and 149 us for a mixed batch of prompts, chunks and
+      // single tokens against 142.)
       T16* const dst = static_cast<T16*>(p.out) +
                        (static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head) * DV;
       float* const pdst = p.part_o + (at + row) * DV;
