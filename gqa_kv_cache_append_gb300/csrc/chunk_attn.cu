@@ -888,18 +888,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the units that a run's end cut: block (c, k) handles
-// rows [32 k, 32 k + 32) of the unit whose first piece is CTA c's, a warp to a
-// row.  With per-piece maxima m, sums l and unnormalised outputs O over
-// disjoint positions: M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, in
-// the pieces' order.
+// rows [32 k, 32 k + 32) of the unit whose first piece is CTA c's, two rows to
+// a warp, four pieces of both at a time with their loads side by side (a row
+// after the other and a piece after the other took 12 us on cold caches).
+// With per-piece maxima m, sums l and unnormalised outputs O over disjoint
+// positions: M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, in the
+// pieces' order.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinRows = 32;
+
 template <typename T16, int DV>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p, int nc) {
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkParams p, int nc) {
+  constexpr int CPL = DV / 32;  // columns a lane
+  constexpr int NP = 4;         // pieces at a time
   pdl_wait_then_release();
   const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int* d = p.desc + static_cast<size_t>(c) * kDescInts;
-  if (!__ldg(d + D_HEAD)) return;
-  const int tok0 = __ldg(d + D_TOK0), ntok = __ldg(d + D_NTOK), j = __ldg(d + D_J);
+  const int4 d4 = __ldg(reinterpret_cast<const int4*>(p.desc + static_cast<size_t>(c) * kDescInts));
   // the CTA that holds the unit's last piece
   int last = -1;
   for (int base = c + 1; base < nc && last < 0; base += 32) {
@@ -907,49 +912,81 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkParams p, in
     const bool e = k < nc && __ldg(p.desc + static_cast<size_t>(k) * kDescInts + D_END);
     const unsigned hit = __ballot_sync(0xffffffffu, e);
     if (hit) last = base + __ffs(hit) - 1;
+    if (!d4.x) return;
   }
-  if (last < 0) return;  // (not reached unless a launch gave up)
-  constexpr int CPL = DV / 32;
-  for (int k = warp; k < 32; k += 8) {
-    const int row = blockIdx.y * 32 + k;
-    const int side = row / kM, rr = row % kM, tok = rr / p.r;
-    const int t = side * p.tq + tok;
-    if (row >= p.srows || tok >= p.tq || t >= ntok) continue;
-    auto at = [&](int x) -> size_t {
-      return static_cast<size_t>(2 * x + (x == c ? 1 : 0)) * p.srows + row;
-    };
-    float M = -INFINITY;
-    for (int x = c + lane; x <= last; x += 32) M = fmaxf(M, __ldg(p.part_ml + 2 * at(x)));
-    M = warp_max(M);
-    float den = 0.f, num[CPL];
+  if (!d4.x || last < 0) return;  // (none cut here)
+  const int tok0 = d4.y, ntok = d4.z, j = d4.w;
+  int row[2], orow[2];
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) num[e] = 0.f;
-    for (int x = c; x <= last; ++x) {
-      const float2 ml = __ldg(reinterpret_cast<const float2*>(p.part_ml) + at(x));
-      if (ml.x == -INFINITY) continue;  // a piece this row sees nothing of
-      const float wgt = ex2(ml.x - M);
-      den = fmaf(wgt, ml.y, den);
-      float o[CPL];
-      if constexpr (CPL == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p.part_o + at(x) * DV) + lane);
-        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
-      } else {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(p.part_o + at(x) * DV) + lane);
-        o[0] = v.x, o[1] = v.y;
+  for (int s = 0; s < 2; ++s) {
+    row[s] = blockIdx.y * kJoinRows + 2 * warp + s;
+    const int side = row[s] / kM, rr = row[s] % kM, tok = rr / p.r;
+    const int t = side * p.tq + tok;
+    orow[s] = (row[s] < p.srows && tok < p.tq && t < ntok) ? t * p.h + (rr - tok * p.r) : -1;
+  }
+  if (orow[0] < 0 && orow[1] < 0) return;
+  float M[2] = {-INFINITY, -INFINITY}, den[2] = {0.f, 0.f}, num[2][CPL];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) num[s][e] = 0.f;
+  for (int x0 = c; x0 <= last; x0 += NP) {
+    float2 ml[2][NP];
+    float o[2][NP][CPL];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int x = x0 + k;
+        const bool use = x <= last && orow[s] >= 0;
+        const size_t at = static_cast<size_t>(2 * x + (x == c ? 1 : 0)) * p.srows + row[s];
+        ml[s][k] = use ? __ldg(reinterpret_cast<const float2*>(p.part_ml) + at)
+                       : make_float2(-INFINITY, 0.f);
+        const float* src = p.part_o + at * DV + lane * CPL;
+        if constexpr (CPL == 4) {
+          const float4 v = use ? __ldg(reinterpret_cast<const float4*>(src))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+          o[s][k][0] = v.x, o[s][k][1] = v.y, o[s][k][2] = v.z, o[s][k][3] = v.w;
+        } else {
+          const float2 v =
+              use ? __ldg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+          o[s][k][0] = v.x, o[s][k][1] = v.y;
+        }
       }
 #pragma unroll
-      for (int e = 0; e < CPL; ++e) num[e] = fmaf(wgt, o[e], num[e]);
+    for (int s = 0; s < 2; ++s) {
+      float mb = M[s];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) mb = fmaxf(mb, ml[s][k].x);
+      const float ref = mb == -INFINITY ? 0.f : mb;
+      const float sc = ex2(M[s] - ref);
+      den[s] *= sc;
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) num[s][e] *= sc;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        // (a piece that the row sees nothing of may not have been written)
+        if (ml[s][k].x == -INFINITY) continue;
+        const float wgt = ex2(ml[s][k].x - ref);
+        den[s] = fmaf(wgt, ml[s][k].y, den[s]);
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) num[s][e] = fmaf(wgt, o[s][k][e], num[s][e]);
+      }
+      M[s] = mb;
     }
-    const float inv = 1.f / den;
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (orow[s] < 0) continue;
+    const float inv = 1.f / den[s];
     T16* dst = static_cast<T16*>(p.out) +
-               (static_cast<size_t>(tok0 + t) * p.h + j * p.r + (rr - tok * p.r)) * DV +
-               lane * CPL;
+               (static_cast<size_t>(tok0) * p.h + j * p.r + orow[s]) * DV + lane * CPL;
     if constexpr (CPL == 4) {
       *reinterpret_cast<uint2*>(dst) =
-          make_uint2(Half16<T16>::pack2(num[0] * inv, num[1] * inv),
-                     Half16<T16>::pack2(num[2] * inv, num[3] * inv));
+          make_uint2(Half16<T16>::pack2(num[s][0] * inv, num[s][1] * inv),
+                     Half16<T16>::pack2(num[s][2] * inv, num[s][3] * inv));
     } else {
-      *reinterpret_cast<uint32_t*>(dst) = Half16<T16>::pack2(num[0] * inv, num[1] * inv);
+      *reinterpret_cast<uint32_t*>(dst) = Half16<T16>::pack2(num[s][0] * inv, num[s][1] * inv);
     }
   }
 }
@@ -1074,8 +1111,8 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p)) return e;
-  cfg.gridDim = dim3(num_sms, (pl.srows + 31) / 32);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(num_sms, (pl.srows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T16, DV>, p, num_sms);
 }
