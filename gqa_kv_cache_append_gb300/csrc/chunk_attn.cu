@@ -888,17 +888,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the units that a run's end cut: block (c, k) handles
-// rows [32 k, 32 k + 32) of the unit whose first piece is CTA c's, two rows to
-// a warp, four pieces of both at a time with their loads side by side (a row
-// after the other and a piece after the other took 12 us on cold caches).
+// side k of the unit whose first piece is CTA c's, 32 rows at a time, two to a
+// warp, four pieces of both with their loads side by side.  (A row after the
+// other and a piece after the other took 12 us on cold caches for a few rows,
+// this 7; blocks of 32 rows each, in eight waves, 21 us for the mixed batch's
+// 300 pieces.)
 // With per-piece maxima m, sums l and unnormalised outputs O over disjoint
 // positions: M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, in the
 // pieces' order.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 32;  // at a time
 
 template <typename T16, int DV>
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkParams p, int nc) {
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    chunk_join_kernel(const ChunkParams p, int nc) {
   constexpr int CPL = DV / 32;  // columns a lane
   constexpr int NP = 4;         // pieces at a time
   pdl_wait_then_release();
@@ -916,77 +919,79 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkPar
   }
   if (!d4.x || last < 0) return;  // (none cut here)
   const int tok0 = d4.y, ntok = d4.z, j = d4.w;
-  int row[2], orow[2];
+  for (int base = 0; base < kM; base += kJoinRows) {
+    int row[2], orow[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    row[s] = blockIdx.y * kJoinRows + 2 * warp + s;
-    const int side = row[s] / kM, rr = row[s] % kM, tok = rr / p.r;
-    const int t = side * p.tq + tok;
-    orow[s] = (row[s] < p.srows && tok < p.tq && t < ntok) ? t * p.h + (rr - tok * p.r) : -1;
-  }
-  if (orow[0] < 0 && orow[1] < 0) return;
-  float M[2] = {-INFINITY, -INFINITY}, den[2] = {0.f, 0.f}, num[2][CPL];
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) num[s][e] = 0.f;
-  for (int x0 = c; x0 <= last; x0 += NP) {
-    float2 ml[2][NP];
-    float o[2][NP][CPL];
+    for (int s = 0; s < 2; ++s) {
+      const int side = blockIdx.y, rr = base + 2 * warp + s, tok = rr / p.r;
+      const int t = side * p.tq + tok;
+      row[s] = side * kM + rr;
+      orow[s] = (tok < p.tq && t < ntok) ? t * p.h + (rr - tok * p.r) : -1;
+    }
+    if (orow[0] < 0 && orow[1] < 0) return;  // (later rows lie behind, too)
+    float M[2] = {-INFINITY, -INFINITY}, den[2] = {0.f, 0.f}, num[2][CPL];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int x = x0 + k;
-        const bool use = x <= last && orow[s] >= 0;
-        const size_t at = static_cast<size_t>(2 * x + (x == c ? 1 : 0)) * p.srows + row[s];
-        ml[s][k] = use ? __ldg(reinterpret_cast<const float2*>(p.part_ml) + at)
-                       : make_float2(-INFINITY, 0.f);
-        const float* src = p.part_o + at * DV + lane * CPL;
-        if constexpr (CPL == 4) {
-          const float4 v = use ? __ldg(reinterpret_cast<const float4*>(src))
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-          o[s][k][0] = v.x, o[s][k][1] = v.y, o[s][k][2] = v.z, o[s][k][3] = v.w;
-        } else {
-          const float2 v =
-              use ? __ldg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
-          o[s][k][0] = v.x, o[s][k][1] = v.y;
+      for (int e = 0; e < CPL; ++e) num[s][e] = 0.f;
+    for (int x0 = c; x0 <= last; x0 += NP) {
+      float2 ml[2][NP];
+      float o[2][NP][CPL];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const int x = x0 + k;
+          const bool use = x <= last && orow[s] >= 0;
+          const size_t at = static_cast<size_t>(2 * x + (x == c ? 1 : 0)) * p.srows + row[s];
+          ml[s][k] = use ? __ldg(reinterpret_cast<const float2*>(p.part_ml) + at)
+                         : make_float2(-INFINITY, 0.f);
+          const float* src = p.part_o + at * DV + lane * CPL;
+          if constexpr (CPL == 4) {
+            const float4 v = use ? __ldg(reinterpret_cast<const float4*>(src))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[s][k][0] = v.x, o[s][k][1] = v.y, o[s][k][2] = v.z, o[s][k][3] = v.w;
+          } else {
+            const float2 v =
+                use ? __ldg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+            o[s][k][0] = v.x, o[s][k][1] = v.y;
+          }
         }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float mb = M[s];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) mb = fmaxf(mb, ml[s][k].x);
+        const float ref = mb == -INFINITY ? 0.f : mb;
+        const float sc = ex2(M[s] - ref);
+        den[s] *= sc;
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) num[s][e] *= sc;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          // (a piece that the row sees nothing of may not have been written)
+          if (ml[s][k].x == -INFINITY) continue;
+          const float wgt = ex2(ml[s][k].x - ref);
+          den[s] = fmaf(wgt, ml[s][k].y, den[s]);
+#pragma unroll
+          for (int e = 0; e < CPL; ++e) num[s][e] = fmaf(wgt, o[s][k][e], num[s][e]);
+        }
+        M[s] = mb;
       }
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      float mb = M[s];
-#pragma unroll
-      for (int k = 0; k < NP; ++k) mb = fmaxf(mb, ml[s][k].x);
-      const float ref = mb == -INFINITY ? 0.f : mb;
-      const float sc = ex2(M[s] - ref);
-      den[s] *= sc;
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) num[s][e] *= sc;
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        // (a piece that the row sees nothing of may not have been written)
-        if (ml[s][k].x == -INFINITY) continue;
-        const float wgt = ex2(ml[s][k].x - ref);
-        den[s] = fmaf(wgt, ml[s][k].y, den[s]);
-#pragma unroll
-        for (int e = 0; e < CPL; ++e) num[s][e] = fmaf(wgt, o[s][k][e], num[s][e]);
+      if (orow[s] < 0) continue;
+      const float inv = 1.f / den[s];
+      T16* dst = static_cast<T16*>(p.out) +
+                 (static_cast<size_t>(tok0) * p.h + j * p.r + orow[s]) * DV + lane * CPL;
+      if constexpr (CPL == 4) {
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(Half16<T16>::pack2(num[s][0] * inv, num[s][1] * inv),
+                       Half16<T16>::pack2(num[s][2] * inv, num[s][3] * inv));
+      } else {
+        *reinterpret_cast<uint32_t*>(dst) = Half16<T16>::pack2(num[s][0] * inv, num[s][1] * inv);
       }
-      M[s] = mb;
-    }
-  }
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (orow[s] < 0) continue;
-    const float inv = 1.f / den[s];
-    T16* dst = static_cast<T16*>(p.out) +
-               (static_cast<size_t>(tok0) * p.h + j * p.r + orow[s]) * DV + lane * CPL;
-    if constexpr (CPL == 4) {
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(Half16<T16>::pack2(num[s][0] * inv, num[s][1] * inv),
-                     Half16<T16>::pack2(num[s][2] * inv, num[s][3] * inv));
-    } else {
-      *reinterpret_cast<uint32_t*>(dst) = Half16<T16>::pack2(num[s][0] * inv, num[s][1] * inv);
     }
   }
 }
@@ -1111,7 +1116,7 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p)) return e;
-  cfg.gridDim = dim3(num_sms, (pl.srows + kJoinRows - 1) / kJoinRows);
+  cfg.gridDim = dim3(num_sms, pl.srows / kM);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T16, DV>, p, num_sms);
