@@ -65,12 +65,12 @@ constexpr int kBatch = 4;  // rows a lane loads ahead of their use
 // behind it.  Measured (graph replay): one block per token, sines in shared
 // memory and a shuffle per exchanged element 58 us for 2 x 4096 fp16 tokens
 // and 113 us for 24 ragged sequences (11,290 tokens, h = 28); a warp per
-// token, the kind of a row chosen row by row 47 and 67 us; this form 40 and 48 us,
-// 5,040 and 4,360 GB/s.
+// token, the kind of a row chosen row by row 47 and 67 us; this form 37 and 46 us,
+// 5,420 and 4,550 GB/s.
 enum { ROW_Q = 0, ROW_K = 1, ROW_V = 2 };
 
 template <typename T, bool FP8, int GS>
-__global__ void __launch_bounds__(kRopeThreads, 8)
+__global__ void __launch_bounds__(kRopeThreads, FP8 ? 8 : 7)
     rope_append_kernel(const RopeLaunch a, int parts, int per_part) {
   constexpr int SIDE = 32 / GS;  // rows side by side
   pdl_wait_then_release();
@@ -169,17 +169,22 @@ __global__ void __launch_bounds__(kRopeThreads, 8)
       r[0].get(w);
       r[1].get(w + 4);
     }
-    // pair k of the lane: first element e0(k), second e1(k) of the eight;
-    // first' = first * A - second * B, second' = second * C + first * D
-    float A[4], B[4], C[4], D[4];
+    // Rotation two elements at a time, y = x * ca + x' * cb: for halves x is
+    // two first (second) elements and x' their mates, for pairs x is a pair
+    // and x' the pair turned around.  The weights are multiplied in.
+    float2 ca[4], cb[4];
     if (KIND != ROW_V && turns) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float w0 = halves ? w[k] : w[2 * k], w1 = halves ? w[4 + k] : w[2 * k + 1];
-        A[k] = w0 * cs[k];
-        B[k] = w1 * sn[k];
-        C[k] = w1 * cs[k];
-        D[k] = w0 * sn[k];
+        if (halves) {  // elements 2 k, 2 k + 1 of the eight: k < 2 first
+          const int m = 2 * (k & 1), o = k < 2 ? 4 : -4;
+          const float sg = k < 2 ? -1.f : 1.f;
+          ca[k] = make_float2(w[2 * k] * cs[m], w[2 * k + 1] * cs[m + 1]);
+          cb[k] = make_float2(sg * w[2 * k + o] * sn[m], sg * w[2 * k + 1 + o] * sn[m + 1]);
+        } else {  // pair k
+          ca[k] = make_float2(w[2 * k] * cs[k], w[2 * k + 1] * cs[k]);
+          cb[k] = make_float2(-w[2 * k + 1] * sn[k], w[2 * k] * sn[k]);
+        }
       }
     }
     for (int st = from; st < to; st += kBatch) {
@@ -190,36 +195,40 @@ __global__ void __launch_bounds__(kRopeThreads, 8)
         if (st + it >= to) break;  // (uniform)
         const int row = (st + it) * SIDE + grp;
         const bool mine = in && row < heads;
-        float v[8];
+        alignas(8) float v[8];
         x[it][0].get(v);
         x[it][1].get(v + 4);
+        float2* const v2 = reinterpret_cast<float2*>(v);
         float inv = 1.f;
         if (norm) {
-          float ss = v[0] * v[0];
+          float2 sq = mul2(v2[0], v2[0]);
 #pragma unroll
-          for (int k = 1; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+          for (int k = 1; k < 4; ++k) sq = fma2(v2[k], v2[k], sq);
+          float ss = sq.x + sq.y;
 #pragma unroll
           for (int o = GS / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           inv = rsqrtf(fmaf(ss, inv_d, a.eps));
         }
         if (KIND != ROW_V) {
-          if (halves) {
+          const float2 inv2 = make_float2(inv, inv);
+          if (norm) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float p = v[k] * inv, q = v[4 + k] * inv;
-              v[k] = fmaf(p, A[k], -(q * B[k]));
-              v[4 + k] = fmaf(q, C[k], p * D[k]);
-            }
+            for (int k = 0; k < 4; ++k) v2[k] = mul2(v2[k], inv2);
+          }
+          if (halves) {
+            float2 y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = fma2(v2[k], ca[k], mul2(v2[k ^ 2], cb[k]));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v2[k] = y[k];
           } else if (turns) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float p = v[2 * k] * inv, q = v[2 * k + 1] * inv;
-              v[2 * k] = fmaf(p, A[k], -(q * B[k]));
-              v[2 * k + 1] = fmaf(q, C[k], p * D[k]);
-            }
+            for (int k = 0; k < 4; ++k)
+              v2[k] = fma2(v2[k], ca[k], mul2(make_float2(v2[k].y, v2[k].x), cb[k]));
           } else if (norm) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= inv * w[k];
+            for (int k = 0; k < 4; ++k)
+              v2[k] = mul2(v2[k], make_float2(w[2 * k], w[2 * k + 1]));
           }
         }
         if (KIND == ROW_Q) {
