@@ -635,8 +635,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         at = at.next();
       }
       Todo nx = {0, {0, 0}, false};
+      // rounds in which both sides have a P.V and an S that is not their last
+      const int inner = min(cur.nt[0], cur.nt[1]) - 1;
       for (int t = 1; t <= cur.T && ok; ++t) {
         const Ring v = at, k = at.next();
+        if (t >= 2 && t < inner) {
+          // as below, with as little as can be between one side's products
+          // and the other's
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            ok = __all_sync(0xffffffffu,
+                            ok && (s == 1 || (wait(C::FULL + v.slot, v.phase) &&
+                                              wait(C::FULL + k.slot, k.phase))) &&
+                                wait(C::P_READY + s, pn[s] & 1));
+            ++pn[s];
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vb = v0 + v.slot * (C::SLOT >> 4), kb = k0 + k.slot * (C::SLOT >> 4);
+            const uint64_t qa = q0 + ((s * C::Q_BYTES) >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int e = 0; e < kN / 16; ++e)
+                mma_16_ts(C::T_O + s * 128, C::T_S + s * 128 + 8 * e, vb + e * (2048 >> 4), kIdescO,
+                          1u);
+              if (s == 1) mma_commit(BAR(C::EMPTY + v.slot));
+#pragma unroll
+              for (int e = 0; e < DK / 16; ++e) {
+                const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
+                mma_bf16(C::T_S + s * 128, qa + o, kb + o, kIdescS, e > 0 ? 1u : 0u);
+              }
+              mma_commit(BAR(C::S_FULL + s));
+              if (s == 1) mma_commit(BAR(C::EMPTY + k.slot));
+            }
+            __syncwarp();
+          }
+          at = k.next();
+          continue;
+        }
         if (t == cur.T) {
           nx = next_seg();
           primed = nx.T > 0 && !nx.twin;
