@@ -127,13 +127,15 @@ static_assert(sizeof(ChunkSeg) <= kSegBytes, "segment ring");
 // ring in shared memory.
 //
 // Work is counted in cached positions: a unit's is the position behind its
-// last token (half of it where it runs as twins) plus kUnitCost for what a
+// last token (three quarters of it where it runs as twins: two tiles of twins
+// were measured at 4,100 cycles, bound by their copies, a two-sided tile at
+// 2,780) plus kUnitCost for what a
 // unit costs however short it is (query rows in, first logits, output), so
 // the units of a sequence but the last form an arithmetic progression and sums
 // of them a closed form.  All units are laid end to end (sequences, KV heads,
 // blocks of query rows) and run c begins at c * W / nc, moved to a tile's
 // edge, or to the unit's when that is near.
-constexpr int kUnitCost = 192;
+constexpr int kUnitCost = 320;
 
 struct ChunkPos {  // a place in the order of all tiles
   int i, j, qt, lt;
@@ -176,7 +178,7 @@ struct ChunkWalk {
   }
   __device__ long long work(int nn, int Lk) const {
     const int nu = units(nn);
-    return last_twin(nn, nu) ? prefix(nu - 1, nn, Lk) + (Lk >> 1) + kUnitCost
+    return last_twin(nn, nu) ? prefix(nu - 1, nn, Lk) + ((3ll * Lk) >> 2) + kUnitCost
                              : prefix(nu, nn, Lk);
   }
   __device__ int tiles(int q, int nn, int Lk) const {
@@ -227,7 +229,8 @@ struct ChunkWalk {
         r.qt = q;
         const int ti = tiles(q, n, L);
         const bool tw = q == nu - 1 && last_twin(n, nu);
-        const int lt = static_cast<int>((rem - prefix(q, n, L)) >> (tw ? 6 : 7));
+        const long long in = rem - prefix(q, n, L);
+        const int lt = static_cast<int>((tw ? (in + in / 3) : in) >> 7);
         r.lt = lt <= near ? 0 : lt >= ti - near ? ti : lt;
         return r;
       }
