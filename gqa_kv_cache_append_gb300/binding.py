@@ -482,11 +482,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _here(x, stream):
     """(current device, stream handle) of a call whose first tensor is x; no
-    device (-2, which no tensor is on) when that is not a CUDA tensor."""
+    device (-2, which no tensor is on) when that is a host tensor."""
     if isinstance(x, torch.Tensor) and not x.is_cuda:
         return -2, 0
-    dev = torch.cuda.current_device() if isinstance(x, torch.Tensor) else -2
-    if stream is None and dev >= 0 and _raw_stream is not None:
+    dev = torch.cuda.current_device()
+    if stream is None and _raw_stream is not None:
         return dev, _raw_stream(dev)
     return dev, _stream(stream)
 

@@ -121,6 +121,7 @@ struct ChunkSeg {
 };
 
 static_assert(sizeof(ChunkSeg) <= kSegBytes, "segment ring");
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 
 // The run of work of one CTA, cut into segments of units.  The TMA warp walks
 // (warp-uniform values) and announces each segment to the others through a
@@ -129,10 +130,9 @@ static_assert(sizeof(ChunkSeg) <= kSegBytes, "segment ring");
 // Work is counted in cached positions: a unit's is the position behind its
 // last token (three quarters of it where it runs as twins: two tiles of twins
 // were measured at 4,100 cycles, bound by their copies, a two-sided tile at
-// 2,780) plus kUnitCost for what a
-// unit costs however short it is (query rows in, first logits, output), so
-// the units of a sequence but the last form an arithmetic progression and sums
-// of them a closed form.  All units are laid end to end (sequences, KV heads,
+// 2,610) plus kUnitCost for what a unit costs however short it is (6,590
+// cycles: query rows in, first logits, output), so the units of a sequence but
+// the last form an arithmetic progression and sums of them a closed form.  All units are laid end to end (sequences, KV heads,
 // blocks of query rows) and run c begins at c * W / nc, moved to a tile's
 // edge, or to the unit's when that is near.
 constexpr int kUnitCost = 320;
@@ -1141,6 +1141,12 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
+    // the split of registers must not ask for more than the launch brings: a
+    // warpgroup would wait for them for ever
+    cudaFuncAttributes fa;
+    if (cudaError_t e2 = cudaFuncGetAttributes(&fa, kern)) return e2;
+    if (fa.numRegs * kThreads < 256 * kRegsSoftmax + 128 * kRegsOther)
+      return cudaErrorLaunchOutOfResources;
     configured.fetch_or(1ull << dev);
   }
   cudaLaunchConfig_t cfg = {};

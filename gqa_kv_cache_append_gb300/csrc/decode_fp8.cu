@@ -427,11 +427,12 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         o[e] = fmaf(o[e], al[e], fmaf(lo[e], 1.f / kLo, hi[e]) * vf);
     };
 
-    while (ok && w.next(seg)) {
+    // A warp whose wait gave up walks on without waiting, reading or writing
+    // outputs: the warpgroup's named barriers need all its warps.
+    while (w.next(seg)) {
       const uint32_t qb = k & 1;
       const int first_new = seg.L - p.nq;  // position of new token 0
-      ok = __all_sync(0xffffffffu, wait(C::Q_FULL + qb, k >> 1));  // (the rows' factors)
-      if (!ok) break;
+      ok = __all_sync(0xffffffffu, ok && wait(C::Q_FULL + qb, k >> 1));  // (the rows' factors)
       m_own = -INFINITY;
 #pragma unroll
       for (int e = 0; e < HP; ++e) l[e] = o[e] = 0.f;
@@ -442,9 +443,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         const int valid = min(kTile, seg.L - lt * kTile);
         // (S_FULL comes after FULL_K, so the second wait is for the scales'
         // visibility alone)
-        ok = __all_sync(0xffffffffu, wait(C::S_FULL + nb, n >> 1) &&
+        ok = __all_sync(0xffffffffu, ok && wait(C::S_FULL + nb, n >> 1) &&
                                          wait(C::FULL_K + st, n / kRing));
-        if (!ok) break;
         tc_fence_after();
         const float* sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + st * 2 * kTile + row;
         float ks[2], vs[2];
@@ -564,12 +564,11 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         }
         // ---- V rows past L_i hold anything: zero them ----
         if (wg == 0 && valid < kTile) {
-          ok = __all_sync(0xffffffffu, wait(C::FULL_V + st, n / kRing));
-          if (!ok) break;
+          ok = __all_sync(0xffffffffu, ok && wait(C::FULL_V + st, n / kRing));
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int pr = row + hf * kHalf;
-            if (pr >= valid) {
+            if (ok && pr >= valid) {
               const uint32_t dst = s_base + st * C::STAGE + C::K_BYTES + pr * DV;
 #pragma unroll
               for (int c = 0; c < DV / 16; ++c)
@@ -584,9 +583,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         if (lane == 0) mbar_arrive(BAR(C::P_READY + nb));
         if (lt > seg.lt0) correct(n - 1);
         if (lt == seg.lt1 - 1) correct(n);
-        if (!ok) break;
       }
-      if (!ok) break;
       ++k;
       if (lane == 0) mbar_arrive(BAR(C::Q_EMPTY + qb));
       // ---- segment end: the row sums across the warpgroup, then the output
@@ -622,7 +619,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
 #pragma unroll
       for (int e = 0; e < HP; ++e) {
         const int a = h0 + e;
-        if (a < nr) {
+        if (ok && a < nr) {
           const float4 v = *reinterpret_cast<const float4*>(rb + 4 * e);
           const float sum = (v.x + v.y) + (v.z + v.w);
           if (whole) {

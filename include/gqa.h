@@ -75,7 +75,8 @@ extern "C" {
 #define GQA_ERR_CUDA        -6  /* a CUDA runtime call failed */
 #define GQA_ERR_DEVICE      -7  /* current device is not sm_103 */
 #define GQA_ERR_SCRATCH_LIMIT -8 /* gqa_decode_attn_noalloc: the call needs more
-                                    scratch than its fixed device buffer holds */
+                                    scratch than its fixed device buffer holds;
+                                    calls with a workspace: it is too small */
 
 /* flags of gqa_decode_step */
 #define GQA_STEP_EARLY_STREAM 1 /* see gqa_decode_step */
@@ -444,7 +445,8 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  * decrease is skipped and sets GQA_DEV_BAD_TOKENS (rows that the entries give
  * to two sequences are unspecified; no access leaves the tensors).  Paged caches, block
  * tables and block sizes are those of the paged calls above.  These calls
- * keep nothing between them: scratch memory is passed in.
+ * keep nothing between them: scratch memory is passed in.  (As elsewhere, the
+ * first call on a device comes before a stream capture.)
  *
  * gqa_rope_table - host only: the position table of gqa_rope_append.
  *
