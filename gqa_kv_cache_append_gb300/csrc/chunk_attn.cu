@@ -413,13 +413,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (ok && w.next(seg)) {
       announce(seg);
-      const int* trow =
-          PAGED ? p.table + static_cast<size_t>(seg.i) * p.max_blocks : nullptr;
+      // the sequence's table entries, 64 at a time ahead of their use (a load
+      // before each tile's copies costs up to 3,200 cycles where the cache's
+      // stream has pushed the table out of L2)
+      PageCursor pc;
+      if (PAGED)
+        pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
+                 (seg.L + p.bsz - 1) / p.bsz, seg.lt0 * kN / p.bsz);
       // lane mm < sub: the pool row of box mm of tile lt
       auto lookup = [&](int lt) -> int {
         const int pm = lt * kN + lane * box;
+        const int blk = pc.get_lanes(lt * kN / p.bsz);
         if (lane >= sub || pm >= seg.L) return oob_row;
-        const int blk = __ldg(trow + pm / p.bsz);
         if (blk < 0 || blk >= p.num_blocks) {
           atomicOr(p.status, GQA_DEV_BAD_BLOCK);
           return oob_row;

@@ -23,7 +23,8 @@
 //
 // Roles (one persistent CTA per SM; 128 threads and 128 for every eight rows):
 //   warp 0     TMA: K and V rows of a tile (boxes of a block's rows, 128- or
-//              64-byte swizzle) into a three-stage ring, one lane per block
+//              64-byte swizzle) into a three-stage ring, one lane per block;
+//              the tile's scales by 16-byte copies
 //   warp 1     issues the S products, warp 2 the O products
 //   warp 3     splits a segment's query rows into e4m3 pieces in shared
 //              memory, up to two segments ahead
@@ -78,7 +79,8 @@ struct F8Cfg {
   static constexpr int OFF_VMAX = OFF_QS + 2 * NR * 4;          // float [2][NWG]
   static constexpr int OFF_COL = (OFF_VMAX + 2 * NWG * 4 + 15) / 16 * 16;  // int [2][NR]
   static constexpr int OFF_BAR = (OFF_COL + 2 * NR * 4 + 15) / 16 * 16;
-  static constexpr int FULL_K = 0, FULL_V = kRing, EMPTY = 2 * kRing, Q_FULL = 3 * kRing,
+  static constexpr int FULL_K = 0, FULL_V = kRing, EMPTY = 2 * kRing, SC_FULL = 3 * kRing,
+                       Q_FULL = 4 * kRing,
                        Q_EMPTY = Q_FULL + 2, S_FULL = Q_EMPTY + 2, S_FREE = S_FULL + 2,
                        P_READY = S_FREE + 2, O_FULL = P_READY + 2, O_FREE = O_FULL + 2,
                        DRAIN = O_FREE + 2, NBAR = DRAIN + 1;
@@ -153,7 +155,12 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     for (int k = 0; k < C::NBAR; ++k) {
       const bool by_warps = (k >= C::S_FREE && k < C::O_FULL) || (k >= C::O_FREE && k < C::DRAIN);
       const bool q_empty = k >= C::Q_EMPTY && k < C::S_FULL;  // softmax warps, last S product
-      mbar_init(BAR(k), k == C::DRAIN ? 2 : by_warps ? 4 * NWG : q_empty ? 4 * NWG + 1 : 1);
+      const bool scales = k >= C::SC_FULL && k < C::Q_FULL;  // the copying warp's lanes
+      mbar_init(BAR(k), k == C::DRAIN ? 2
+                        : scales      ? 32
+                        : by_warps    ? 4 * NWG
+                        : q_empty     ? 4 * NWG + 1
+                                      : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -195,29 +202,28 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     uint32_t n = 0;
     bool ok = true;
     while (ok && w.next(seg)) {
-      const int* trow = p.table + static_cast<size_t>(seg.i) * p.max_blocks;
-      auto lookup = [&](int lt) -> int {
-        const int pm = lt * kTile + lane * box;
-        if (lane >= sub || pm >= seg.L) return oob_row;
-        const int blk = __ldg(trow + pm / p.bsz);
-        if (blk < 0 || blk >= p.num_blocks) {
-          atomicOr(p.status, GQA_DEV_BAD_BLOCK);
-          return oob_row;
-        }
-        return (blk * p.g + seg.j) * p.bsz + pm % p.bsz;
-      };
-      int row = lookup(seg.lt0);
+      // the sequence's table entries, 64 at a time ahead of their use: looked
+      // up tile by tile, the load from a table that the cache's stream has
+      // pushed out of L2 took 3,200 cycles before each tile's copies
+      PageCursor pc;
+      pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks, (seg.L + p.bsz - 1) / p.bsz,
+               seg.lt0 * kTile / p.bsz);
       for (int lt = seg.lt0; lt < seg.lt1; ++lt, ++n) {
-        const int cur = row;
-        if (lt + 1 < seg.lt1) row = lookup(lt + 1);
+        // the tile's blocks, one a lane; lane mm < sub: the pool row of box mm
+        const int ent = pc.get_lanes(lt * kTile / p.bsz);
+        const int pm = lt * kTile + lane * box;
+        int cur = oob_row;
+        if (lane < sub && pm < seg.L) {
+          if (ent >= 0 && ent < p.num_blocks)
+            cur = (ent * p.g + seg.j) * p.bsz + pm % p.bsz;
+          else
+            atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+        }
         const int st = n % kRing;
-        // the scales of blocks in use (the others' are taken as 0)
-        const bool has = lane < sub && cur != oob_row;
-        const uint32_t sc_bytes = 8u * box * __popc(__ballot_sync(0xffffffffu, has));
         ok = __all_sync(0xffffffffu, wait(C::EMPTY + st, ((n / kRing) & 1) ^ 1));
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(BAR(C::FULL_K + st), C::K_BYTES + sc_bytes);
+          mbar_arrive_expect_tx(BAR(C::FULL_K + st), C::K_BYTES);
           mbar_arrive_expect_tx(BAR(C::FULL_V + st), C::V_BYTES);
         }
         __syncwarp();
@@ -226,13 +232,24 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           tma_load_2d(dst + lane * box * DK, &tm_k, BAR(C::FULL_K + st), 0, cur, pol);
           tma_load_2d(dst + C::K_BYTES + lane * box * DV, &tm_v, BAR(C::FULL_V + st), 0, cur, pol);
         }
-        if (has) {
-          const uint32_t sc = s_base + C::OFF_SC + (st * 2 * kTile + lane * box) * 4;
-          bulk_load(sc, p.k_scale + cur, box * 4, BAR(C::FULL_K + st));
-          bulk_load(sc + kTile * 4, p.v_scale + cur, box * 4, BAR(C::FULL_K + st));
+        // the scales of this lane's eight positions (past L_i, or through a
+        // bad entry: none).  Four instructions a tile: a bulk copy takes the
+        // warp that issues it ~100 cycles, and two more per block beside K's
+        // and V's made this warp the bound with 32-row blocks.
+        const int pos = lt * kTile + lane * 8;
+        const int blk = __shfl_sync(0xffffffffu, ent, min(31, lane * 8 / p.bsz));
+        if (pos < seg.L && blk >= 0 && blk < p.num_blocks) {
+          const size_t at = (static_cast<size_t>(blk) * p.g + seg.j) * p.bsz + pos % p.bsz;
+          const uint32_t sd = s_base + C::OFF_SC + (st * 2 * kTile + lane * 8) * 4;
+          async_copy16(sd, p.k_scale + at);
+          async_copy16(sd + 16, p.k_scale + at + 4);
+          async_copy16(sd + kTile * 4, p.v_scale + at);
+          async_copy16(sd + kTile * 4 + 16, p.v_scale + at + 4);
         }
+        async_copies_arrive(BAR(C::SC_FULL + st));
       }
     }
+    async_copies_wait();
     if (!ok) {  // copies in flight must land before the CTA exits (bounded)
       const long long t0 = clock64();
       for (int s = 0; s < kRing; ++s) {
@@ -319,11 +336,13 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     __syncwarp();
   } else if (warp == 3) {
     // ============================ query rows ==============================
-    constexpr int EPL = DK / 32;  // elements a lane; a warp to a row, four rows at a time
+    constexpr int EPL = DK / 32;  // elements a lane; a warp to a row, eight rows at a time
     uint32_t k = 0;
+    bool ok = true;
     while (w.next(seg)) {
       const uint32_t qb = k & 1;
-      if (!__all_sync(0xffffffffu, wait(C::Q_EMPTY + qb, (k >> 1) ^ 1))) break;
+      ok = __all_sync(0xffffffffu, wait(C::Q_EMPTY + qb, (k >> 1) ^ 1));
+      if (!ok) break;
       const __nv_bfloat16* q0 =
           p.q + (static_cast<size_t>(seg.i) * p.nq * p.h + seg.j * p.r) * DK + lane * EPL;
       uint8_t* dst = sm + C::OFF_Q + qb * C::Q_BYTES;
@@ -441,10 +460,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         const uint32_t nb = n & 1;
         const int st = n % kRing;
         const int valid = min(kTile, seg.L - lt * kTile);
-        // (S_FULL comes after FULL_K, so the second wait is for the scales'
-        // visibility alone)
         ok = __all_sync(0xffffffffu, ok && wait(C::S_FULL + nb, n >> 1) &&
-                                         wait(C::FULL_K + st, n / kRing));
+                                         wait(C::SC_FULL + st, n / kRing));
         tc_fence_after();
         const float* sc = reinterpret_cast<const float*>(sm + C::OFF_SC) + st * 2 * kTile + row;
         float ks[2], vs[2];

@@ -20,6 +20,18 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// 16 bytes global -> shared without passing registers; the arrival of all of
+// this thread's earlier ones on an mbarrier (one of its count); their end
+__device__ __forceinline__ void async_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void async_copies_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // packed tokens: sequence i's new tokens are rows cu[i] .. cu[i + 1] - 1
 // ---------------------------------------------------------------------------
