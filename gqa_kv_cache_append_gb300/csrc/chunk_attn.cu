@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int oob_row = PAGED ? p.num_blocks * p.g * p.bsz : 0;
     const int box = PAGED ? min(p.bsz, kN) : kN;
     const int sub = kN / box;  // boxes a tile and 64-column half
+    const int sh = PAGED ? __ffs(p.bsz) - 1 : 0, mask = p.bsz - 1;  // (a power of two)
     uint32_t slot_n = 0, qn[2] = {0, 0}, edge_n = 0;
     uint32_t kn = 0;  // segments announced
     bool ok = __all_sync(0xffffffffu, wait(C::RUN_END, 0));
@@ -419,17 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       PageCursor pc;
       if (PAGED)
         pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
-                 (seg.L + p.bsz - 1) / p.bsz, seg.lt0 * kN / p.bsz);
+                 static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh), (seg.lt0 * kN) >> sh);
       // lane mm < sub: the pool row of box mm of tile lt
       auto lookup = [&](int lt) -> int {
         const int pm = lt * kN + lane * box;
-        const int blk = pc.get_lanes(lt * kN / p.bsz);
+        const int blk = pc.get_lanes((lt * kN) >> sh);
         if (lane >= sub || pm >= seg.L) return oob_row;
         if (blk < 0 || blk >= p.num_blocks) {
           atomicOr(p.status, GQA_DEV_BAD_BLOCK);
           return oob_row;
         }
-        return (blk * p.g + seg.j) * p.bsz + pm % p.bsz;
+        return (blk * p.g + seg.j) * p.bsz + (pm & mask);
       };
       auto load_q = [&](int side) {
         if (!ok || seg.side_tiles(side, p.tq) == 0) return;

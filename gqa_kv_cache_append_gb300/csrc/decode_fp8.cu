@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     const int oob_row = p.num_blocks * p.g * p.bsz;
     const int box = min(p.bsz, kTile);
     const int sub = kTile / box;  // boxes a tile
+    const int sh = __ffs(p.bsz) - 1, mask = p.bsz - 1;  // (a power of two)
     uint32_t n = 0;
     bool ok = true;
     while (ok && w.next(seg)) {
@@ -206,16 +207,17 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
       // up tile by tile, the load from a table that the cache's stream has
       // pushed out of L2 took 3,200 cycles before each tile's copies
       PageCursor pc;
-      pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks, (seg.L + p.bsz - 1) / p.bsz,
-               seg.lt0 * kTile / p.bsz);
+      pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
+               static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
+               (seg.lt0 * kTile) >> sh);
       for (int lt = seg.lt0; lt < seg.lt1; ++lt, ++n) {
         // the tile's blocks, one a lane; lane mm < sub: the pool row of box mm
-        const int ent = pc.get_lanes(lt * kTile / p.bsz);
+        const int ent = pc.get_lanes((lt * kTile) >> sh);
         const int pm = lt * kTile + lane * box;
         int cur = oob_row;
         if (lane < sub && pm < seg.L) {
           if (ent >= 0 && ent < p.num_blocks)
-            cur = (ent * p.g + seg.j) * p.bsz + pm % p.bsz;
+            cur = (ent * p.g + seg.j) * p.bsz + (pm & mask);
           else
             atomicOr(p.status, GQA_DEV_BAD_BLOCK);
         }
@@ -237,9 +239,9 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         // warp that issues it ~100 cycles, and two more per block beside K's
         // and V's made this warp the bound with 32-row blocks.
         const int pos = lt * kTile + lane * 8;
-        const int blk = __shfl_sync(0xffffffffu, ent, min(31, lane * 8 / p.bsz));
+        const int blk = __shfl_sync(0xffffffffu, ent, (lane * 8) >> sh);
         if (pos < seg.L && blk >= 0 && blk < p.num_blocks) {
-          const size_t at = (static_cast<size_t>(blk) * p.g + seg.j) * p.bsz + pos % p.bsz;
+          const size_t at = (static_cast<size_t>(blk) * p.g + seg.j) * p.bsz + (pos & mask);
           const uint32_t sd = s_base + C::OFF_SC + (st * 2 * kTile + lane * 8) * 4;
           async_copy16(sd, p.k_scale + at);
           async_copy16(sd + 16, p.k_scale + at + 4);
