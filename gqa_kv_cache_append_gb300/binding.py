@@ -572,9 +572,9 @@ def gqa_rope_append(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_cache, v_cach
         cap = k_cache.shape[2]
     ty = _TORCH.get(dt, ())
     _launch("gqa_rope_append", lib.gqa_rope_append, *args,
-          _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
-          _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev),
-          int(b), int(total), int(h), int(g), int(d_k), int(d_v), int(cap), dt, st)
+            _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
+            _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev),
+            int(b), int(total), int(h), int(g), int(d_k), int(d_v), int(cap), dt, st)
 
 
 def _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, ty, dev):
@@ -599,7 +599,7 @@ def gqa_rope_append_paged(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_pool, v
     kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v,
                                     _TORCH.get(dt, ()), dev)
     _launch("gqa_rope_append_paged", lib.gqa_rope_append_paged, *args, kp, vp, tp, int(b),
-          int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, st)
+            int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, st)
 
 
 def _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g, d_k, d_v, dev):
@@ -626,7 +626,7 @@ def gqa_rope_append_fp8_paged(q, k_new, v_new, cu_tokens, seq_lens, q_out, k_poo
     kp, vp, ks, vs, tp, bs, mb, nb = _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g,
                                              d_k, d_v, dev)
     _launch("gqa_rope_append_fp8_paged", lib.gqa_rope_append_fp8_paged, *args, kp, vp, ks, vs, tp,
-          int(b), int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, st)
+            int(b), int(total), int(h), int(g), int(d_k), int(d_v), bs, mb, nb, dt, st)
 
 
 def gqa_kv_read_fp8_paged(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, k_cache,
@@ -641,10 +641,10 @@ def gqa_kv_read_fp8_paged(k_pool, v_pool, k_scale, v_scale, block_table, seq_len
     kp, vp, ks, vs, tp, bs, mb, nb = _pools8(k_pool, v_pool, k_scale, v_scale, block_table, b, g,
                                              d_k, d_v, dev)
     _launch("gqa_kv_read_fp8_paged", lib.gqa_kv_read_fp8_paged, kp, vp, ks, vs, tp,
-          _tensor(seq_lens, "seq_lens", b, _I32, dev),
-          _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
-          _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev), int(b), int(g), int(d_k),
-          int(d_v), bs, mb, nb, int(cap), dt, st)
+            _tensor(seq_lens, "seq_lens", b, _I32, dev),
+            _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
+            _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev), int(b), int(g), int(d_k),
+            int(d_v), bs, mb, nb, int(cap), dt, st)
 
 
 def gqa_chunk_attn_workspace(total, h, g, d_k, d_v, num_sms=0) -> int:
@@ -689,15 +689,15 @@ def gqa_chunk_attn(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, 
         total = q.shape[0]
     if cap is None:
         cap = k_cache.shape[2]
-    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g, d_k,
-                               d_v)
+    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g,
+                               d_k, d_v)
     _launch("gqa_chunk_attn", lib.gqa_chunk_attn, _tensor(q, "q", total * h * d_k, ty, dev),
-          _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
-          _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev),
-          _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
-          _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
-          int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev),
-          int(cap), dt, wp, wn, st)
+            _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
+            _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev),
+            _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
+            _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
+            int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev),
+            int(cap), dt, wp, wn, st)
 
 
 def gqa_chunk_attn_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k, d_v,
@@ -710,14 +710,14 @@ def gqa_chunk_attn_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b,
     if total is None:
         total = q.shape[0]
     kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, ty, dev)
-    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g, d_k,
-                               d_v)
+    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g,
+                               d_k, d_v)
     _launch("gqa_chunk_attn_paged", lib.gqa_chunk_attn_paged,
-          _tensor(q, "q", total * h * d_k, ty, dev), kp, vp, tp,
-          _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
-          _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
-          int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev), bs,
-          mb, nb, dt, wp, wn, st)
+            _tensor(q, "q", total * h * d_k, ty, dev), kp, vp, tp,
+            _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
+            _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
+            int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev), bs,
+            mb, nb, dt, wp, wn, st)
 
 
 def gqa_decode_attn_fp8_workspace(b, n, h, g, d_k, d_v, cap, num_sms=0) -> int:

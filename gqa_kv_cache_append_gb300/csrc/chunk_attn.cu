@@ -21,7 +21,9 @@
 // Roles (384 threads, one persistent CTA per SM):
 //   warps 0-3  softmax of side A, output; thread = query row = TMEM lane
 //   warps 4-7  the same for side B
-//   warp 8     one lane issues every product
+//   warp 8     issues every product: the whole warp walks the loop and one
+//              elected lane issues (from one lane's branch eight products took
+//              460 cycles to issue, as long as they run)
 //   warp 10    TMA: the sides' query rows once per unit, K and V tiles into a
 //              ring (64-column boxes, 128-byte swizzle)
 //   warp 11    the run's end (the TMA warp finds its start meanwhile)
@@ -37,6 +39,13 @@
 // output, all fp32) in the workspace, and a second small kernel joins them.
 //
 // Rows >= L_i: masked out of S, their V rows zeroed in shared memory.
+//
+// Bound by the tensor cores where units are long: a prompt of 8,192 tokens,
+// h = 64, g = 8, d = 128, bf16: 648 us, 1,696 TFLOP/s (graph replay); what the
+// pipe still waits for is a side's own chain of S, softmax and hand-over, which
+// is a little longer than the other side's products.  Short units are bound
+// by their fixed cost (query rows in, first logits, output): 135 us for 32
+// mixed sequences of 5,957 tokens, 17.5 us for eight chunks of 4 to 12.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -74,7 +83,8 @@ struct ChunkCfg {
   static constexpr int OFF_BAR = OFF_RING + NS * SLOT;
   static constexpr int FULL = 0, EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
                        S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
-                       SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs, V_EDGE = SEG_EMPTY + kSegs,
+                       SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs,
+                       V_EDGE = SEG_EMPTY + kSegs,
                        TWIN = V_EDGE + 1, RUN_END = TWIN + 2, DRAIN = RUN_END + 1, NBAR = DRAIN + 1;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
   static constexpr int OFF_ML = OFF_SEG + kSegs * kSegBytes;  // float2 [2][kM]: twins' maxima, sums
@@ -132,9 +142,11 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register
 // were measured at 4,100 cycles, bound by their copies, a two-sided tile at
 // 2,610) plus kUnitCost for what a unit costs however short it is (6,590
 // cycles: query rows in, first logits, output), so the units of a sequence but
-// the last form an arithmetic progression and sums of them a closed form.  All units are laid end to end (sequences, KV heads,
-// blocks of query rows) and run c begins at c * W / nc, moved to a tile's
-// edge, or to the unit's when that is near.
+// the last form an arithmetic progression and sums of them a closed form.  All
+// units are laid end to end (sequences, KV heads, blocks of query rows) and run
+// c begins at c * W / nc, moved to a tile's edge, or to the unit's when that is
+// near.  (With half the work for twins and a cost of 192 the prompt takes 675 us
+// where this takes 650.)
 constexpr int kUnitCost = 320;
 
 struct ChunkPos {  // a place in the order of all tiles
@@ -414,13 +426,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (ok && w.next(seg)) {
       announce(seg);
-      // the sequence's table entries, 64 at a time ahead of their use (a load
-      // before each tile's copies costs up to 3,200 cycles where the cache's
-      // stream has pushed the table out of L2)
+      // the sequence's table entries, 64 at a time ahead of their use: no load
+      // stands before a tile's copies
       PageCursor pc;
       if (PAGED)
         pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
-                 static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh), (seg.lt0 * kN) >> sh);
+                 static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
+                 (seg.lt0 * kN) >> sh);
       // lane mm < sub: the pool row of box mm of tile lt
       auto lookup = [&](int lt) -> int {
         const int pm = lt * kN + lane * box;
@@ -869,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // is aligned to them.  (Rows turned in shared memory or by shuffles
       // between four lanes touch fewer lines a store but cost more
       // instructions: 155 and 149 us for a mixed batch of prompts, chunks and
-      // single tokens against 142.)
+      // single tokens where this took 142.)
       T16* const dst = static_cast<T16*>(p.out) +
                        (static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head) * DV;
       float* const pdst = p.part_o + (at + row) * DV;

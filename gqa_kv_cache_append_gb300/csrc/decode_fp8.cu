@@ -35,6 +35,12 @@
 //
 // The tiles of all units are laid end to end and dealt out evenly (Walker); a
 // unit cut between CTAs leaves partial results, joined by the combine kernel.
+//
+// Bound by HBM where sequences are many and long: b = 32, L = 8,192, h = 64,
+// g = 8, d = 128: 87 us, 6,370 GB/s (graph replay).  A few tiles a CTA: start,
+// first tile and join (24 ragged sequences of 512 to 32,766, g = 4, two tokens
+// of seven heads: 41 us, 3,700 GB/s; 32-row blocks also cost the TMA warp
+// sixteen copies a tile at ~100 cycles each).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -56,7 +62,7 @@ template <int NR, int DK, int DV>
 struct F8Cfg {
   // softmax warpgroups of eight query rows each: a warpgroup's time per tile
   // (one warp to a sub-partition, long dependent chains) is what bounds the
-  // loop.  Sixteen rows on one warpgroup: 51 us where two take 43 (24 ragged
+  // loop.  Sixteen rows on one warpgroup: 51 us where two took 43 (24 ragged
   // sequences of 512 to 32,766, g = 4, two tokens of seven heads)
   static constexpr int HP = 8;
   static constexpr int NWG = NR / HP;
@@ -203,9 +209,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     uint32_t n = 0;
     bool ok = true;
     while (ok && w.next(seg)) {
-      // the sequence's table entries, 64 at a time ahead of their use: looked
-      // up tile by tile, the load from a table that the cache's stream has
-      // pushed out of L2 took 3,200 cycles before each tile's copies
+      // the sequence's table entries, 64 at a time ahead of their use: no load
+      // stands before a tile's copies
       PageCursor pc;
       pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
                static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),

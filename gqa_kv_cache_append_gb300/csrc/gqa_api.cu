@@ -508,7 +508,8 @@ int paged_args_check(const int32_t* block_table, int g, int block_size, int max_
 bool encode_u8_map(CUtensorMap* map, const void* base, int d, uint64_t rows, uint32_t box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc || (d != 64 && d != 128)) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), rows}, st[1] = {static_cast<cuuint64_t>(d)};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), rows};
+  const cuuint64_t st[1] = {static_cast<cuuint64_t>(d)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(d), box_rows}, es[2] = {1u, 1u};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, st, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE,

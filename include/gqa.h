@@ -443,10 +443,10 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  * sequence with n_i > 0 and L_i outside [n_i, cap] is skipped and sets
  * GQA_DEV_BAD_SEQ_LEN; one whose cu_tokens entries are outside [0, total] or
  * decrease is skipped and sets GQA_DEV_BAD_TOKENS (rows that the entries give
- * to two sequences are unspecified; no access leaves the tensors).  Paged caches, block
- * tables and block sizes are those of the paged calls above.  These calls
- * keep nothing between them: scratch memory is passed in.  (As elsewhere, the
- * first call on a device comes before a stream capture.)
+ * to two sequences are unspecified; no access leaves the tensors).  Paged
+ * caches, block tables and block sizes are those of the paged calls above.
+ * These calls keep nothing between them: scratch memory is passed in.  (As
+ * elsewhere, the first call on a device comes before a stream capture.)
  *
  * gqa_rope_table - host only: the position table of gqa_rope_append.
  *
@@ -462,7 +462,7 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  *                        (2 log theta), the pair that turns t times over the
  *                        original length, first = max(floor(at(high)), 0),
  *                        last = min(ceil(at(low)), rot - 1) and x =
- *                        clamp((m - first) / (last - first), 0, 1):
+ *                        clamp((m - first) / max(last - first, 0.001), 0, 1):
  *                        (1 - x) f_m + x f_m / factor; rope_scale =
  *                        0.1 log(factor) + 1 for factor > 1
  * (0 < low < high, original_len > 0 for the last two.)
@@ -495,8 +495,8 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  *   [num_blocks, g, block_size, d_k] and v_pool [.., d_v] hold e4m3 values,
  *   k_scale and v_scale [num_blocks, g, block_size] fp32 one scale per row.
  *   A row x (in fp32, after norm and rotation) is stored as scale =
- *   max|x| / 448 and round-to-nearest e4m3(x * (448 / max|x|)); a row of zeros has
- *   scale 0.  d_k and d_v multiples of 16.  Rows that hold infinities or
+ *   max|x| / 448 and round-to-nearest e4m3(x * (448 / max|x|)); a row of zeros
+ *   has scale 0.  d_k and d_v multiples of 16.  Rows that hold infinities or
  *   NaN are stored as rows that hold NaN.  The scales are 16-byte aligned for
  *   gqa_decode_attn_fp8_paged.
  *
