@@ -324,3 +324,87 @@ def test_legacy_default_stream():
     assert B.gqa_device_status(0) == 0
     for i in range(3):
         e.check(i, 49, qo[50 * i + 49], out[50 * i + 49])
+
+
+def test_pools_past_32_bits():
+    """Blocks that begin past 2^32 elements of their pool (2^33 bytes of the
+    16-bit ones), beside blocks at its start."""
+    e = Engine(seed=7)
+    B, bf = e.B, torch.bfloat16
+    nb = (1 << 32) // (e.g * e.block * e.d) + 100
+    shape = (nb, e.g, e.block, e.d)
+    e.k, e.v = (torch.empty(shape, dtype=bf, device="cuda") for _ in range(2))
+    e.k8, e.v8 = (torch.empty(shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    e.ks, e.vs = (torch.empty(shape[:3], device="cuda") for _ in range(2))
+    e.table = torch.where(e.table % 3 == 0, e.table, nb - 1 - e.table).to(torch.int32)
+    for pool, fill in ((e.k, float("nan")), (e.v, float("nan")), (e.k8, 0x7F), (e.v8, 0x7F),
+                       (e.ks, float("nan")), (e.vs, float("nan"))):
+        pool[:100] = fill
+        pool[-100:] = fill
+    ns = [500, 33, 270]
+    e.lens.copy_(torch.tensor(ns, dtype=torch.int32))
+    t = sum(ns)
+    q, k, v = e.tokens(t)
+    qo, out = (torch.zeros((t, e.h, e.d), dtype=bf, device="cuda") for _ in range(2))
+    e.append(q, k, v, cu_of(ns), qo)
+    e.append(q, k, v, cu_of(ns), qo, fp8=True)
+    B.gqa_chunk_attn_paged(qo, e.k, e.v, e.table, cu_of(ns), e.lens, e.b, e.h, e.g, e.d, e.d,
+                           e.scale, out)
+    last = torch.stack([qo[sum(ns[:i + 1]) - 1] for i in range(3)])
+    o8 = torch.zeros_like(last)
+    B.gqa_decode_attn_fp8_paged(last, e.k8, e.v8, e.ks, e.vs, e.table, e.lens, e.b, e.h, e.g,
+                                e.d, e.d, e.scale, o8)
+    kc, vc = (torch.zeros((e.b, e.g, 512, e.d), dtype=bf, device="cuda") for _ in range(2))
+    B.gqa_kv_read_fp8_paged(e.k8, e.v8, e.ks, e.vs, e.table, e.lens, kc, vc, e.b, e.g, e.d, e.d)
+    assert B.gqa_device_status() == 0
+    at = 0
+    for i, n in enumerate(ns):
+        assert torch.equal(e.rows(e.v, i, n).transpose(0, 1), v[at:at + n])
+        for s in range(0, n, 61):
+            e.check(i, s, qo[at + s], out[at + s])
+        e.check(i, n - 1, qo[at + n - 1], out[at + n - 1])
+        e.check(i, n - 1, last[i], o8[i], fp8=True)
+        want = e.rows(e.v8, i, n, e.vs).float().to(bf)  # (the product in fp32, then bf16)
+        assert torch.equal(vc[i, :, :n], want)
+        at += n
+
+
+def test_cache_past_32_bits():
+    """A contiguous cache of more than 2^32 elements: a sequence of 33 million
+    positions, whose heads each look for rows far apart, and one behind it."""
+    B, bf = _b(), torch.bfloat16
+    gen = torch.Generator("cuda").manual_seed(8)
+    h, d, cap, ns = 8, 64, (1 << 25) + 40, [3, 5]
+    ls = [cap, 200]
+    k, v = (torch.randn((2, 1, cap, d), generator=gen, device="cuda", dtype=bf) for _ in range(2))
+    cu, lens = cu_of(ns), torch.tensor(ls, dtype=torch.int32, device="cuda")
+    q, kn, vn = (torch.randn((8, n, d), generator=gen, device="cuda", dtype=bf)
+                 for n in (h, 1, 1))
+    # (no outlier in length: |q| = 8: a query's logit with four times itself is 32)
+    q = (q.float() * 8 / q.float().norm(dim=-1, keepdim=True)).to(bf)
+    phase, factor = B.gqa_rope_table(d, 500000.0)
+    qo, out = (torch.zeros_like(q) for _ in range(2))
+    B.gqa_rope_append(q, kn, vn, cu, lens, qo, k, v, 2, h, 1, d, d, rope=phase,
+                      rope_scale=factor)
+    # the appended rows: the angle is the table's turns times the position
+    for i, (at, n, l) in enumerate(((0, 3, ls[0]), (3, 5, ls[1]))):
+        assert torch.equal(v[i, 0, l - n:l], vn[at:at + n, 0])
+        for s in range(n):
+            pos = l - n + s
+            ang = torch.tensor([(int(f) % (1 << 64)) * pos % (1 << 64) / 2.0 ** 64 * 2 * math.pi
+                                for f in phase.tolist()], dtype=torch.float64, device="cuda")
+            x = kn[at + s, 0].double()
+            a, c = x[:d // 2], x[d // 2:]
+            want = torch.cat([a * ang.cos() - c * ang.sin(), c * ang.cos() + a * ang.sin()])
+            err = 1e-6 * (a.abs() + c.abs()).repeat(2)
+            got = k[i, 0, pos].double()
+            assert ((got - want).abs() <= err + U * (want.abs() + err)).all()
+    # a row for each head of the first sequence's last token, far apart
+    for a in range(h):
+        k[0, 0, a * (cap - 4) // (h - 1)] = 4 * qo[2, a]
+    B.gqa_chunk_attn(qo, k, v, cu, lens, 2, h, 1, d, d, 0.125, out)
+    assert B.gqa_device_status() == 0
+    for at, i, pos in ((2, 0, cap - 1), (3, 1, 195), (7, 1, 199)):
+        o, a = attend(qo[at], k[i, :, :pos + 1], v[i, :, :pos + 1], 0.125)
+        err = (out[at].double() - o).abs()
+        assert (err <= U * o.abs() + U * a + 2.0 ** -6).all(), float(err.max())
