@@ -281,18 +281,19 @@ __global__ void __launch_bounds__(kRopeThreads, FP8 ? 8 : 7)
 // ---------------------------------------------------------------------------
 // e4m3 cache -> rows of the call's type: positions [64 x, 64 x + 64) of KV
 // head y of sequence z.  A thread takes one 16-byte piece of every
-// (256 / pieces)-th row, up to four rows of K and of V at a time with their
-// loads side by side.
-// Memory-bound: d + 4 bytes read and d * sizeof(T) written per row.
-// Six sequences of up to 4,849 positions, g = 8, d = 128, to bf16: 16.5 us,
-// 4,640 GB/s, 62 % of the issue slots for the conversions.
+// (256 / pieces)-th row, two rows of K and of V at a time with their loads
+// side by side.
+// Memory-bound: d + 4 bytes read and d * sizeof(T) written per row.  Six
+// sequences of up to 4,849 positions, g = 8, d = 128, to bf16: 15.2 us, 5,040
+// GB/s, 65 % of the issue slots for the conversions.  (Room for four rows side
+// by side, 64 registers and four blocks an SM: 16.5 us.)
 // ---------------------------------------------------------------------------
 constexpr int kReadRows = 64;
 constexpr int kReadThreads = 256;
 
 struct ReadRows {  // what a thread reads of one tensor
-  uint4 raw[4];
-  float sc[4];
+  uint4 raw[2];
+  float sc[2];
   unsigned use;    // bit u: row u is there
   int c, row0, step, d;
 
@@ -309,7 +310,7 @@ struct ReadRows {  // what a thread reads of one tensor
                        int num_blocks, unsigned int* status) {
     use = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       const int rr = row0 + base + u * step;
       if (row0 >= rows || rr >= rows) continue;
       const int p = p0 + rr;
@@ -328,7 +329,7 @@ struct ReadRows {  // what a thread reads of one tensor
   template <typename T>
   __device__ void store(T* __restrict__ dst, int base, bool sectors) const {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       if (!(use & (1u << u))) continue;
       T* to = dst + static_cast<size_t>(row0 + base + u * step) * d + 16 * c;
       const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
@@ -351,7 +352,7 @@ struct ReadRows {  // what a thread reads of one tensor
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kReadThreads)
+__global__ void __launch_bounds__(kReadThreads, 5)
     kv_read_fp8_kernel(const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
                        const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                        const int* __restrict__ table, const int* __restrict__ lens,
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kReadThreads)
   ReadRows k, v;
   k.start(dk);
   v.start(dv);
-  for (int kb = 0, vb = 0; kb < rows || vb < rows; kb += 4 * k.step, vb += 4 * v.step) {
+  for (int kb = 0, vb = 0; kb < rows || vb < rows; kb += 2 * k.step, vb += 2 * v.step) {
     k.load(k_pool, k_scale, trow, kb, p0, rows, g, j, bshift, num_blocks, status);
     v.load(v_pool, v_scale, trow, vb, p0, rows, g, j, bshift, num_blocks, status);
     k.store(k_cache + dst0 * dk, kb, sectors);
