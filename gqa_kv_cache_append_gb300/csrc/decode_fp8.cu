@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
   const uint32_t s_base = smem_u32(sm);
   if (s_base & 1023u) {  // never seen; the swizzled layouts need it
     if (threadIdx.x == 0) atomicOr(p.status, GQA_DEV_INTERNAL);
+    pdl_wait();  // (what follows this grid is ordered behind what it followed)
     return;
   }
   auto BAR = [&](int k) -> uint32_t { return s_base + C::OFF_BAR + 8u * k; };

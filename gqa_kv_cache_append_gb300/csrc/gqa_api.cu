@@ -143,16 +143,19 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     before += __shfl_xor_sync(0xffffffffu, before, o);
     ti += __shfl_xor_sync(0xffffffffu, ti, o);
   }
+  // The lengths were read before the wait: the decode kernel releases this
+  // launch only after the kernel ahead of it (which may write seq_lens) has
+  // completed.  The partials come from the decode kernel itself.  Every block
+  // waits, also one without a cut unit: the next launch on the stream (or the
+  // next node of a graph) is ordered behind this grid alone, and were no unit
+  // cut and no block waiting, this grid could end before the decode kernel.
+  pdl_wait();
   if (ti == 0) return;  // (uniform across the CTA)
   const long long W = all * g;
   const long long u0 = before * g + static_cast<long long>(j) * ti;
   long long c0, c1;
   unit_ctas(u0, u0 + ti, W, nc, c0, c1);
   if (c0 == c1) return;
-  // the lengths were read before the wait: the decode kernel releases this
-  // launch only after the kernel ahead of it (which may write seq_lens) has
-  // completed.  The partials come from the decode kernel itself.
-  pdl_wait();
   // this warp's pieces c0 + wid + 4k, in batches of 8 (every load of a batch
   // issued before any use); batches merge online (running max M, sums)
   constexpr int kBatch = 8;
