@@ -13,13 +13,23 @@
 //
 //   S^T [T x 2 NR]   = K8 . (Qhi, Qlo)^T               (tcgen05.mma, 2 x M=128)
 //   x[p, a]          = (Shi + Slo / 16) * ks[p] * qs[a] * scale * log2 e
-//   w[p, a]          = exp2(x - m_a),  l_a += w
-//   P[p, a]          = w * vs[p] * 256 / vmax          (vmax = max vs of the tile)
-//   O^T [d_v x 2 NR] = V8^T . (Phi, Plo)^T             (tcgen05.mma, M=128)
-//   o_a              = o_a * 2^(m_old - m) + (Ohi + Olo / 16) * vmax / 256
+//   y_a              = max_p x[p, a] + log2(vs[p] / vmax)    (vmax = max vs of the tile)
+//   w[p, a]          = exp2(x - y_a)
+//   P[p, a]          = w * vs[p] * 256 / vmax                (the largest is 256)
+//   O^T [d_v x 2 NR] = V8^T . (Phi, Plo)^T                   (tcgen05.mma, M=128)
+//   m_a              = max(m_old, y_a)                       (of the tiles so far)
+//   l_a              = l_a * 2^(m_old - m) + sum_p w * 2^(y_a - m)
+//   o_a              = o_a * 2^(m_old - m) + (Ohi + Olo / 16) * 2^(y_a - m) * vmax / 256
 //
 // qs[a] is a power of two that puts the row's largest value into [128, 256),
-// so scaling loses nothing; P's common factor does the same for a tile.
+// so scaling loses nothing.  The pieces of P have e4m3's short range, not
+// bf16's: below 2^-6 their step stays at 2^-13.  So P is taken against its own
+// tile's largest product of weight and V scale, and a term loses more than its
+// 8 bits only where it is below 2^-14 of the tile's largest (by 2^-22 of that
+// at most).  Taken against the running maximum and the largest scale apart,
+// one dominant early position with a small V row wiped out all later tiles:
+// 24 % of the output at 32,768 positions, 72 % at 131,072.  The logarithm only
+// picks y_a, which cancels; it is held at -64 or above, so w stays below 2^64.
 //
 // Roles (one persistent CTA per SM; 128 threads and 128 for every eight rows):
 //   warp 0     TMA: K and V rows of a tile (boxes of a block's rows, 128- or
@@ -78,12 +88,15 @@ struct F8Cfg {
   static constexpr int OFF_TAIL = OFF_Q + 2 * Q_BYTES;
   static constexpr int OFF_PAD = OFF_TAIL + (DV == 64 ? V_BYTES : 0);
   static constexpr int OFF_SC = OFF_PAD;                        // float [kRing][2][kTile]
-  static constexpr int OFF_RED = OFF_SC + kRing * 2 * kTile * 4;  // [NWG][2][HP + 1][4]
-  static constexpr int OFF_MAX = OFF_RED + NWG * 2 * (HP + 1) * 16;
-  static constexpr int OFF_ALPHA = OFF_MAX + 2 * NR * 4;        // float [2][NR]
-  static constexpr int OFF_QS = OFF_ALPHA + 2 * NR * 4;         // float [2][NR]
-  static constexpr int OFF_VMAX = OFF_QS + 2 * NR * 4;          // float [2][NWG]
-  static constexpr int OFF_COL = (OFF_VMAX + 2 * NWG * 4 + 15) / 16 * 16;  // int [2][NR]
+  static constexpr int OFF_RED = OFF_SC + kRing * 2 * kTile * 4;  // [NWG][2][HP][4]
+  // of a query row and tile: its reference y, the running maximum m, and the
+  // factors 2^(m_old - m) of what is held and 2^(y - m) of the tile's
+  static constexpr int OFF_REF = OFF_RED + NWG * 2 * HP * 16;   // float [2][NR] each
+  static constexpr int OFF_RUN = OFF_REF + 2 * NR * 4;
+  static constexpr int OFF_ALPHA = OFF_RUN + 2 * NR * 4;
+  static constexpr int OFF_PART = OFF_ALPHA + 2 * NR * 4;
+  static constexpr int OFF_QS = OFF_PART + 2 * NR * 4;          // float [2][NR]
+  static constexpr int OFF_COL = OFF_QS + 2 * NR * 4;           // int [2][NR]
   static constexpr int OFF_BAR = (OFF_COL + 2 * NR * 4 + 15) / 16 * 16;
   static constexpr int FULL_K = 0, FULL_V = kRing, EMPTY = 2 * kRing, SC_FULL = 3 * kRing,
                        Q_FULL = 4 * kRing,
@@ -113,6 +126,16 @@ struct F8Params {
   unsigned int* status;
   long long budget;
 };
+
+// N floats of shared memory (16-byte aligned) that every lane reads alike
+template <int N>
+__device__ __forceinline__ void load_all(float (&v)[N], const float* src) {
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(src + k);
+    v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
+  }
+}
 
 // e4m3 x e4m3 -> fp32 descriptor: D fp32, both formats 0, A / B transposed
 // (MN-major) or not
@@ -422,17 +445,19 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     const int bar_id = 1 + wg;
     const uint32_t lane_off = static_cast<uint32_t>(qd * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::T_S + h0, tO = tmem + lane_off + C::T_O + h0;
-    float* red = reinterpret_cast<float*>(sm + C::OFF_RED) + wg * 2 * (HP + 1) * 4;
-    float* max_sm = reinterpret_cast<float*>(sm + C::OFF_MAX);
+    float* red = reinterpret_cast<float*>(sm + C::OFF_RED) + wg * 2 * HP * 4;
+    float* ref_sm = reinterpret_cast<float*>(sm + C::OFF_REF);
+    float* run_sm = reinterpret_cast<float*>(sm + C::OFF_RUN);
     float* alpha_sm = reinterpret_cast<float*>(sm + C::OFF_ALPHA);
-    float* vmax_sm = reinterpret_cast<float*>(sm + C::OFF_VMAX);
+    float* part_sm = reinterpret_cast<float*>(sm + C::OFF_PART);
     float l[HP], o[HP];
+    float vm = 0.f, vm_last = 0.f;  // largest V scale of the tile, and of the one before
     float m_own = -INFINITY;  // running maximum of query row h0 + row (row < HP)
     uint32_t n = 0, k = 0;
     bool ok = true;
 
-    // o = o * alpha + tile mt's product
-    auto correct = [&](uint32_t mt) {
+    // o = o * alpha + tile mt's product, whose largest V scale is vt
+    auto correct = [&](uint32_t mt, float vt) {
       const uint32_t nb = mt & 1;
       ok = ok && __all_sync(0xffffffffu, wait(C::O_FULL + nb, mt >> 1));
       if (!ok) return;
@@ -447,11 +472,13 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::O_FREE + nb));
-      const float vf = vmax_sm[nb * NWG + wg] * (1.f / 256.f);
-      const float* al = alpha_sm + nb * NR + h0;
+      const float vf = vt * (1.f / 256.f);
+      float al[HP], pt[HP];
+      load_all(al, alpha_sm + nb * NR + h0);
+      load_all(pt, part_sm + nb * NR + h0);
 #pragma unroll
       for (int e = 0; e < HP; ++e)
-        o[e] = fmaf(o[e], al[e], fmaf(lo[e], 1.f / kLo, hi[e]) * vf);
+        o[e] = fmaf(o[e], al[e], fmaf(lo[e], 1.f / kLo, hi[e]) * (pt[e] * vf));
     };
 
     // A warp whose wait gave up walks on without waiting, reading or writing
@@ -479,19 +506,43 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           ks[hf] = in ? sc[hf * kHalf] : 0.f;
           vs[hf] = in ? sc[kTile + hf * kHalf] : 0.f;
         }
-        float x[2][HP];
+        float x[2][HP], lo[2][HP];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float lo[HP];
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int c = 0; c < HP; c += 8) {
             tmem_ld8(tS + (nb * 2 + hf) * N + c, &x[hf][c]);
-            tmem_ld8(tS + (nb * 2 + hf) * N + RP + c, lo + c);
+            tmem_ld8(tS + (nb * 2 + hf) * N + RP + c, &lo[hf][c]);
           }
-          tmem_wait_ld();
+        // the tile's largest V scale, every warp for itself (while S is
+        // on its way)
+        vm_last = vm;
+        vm = 0.f;
 #pragma unroll
-          for (int e = 0; e < HP; ++e) x[hf][e] = fmaf(lo[e], 1.f / kLo, x[hf][e]);
+        for (int hf = 0; hf < 2; ++hf) {
+          const int p0 = hf * kHalf + 4 * lane;
+          const float4 v = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(sm + C::OFF_SC) + (st * 2 + 1) * kTile + p0);
+          vm = fmaxf(vm, p0 < valid ? v.x : 0.f);
+          vm = fmaxf(vm, p0 + 1 < valid ? v.y : 0.f);
+          vm = fmaxf(vm, p0 + 2 < valid ? v.z : 0.f);
+          vm = fmaxf(vm, p0 + 3 < valid ? v.w : 0.f);
         }
+        vm = warp_max(vm);
+        // (scales so small that the factor would overflow: scaled up first)
+        const float up = vm < 0x1p-60f ? 0x1p60f : 1.f;
+        const float vinv = vm > 0.f ? __fdividef(256.f, vm * up) : 0.f;
+        float fv[2], lv[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          fv[hf] = vs[hf] * up * vinv;  // 256 vs / vmax
+          lv[hf] = fmaxf(__log2f(fv[hf]) - 8.f, -64.f);
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int e = 0; e < HP; ++e) x[hf][e] = fmaf(lo[hf][e], 1.f / kLo, x[hf][e]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::S_FREE + nb));
@@ -516,41 +567,37 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
             }
           }
         }
-        // ---- maxima over the tile's positions, and of the V scales ----
+        // ---- maxima over the tile's positions ----
         float mine = -INFINITY;
 #pragma unroll
         for (int e = 0; e < HP; ++e) {
-          const float wm = warp_max(fmaxf(x[0][e], x[1][e]));
+          const float wm = warp_max(fmaxf(x[0][e] + lv[0], x[1][e] + lv[1]));
           if (lane == e) mine = wm;
         }
-        const float wv = warp_max(fmaxf(vs[0], vs[1]));
-        if (lane == HP) mine = wv;
-        float* rb = red + nb * (HP + 1) * 4;
-        if (lane <= HP) rb[lane * 4 + wq] = mine;
+        float* rb = red + nb * HP * 4;
+        if (lane < HP) rb[lane * 4 + wq] = mine;
         named_bar_sync(bar_id, 128);
-        if (row <= HP) {
+        if (row < HP) {
           const float4 v = *reinterpret_cast<const float4*>(rb + 4 * row);
-          const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-          if (row < HP) {
-            const float mn = fmaxf(m_own, mx);
-            const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet
-            alpha_sm[nb * NR + h0 + row] = ex2(m_own - ref);
-            max_sm[nb * NR + h0 + row] = ref;
-            m_own = mn;
-          } else {
-            vmax_sm[nb * NWG + wg] = mx;
-          }
+          const float y = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+          const float mn = fmaxf(m_own, y);
+          const float run = mn == -INFINITY ? 0.f : mn;  // nothing seen yet
+          const int a = nb * NR + h0 + row;
+          ref_sm[a] = y == -INFINITY ? 0.f : y;          // nothing of this tile
+          run_sm[a] = run;
+          alpha_sm[a] = ex2(m_own - run);
+          part_sm[a] = ex2(y - run);
+          m_own = mn;
         }
         named_bar_sync(bar_id, 128);
-        const float vm = vmax_sm[nb * NWG + wg];
-        const float vinv = vm > 0.f ? 256.f / vm : 0.f;
-        const float* mx = max_sm + nb * NR + h0;
-        const float* al = alpha_sm + nb * NR + h0;
-        const float fv[2] = {vs[0] * vinv, vs[1] * vinv};
+        float ref[HP], al[HP], pt[HP];
+        load_all(ref, ref_sm + nb * NR + h0);
+        load_all(al, alpha_sm + nb * NR + h0);
+        load_all(pt, part_sm + nb * NR + h0);
 #pragma unroll
         for (int e = 0; e < HP; ++e) {
-          const float w0 = ex2(x[0][e] - mx[e]), w1 = ex2(x[1][e] - mx[e]);
-          l[e] = fmaf(l[e], al[e], w0 + w1);
+          const float w0 = ex2(x[0][e] - ref[e]), w1 = ex2(x[1][e] - ref[e]);
+          l[e] = fmaf(l[e], al[e], (w0 + w1) * pt[e]);
           x[0][e] = w0 * fv[0];
           x[1][e] = w1 * fv[1];
         }
@@ -606,15 +653,15 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::P_READY + nb));
-        if (lt > seg.lt0) correct(n - 1);
-        if (lt == seg.lt1 - 1) correct(n);
+        if (lt > seg.lt0) correct(n - 1, vm_last);
+        if (lt == seg.lt1 - 1) correct(n, vm);
       }
       ++k;
       if (lane == 0) mbar_arrive(BAR(C::Q_EMPTY + qb));
       // ---- segment end: the row sums across the warpgroup, then the output
       // or a partial ----
       const uint32_t nb = (n - 1) & 1;
-      float* rb = red + nb * (HP + 1) * 4;
+      float* rb = red + nb * HP * 4;
       {
         // each round trades half of the sums still held with a partner lane;
         // lane x ends with the warp's sum of row x / (32 / HP)
@@ -653,7 +700,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
             const size_t sl = slot * nr + a;
             if (row < DV) p.part_o[sl * DV + row] = o[e];
             if (row == 0) {
-              p.part_ml[2 * sl] = sum > 0.f ? max_sm[nb * NR + a] : -INFINITY;
+              p.part_ml[2 * sl] = sum > 0.f ? run_sm[nb * NR + a] : -INFINITY;
               p.part_ml[2 * sl + 1] = sum;
             }
           }
