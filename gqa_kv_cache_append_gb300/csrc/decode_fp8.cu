@@ -419,7 +419,9 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           // 2^ke * amax in [128, 256)
           int ke = 0;
           if (amax > 0.f && amax < INFINITY) ke = min(max(7 - ilogbf(amax), -126), 126);
-          const float up = ldexpf(1.f, ke);
+          // (an infinity would saturate to 448: the row is NaN, as its logits
+          // are in the formula)
+          const float up = amax < INFINITY ? ldexpf(1.f, ke) : NAN;
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] *= up;
           uint32_t hi, lo;

@@ -599,8 +599,8 @@ int gqa_chunk_attn_workspace(int total, int h, int g, int d_k, int d_v, int num_
  * largest), and of a position's weight times its V scale down to 2^-14 of the
  * largest such product among the 256 positions of its tile (below that it is
  * off by up to 2^-22 of that product; V scales of a tile within 2^64 of one
- * another).  Rows p >= L_i are never used, whatever they hold.  The same call
- * gives the same bits.
+ * another).  A query row with an infinity or NaN gives NaN.  Rows p >= L_i are
+ * never used, whatever they hold.  The same call gives the same bits.
  * Supported: GQA_BF16; d_k, d_v in {64, 128} (they may differ); n * (h / g)
  * <= 32; b <= 65535.  (Other types: gqa_kv_read_fp8_paged, then the 16-bit
  * and fp32 calls.)
