@@ -12,11 +12,16 @@
 //   O [128 x d_v] += P . V_tile                   (tcgen05.mma, P in tensor memory)
 //
 // While one side's softmax runs, the tensor cores work on the other side.
-// m is a row's running maximum, raised only when it grows by more than 2^8
-// in the exponent (P stays below 2^8, so 16-bit P and fp32 sums lose
-// nothing); O is rescaled in tensor memory on those occasions alone.  P is
-// rounded to the cache's type for the product; the row sum adds the fp32
-// values.
+// m is a row's running maximum, raised only when the exponent grows past it by
+// more than a few powers of two (the lazy rescaling known from published
+// attention kernels); O is rescaled in tensor memory on those occasions alone.
+// P is rounded to the cache's type for the product (the row sum adds the fp32
+// values): to bf16's range whatever is raised, so P may grow to 2^8.  fp16 ends
+// at 2^-14 (2^-25 with subnormals), where the weights of a long cache behind
+// one dominant position lie: there P is taken 2^11 higher and m raised past
+// 2^4, which uses the range up to 2^15 and keeps weights down to 2^-25 of the
+// largest whole (below, they are off by up to 2^-36 of it).  The factor 2^11 is
+// in l and O alike and cancels.
 //
 // Roles (384 threads, one persistent CTA per SM):
 //   warps 0-3  softmax of side A, output; thread = query row = TMEM lane
@@ -69,9 +74,13 @@ constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kDescInts = 8;      // per CTA, see below
 constexpr int kSegs = 4;          // segments announced ahead
 constexpr int kSegBytes = 48;
-// a row's reference maximum is raised when the new one is this much larger
-// (base 2)
-constexpr float kRaise = 8.f;
+// A row's reference maximum is raised when the new one is this much larger, and
+// P is taken this much higher (both base 2).
+template <typename T16>
+struct PRange {
+  static constexpr float kRaise = Half16<T16>::kBf16 ? 8.f : 4.f;
+  static constexpr float kLift = Half16<T16>::kBf16 ? 0.f : 11.f;
+};
 
 template <int DK, int DV>
 struct ChunkCfg {
@@ -803,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         // S_FULL also covers the products issued before it: O is complete
         // up to the last tile
-        if (__any_sync(0xffffffffu, (mn - m) * sl > kRaise)) {
+        if (__any_sync(0xffffffffu, (mn - m) * sl > PRange<T16>::kRaise)) {
           const float ref = mn == -INFINITY ? 0.f : mn;
           const float alpha = ex2((m - ref) * sl);
           m = mn;
@@ -820,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float off = m == -INFINITY ? 0.f : -m * sl;
+        const float off = m == -INFINITY ? 0.f : PRange<T16>::kLift - m * sl;
         const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
