@@ -861,7 +861,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      float ms = l > 0.f ? m * sl : -INFINITY;  // base 2
+      // (base 2; a sum that is NaN keeps its piece from counting as empty)
+      float ms = l > 0.f ? m * sl : l == 0.f ? -INFINITY : l;
       float wo = 1.f, wt = 0.f;                 // factors of this side's O, of its twin's
       if (twin) {
         // (a bounded wait, as every wait here; then the other side's O is
@@ -878,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wo = ex2(ms - ref);
         wt = ex2(t2.x - ref);
         l = l * wo + t2.y * wt;
-        ms = mj;
+        ms = l >= 0.f ? mj : l;
       }
       const int c0 = twin ? side * (DV / 64) : 0, c1 = twin ? c0 + DV / 64 : DV / 32;
       const float inv = 1.f / l;

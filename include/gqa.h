@@ -556,8 +556,8 @@ int gqa_kv_read_fp8_paged(const void* k_pool, const void* v_pool, const float* k
  *   does not matter.  Calls that overlap on the GPU need one each (so do
  *   captured graphs that are replayed side by side).
  * Rows p >= L_i of the caches are never used, whatever they hold; rows p < L_i
- * hold finite values (a later token's infinity or NaN may reach an earlier
- * token of the same chunk).  Every element is accumulated in fp32, in an order
+ * hold finite values (a NaN reaches the tokens that see it, and a later
+ * token's infinity or NaN may reach an earlier one of the same chunk).  Every element is accumulated in fp32, in an order
  * that depends on the lengths alone: the same call gives the same bits.
  * Supported: GQA_BF16 and GQA_F16, d_k and d_v in {64, 128} (they may
  * differ), h / g <= 128, b <= 65535.  GQA_ERR_SCRATCH_LIMIT: the workspace is
