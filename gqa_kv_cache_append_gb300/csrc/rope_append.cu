@@ -12,9 +12,10 @@
 //             s = max|x| / 448, x / s rounded to e4m3
 // Everything in between is fp32.  Angles: f_m is kept as the 64-bit fraction
 // of a turn per position, so P * f_m mod one turn is one wrapping 64-bit
-// product and far positions lose nothing; its upper 32 bits are the angle in
-// units of 2^-32 turns (half a unit is 7e-10 rad), rounded to fp32 for
-// sincospi.
+// product and far positions lose nothing; as a signed number it is the angle
+// over pi in units of 2^-63, rounded to fp32 half by half (2^-23 of itself) for
+// sincospi.  (The upper half alone leaves small angles off by up to 1.5e-9
+// rad; a 64-bit conversion takes 37.65 us where this takes 37.2.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -145,7 +146,9 @@ __global__ void __launch_bounds__(kRopeThreads, FP8 ? 8 : 7)
       const unsigned long long ph =
           __ldg(a.phase + 4 * g8 + k) * static_cast<unsigned long long>(P);
       // the angle over pi, in [-1, 1)
-      sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 0x1p-31f, &sn[k], &cs[k]);
+      const float turn = fmaf(static_cast<float>(static_cast<uint32_t>(ph)), 0x1p-32f,
+                              static_cast<float>(static_cast<int>(ph >> 32)));
+      sincospif(turn * 0x1p-31f, &sn[k], &cs[k]);
       cs[k] *= a.rope_scale;
       sn[k] *= a.rope_scale;
     }

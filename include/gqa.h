@@ -475,8 +475,8 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  *      v_cache[i, j, P, :] = v_new[t, j, :]                  (bit for bit)
  *   norm(x, w) = x / sqrt(mean(x^2) + eps) * w, left out when q_weight and
  *   k_weight are NULL; rot turns the pairs of the first `rot` elements (layout
- *   GQA_ROPE_HALF or GQA_ROPE_PAIRS) by the table's angles times P, exact for
- *   every position, and multiplies them by rope_scale; left out when phase is
+ *   GQA_ROPE_HALF or GQA_ROPE_PAIRS) by the table's angles times P (reduced to
+ *   a turn exactly, then rounded to fp32) and multiplies them by rope_scale; left out when phase is
  *   NULL (then rot and layout are not looked at).  fp32 throughout, rounded
  *   once when stored.
  *   q [total, h, d_k], k_new [total, g, d_k], v_new [total, g, d_v] (read;
