@@ -80,6 +80,8 @@ template <typename T>
 struct Piece4 {
   uint2 raw;
   __device__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint2*>(p)); }
+  // (of memory that this kernel writes)
+  __device__ void load_own(const T* p) { raw = *reinterpret_cast<const uint2*>(p); }
   __device__ void zero() { raw = make_uint2(0u, 0u); }
   __device__ void get(float* x) const {
     const uint32_t w[2] = {raw.x, raw.y};
@@ -106,6 +108,7 @@ template <>
 struct Piece4<float> {
   float4 raw;
   __device__ void load(const float* p) { raw = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ void load_own(const float* p) { raw = *reinterpret_cast<const float4*>(p); }
   __device__ void zero() { raw = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ void get(float* x) const { x[0] = raw.x, x[1] = raw.y, x[2] = raw.z, x[3] = raw.w; }
   __device__ static void store(float* p, const float* x) {

@@ -476,9 +476,9 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  *   norm(x, w) = x / sqrt(mean(x^2) + eps) * w, left out when q_weight and
  *   k_weight are NULL; rot turns the pairs of the first `rot` elements (layout
  *   GQA_ROPE_HALF or GQA_ROPE_PAIRS) by the table's angles times P (reduced to
- *   a turn exactly, then rounded to fp32) and multiplies them by rope_scale; left out when phase is
- *   NULL (then rot and layout are not looked at).  fp32 throughout, rounded
- *   once when stored.
+ *   a turn exactly, then rounded to fp32) and multiplies them by rope_scale;
+ *   left out when phase is NULL (then rot and layout are not looked at).  fp32
+ *   throughout, rounded once when stored.
  *   q [total, h, d_k], k_new [total, g, d_k], v_new [total, g, d_v] (read;
  *     heads contiguous, consecutive tokens q_stride / k_stride / v_stride
  *     elements apart, so the three may be slices of one projection's output)
