@@ -495,6 +495,8 @@ int rope_check(const RopeLaunch& a, int layout, int dtype, bool fp8) {
       off16(a.v_cache) || off16(a.q_w) || off16(a.k_w) || off4(a.k_scale) || off4(a.v_scale) ||
       off4(a.cu) || off4(a.lens))
     return GQA_ERR_ALIGN;
+  // in place, a token's output must lie where its query lies
+  if (a.q != nullptr && a.q == a.q_out && a.q_stride != dq && a.total > 1) return GQA_ERR_SHAPE;
   return GQA_OK;
 }
 

@@ -484,7 +484,8 @@ int gqa_decode_plan(int b, int n, int h, int g, int d_k, int d_v, int cap, int d
  *     elements apart, so the three may be slices of one projection's output)
  *   q_weight, k_weight [d_k] (read, both or neither)
  *   phase [rot / 2] uint64 (device, read)
- *   q_out [total, h, d_k] (written; may be q itself when q_stride = h * d_k).
+ *   q_out [total, h, d_k] (written; may be q itself when q_stride = h * d_k,
+ *     GQA_ERR_SHAPE with another stride; otherwise it overlaps no input).
  *     q and q_out both NULL: only the cache is written.
  *   k_cache [b, g, cap, d_k], v_cache [b, g, cap, d_v] (rows P written)
  * Supported: GQA_F32, GQA_BF16, GQA_F16; d_k, d_v multiples of 8 up to 256;
@@ -549,7 +550,7 @@ int gqa_kv_read_fp8_paged(const void* k_pool, const void* v_pool, const float* k
  *                    v_cache[i, j, p, :]
  * A whole prompt is a chunk with n_i = L_i, a decode step one with n_i = 1;
  * sequences of a call mix freely.  There is no limit on n_i.
- *   q [total, h, d_k] (read), out [total, h, d_v] (written)
+ *   q [total, h, d_k] (read), out [total, h, d_v] (written; overlaps no input)
  *   k_cache [b, g, cap, d_k], v_cache [b, g, cap, d_v] (read)
  *   workspace: device memory, 256-byte aligned, of at least the bytes that
  *   gqa_chunk_attn_workspace gives; what it holds before and after the call
