@@ -601,7 +601,9 @@ int gqa_chunk_attn_workspace(int total, int h, int g, int d_k, int d_v, int num_
  * largest such product among the 256 positions of its tile (below that it is
  * off by up to 2^-22 of that product; V scales of a tile within 2^64 of one
  * another).  A query row with an infinity or NaN gives NaN.  Rows p >= L_i are
- * never used, whatever they hold.  The same call gives the same bits.
+ * never used, whatever they hold; rows p < L_i hold finite values (one stored
+ * from infinities or NaN reaches the tokens that see it, and may reach the
+ * other new tokens of its sequence).  The same call gives the same bits.
  * Supported: GQA_BF16; d_k, d_v in {64, 128} (they may differ); n * (h / g)
  * <= 32; b <= 65535.  (Other types: gqa_kv_read_fp8_paged, then the 16-bit
  * and fp32 calls.)
