@@ -9,7 +9,7 @@
 //             (a cos t - c sin t, c cos t + a sin t) * rope_scale,
 //             t = P * f_m for pair m: elements (m, m + rot/2) or (2m, 2m + 1)
 //   store     rounded once to the type of the call, or for an e4m3 cache
-//             s = max|x| / 448, x / s rounded to e4m3
+//             s = max|x| / 448, x * (448 / max|x|) rounded to e4m3
 // Everything in between is fp32.  Angles: f_m is kept as the 64-bit fraction
 // of a turn per position, so P * f_m mod one turn is one wrapping 64-bit
 // product and far positions lose nothing; as a signed number it is the angle
@@ -424,14 +424,18 @@ cudaError_t launch_rope_gs(const RopeLaunch& a, int num_sms, cudaStream_t st) {
   constexpr int SIDE = 32 / GS;
   const int nq = ((a.q != nullptr ? a.h : 0) + SIDE - 1) / SIDE, nk = (a.g + SIDE - 1) / SIDE;
   const int steps = nq + 2 * nk;
-  // a warp takes a whole token, unless that leaves the SMs short of warps
-  // (16 each): then the token's rows are dealt out to several.  (More than 16:
-  // 4.0 -> 4.6 us for 64 tokens.)  Where the warps would all fit at once (32 an
-  // SM) a token goes to two: 42 -> 40.5 us for 4,308 tokens, while 8,192 tokens
-  // take 36.8 us whole and 37.2 halved.
+  // A warp takes a whole token, unless that leaves the SMs short of warps (16
+  // each): then the token's rows are dealt out to several.  (More than 16: 4.0
+  // -> 4.6 us for 64 tokens.)  With fewer than 32 tokens an SM (28 to 32 warps
+  // fit at once) a token of 16 steps or more goes to two, for a shorter tail.
+  // One warp against two, 2,500 and 4,800 tokens: h = 64, g = 8, d = 128 (40
+  // steps) bf16 30.6 and 47.9 us against 27.4 and 42.0, fp32 52.9 and 88.7
+  // against 49.0 and 76.2, bf16 to e4m3 40.2 and 44.6 against 33.3 and 45.8;
+  // h = 16, g = 4 (12 steps) bf16 11.4 and 18.8 against 11.0 and 19.0; h = 8,
+  // g = 2 (6 steps) bf16 7.9 and 10.7 against 8.7 and 12.5.
   const long long want = 16ll * num_sms;
   long long deal = (want + a.total - 1) / a.total;
-  if (a.total < 2 * want) deal = std::max(deal, 2ll);
+  if (a.total < 2 * want && steps >= 16) deal = std::max(deal, 2ll);
   int parts = static_cast<int>(std::min<long long>(deal, steps));
   const int per_part = (steps + parts - 1) / parts;
   parts = (steps + per_part - 1) / per_part;
