@@ -46,11 +46,14 @@
 // Rows >= L_i: masked out of S, their V rows zeroed in shared memory.
 //
 // Bound by the tensor cores where units are long: a prompt of 8,192 tokens,
-// h = 64, g = 8, d = 128, bf16: 648 us, 1,696 TFLOP/s (graph replay); what the
-// pipe still waits for is a side's own chain of S, softmax and hand-over, which
-// is a little longer than the other side's products.  Short units are bound
-// by their fixed cost (query rows in, first logits, output): 135 us for 32
-// mixed sequences of 5,957 tokens, 17.5 us for eight chunks of 4 to 12.
+// h = 64, g = 8, d = 128, bf16: 649 to 653 us, 1,690 TFLOP/s, in a short graph
+// replay, 704 to 718 us, 1,530 to 1,560, among other passes, as the clock falls
+// under the power limit.  What the pipe still waits for is a side's own chain
+// of S, softmax and hand-over, which is a little longer than the other side's
+// products.  Short units are bound by their fixed cost (query rows in, first
+// logits, output): 130 to 141 us for 32 mixed sequences of 5,957 tokens, 33.8
+// us for 48 packed short prompts with 64-wide heads, 17.8 us for eight chunks
+// of 4 to 12 tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -155,7 +158,9 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register
 // units are laid end to end (sequences, KV heads, blocks of query rows) and run
 // c begins at c * W / nc, moved to a tile's edge, or to the unit's when that is
 // near.  (With half the work for twins and a cost of 192 the prompt takes 675 us
-// where this takes 650.)
+// where this takes 650.  The cost alone, graph replay: 192, 320, 448, 576 give
+// 134, 131, 133, 137 us for the mixed batch, and with 64-wide heads 105, 107,
+// 110, 114 us for it and 33.0, 33.6, 34.7, 35.4 us for packed short prompts.)
 constexpr int kUnitCost = 320;
 
 struct ChunkPos {  // a place in the order of all tiles
@@ -280,7 +285,8 @@ struct ChunkWalk {
     }
     W *= g;
     r = {b, 0, 0, 0};
-    // a run is worth at least two tiles: less costs more to join than it saves
+    // a run is worth at least a tile (two with much work): less costs more to
+    // join than it saves
     nc = static_cast<int>(min(static_cast<long long>(nc), W / (2 * kN) + 1));
     if (W == 0 || c > nc) return false;
     if (c == nc) return true;

@@ -47,10 +47,11 @@
 // unit cut between CTAs leaves partial results, joined by the combine kernel.
 //
 // Bound by HBM where sequences are many and long: b = 32, L = 8,192, h = 64,
-// g = 8, d = 128: 87 us, 6,370 GB/s (graph replay).  A few tiles a CTA: start,
-// first tile and join (24 ragged sequences of 512 to 32,766, g = 4, two tokens
-// of seven heads: 41 us, 3,700 GB/s; 32-row blocks also cost the TMA warp
-// sixteen copies a tile at ~100 cycles each).
+// g = 8, d = 128: 89.5 us, 6,200 GB/s (graph replay; 88.9 with the weights
+// against the running maximum).  A few tiles a CTA: start, first tile and join
+// (24 ragged sequences of 512 to 32,766, g = 4, two tokens of seven heads: 43
+// us, 3,550 GB/s, 42 with the running maximum; 32-row blocks also cost the TMA
+// warp sixteen copies a tile at ~100 cycles each).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -264,9 +265,9 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           tma_load_2d(dst + C::K_BYTES + lane * box * DV, &tm_v, BAR(C::FULL_V + st), 0, cur, pol);
         }
         // the scales of this lane's eight positions (past L_i, or through a
-        // bad entry: none).  Four instructions a tile: a bulk copy takes the
-        // warp that issues it ~100 cycles, and two more per block beside K's
-        // and V's made this warp the bound with 32-row blocks.
+        // bad entry: none).  Four instructions a tile; as two more bulk copies a
+        // block (~100 cycles of the issuing warp each) they took as long, 41 to
+        // 42 us with 32-row blocks.
         const int pos = lt * kTile + lane * 8;
         const int blk = __shfl_sync(0xffffffffu, ent, (lane * 8) >> sh);
         if (pos < seg.L && blk >= 0 && blk < p.num_blocks) {

@@ -62,12 +62,16 @@ constexpr int kBatch = 4;  // rows a lane loads ahead of their use
 // multiplied in.  Warps do not wait for one another, and the first rows'
 // loads go out before the position is known.
 //
-// Bound by memory (every row read and written once) and by instructions close
-// behind it.  Measured (graph replay): one block per token, sines in shared
-// memory and a shuffle per exchanged element 58 us for 2 x 4096 fp16 tokens
-// and 113 us for 24 ragged sequences (11,290 tokens, h = 28); a warp per
-// token, the kind of a row chosen row by row 47 and 67 us; this form 37 and
-// 46 us, 5,410 and 4,540 GB/s.
+// Bound by memory (every row read and written once) where rows are only
+// turned; with the norm by its loads' latency, a batch of rows being loaded
+// only when the one before it is done and registers holding 28 warps an SM,
+// and by instructions close behind (63 % of the issue slots).  Measured (graph
+// replay): one block per token, sines in shared memory and a shuffle per
+// exchanged element 58 us for 2 x 4096 fp16 tokens and 113 us for 24 ragged
+// sequences with norm (11,290 tokens, h = 28); a warp per token, the kind of a
+// row chosen row by row 47 and 67 us; this form 36.8 and 45.1 us, 5,480 and
+// 4,600 GB/s.  fp32, with norm, 8,192 tokens of h = 32, g = 8: 78.8 us, 5,110
+// GB/s; into e4m3 rows, 4,305 tokens of h = 64, g = 8: 40.5 us, 4,140 GB/s.
 enum { ROW_Q = 0, ROW_K = 1, ROW_V = 2 };
 
 template <typename T, bool FP8, int GS>
