@@ -13,9 +13,9 @@
 //
 //   S^T [T x 2 NR]   = K8 . (Qhi, Qlo)^T               (tcgen05.mma, 2 x M=128)
 //   x[p, a]          = (Shi + Slo / 16) * ks[p] * qs[a] * scale * log2 e
-//   y_a              = max_p x[p, a] + log2(vs[p] / vmax)    (vmax = max vs of the tile)
+//   y_a              = max_p x[p, a] + log2|vs[p] / vmax|    (vmax = max |vs| of the tile)
 //   w[p, a]          = exp2(x - y_a)
-//   P[p, a]          = w * vs[p] * 256 / vmax                (the largest is 256)
+//   P[p, a]          = w * vs[p] * 256 / vmax                (256 at the largest)
 //   O^T [d_v x 2 NR] = V8^T . (Phi, Plo)^T                   (tcgen05.mma, M=128)
 //   m_a              = max(m_old, y_a)                       (of the tiles so far)
 //   l_a              = l_a * 2^(m_old - m) + sum_p w * 2^(y_a - m)
@@ -526,10 +526,10 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           const int p0 = hf * kHalf + 4 * lane;
           const float4 v = *reinterpret_cast<const float4*>(
               reinterpret_cast<const float*>(sm + C::OFF_SC) + (st * 2 + 1) * kTile + p0);
-          vm = fmaxf(vm, p0 < valid ? v.x : 0.f);
-          vm = fmaxf(vm, p0 + 1 < valid ? v.y : 0.f);
-          vm = fmaxf(vm, p0 + 2 < valid ? v.z : 0.f);
-          vm = fmaxf(vm, p0 + 3 < valid ? v.w : 0.f);
+          vm = fmaxf(vm, p0 < valid ? fabsf(v.x) : 0.f);
+          vm = fmaxf(vm, p0 + 1 < valid ? fabsf(v.y) : 0.f);
+          vm = fmaxf(vm, p0 + 2 < valid ? fabsf(v.z) : 0.f);
+          vm = fmaxf(vm, p0 + 3 < valid ? fabsf(v.w) : 0.f);
         }
         vm = warp_max(vm);
         // (scales so small that the factor would overflow: scaled up first)
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           fv[hf] = vs[hf] * up * vinv;  // 256 vs / vmax
-          lv[hf] = fmaxf(__log2f(fv[hf]) - 8.f, -64.f);
+          lv[hf] = fmaxf(__log2f(fabsf(fv[hf])) - 8.f, -64.f);
         }
         tmem_wait_ld();
 #pragma unroll

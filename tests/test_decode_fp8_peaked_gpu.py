@@ -93,7 +93,7 @@ class Peaked:
                 x[..., see:] = -math.inf
                 w = torch.softmax(x, -1)
                 ref, A = w @ v, w @ v.abs()
-                T = torch.nn.functional.pad(w * vs[:, None], (0, pad)).view(g, r, -1, 256).amax(-1)
+                T = torch.nn.functional.pad(w * vs.abs()[:, None], (0, pad)).view(g, r, -1, 256).amax(-1)
                 E = (q.abs() @ k.abs().transpose(1, 2) * self.scale).amax(-1, keepdim=True)
                 Q = 2.0 ** -21 * self.scale * q.abs().amax(-1, keepdim=True) * ksum
                 tol = (U * ref.abs() + U * A + 2.0 ** -22 * (T @ v8t) +
@@ -134,6 +134,18 @@ def test_rows_of_very_different_sizes(b, length, v_spread, share):
 def test_rows_all_small_or_large(power):
     c = Peaked(2, 700, sink=0.1, seed=3)
     c.pools[1][1].mul_(2.0 ** power)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("which", ["some", "all"])
+@pytest.mark.parametrize("length", [700, 20001])
+def test_negative_scales(which, length):
+    """Rows are scale times value, whatever the scale's sign."""
+    c = Peaked(2, length, share=0.0, sink=1.0, v_spread=2.0, seed=5)
+    for _, sc in c.pools:
+        flip = torch.rand(sc.shape, device="cuda") < 0.5 if which == "some" else sc > 0
+        sc.copy_(torch.where(flip, -sc, sc))
     c.run()
     c.check()
 
