@@ -88,6 +88,16 @@ SIGNATURES = {
     "gqa_decode_attn_fp8_paged": (_I, [_VP] * 7 + [_I] * 6 + [_F, _VP] + [_I] * 4 +
                                   [_VP, _LL, _VP]),
     "gqa_decode_attn_fp8_workspace": (_I, [_I] * 6 + [_LL, _I, ctypes.POINTER(_LL)]),
+    "gqa_chunk_attn_window": (_I, [_VP] * 5 + [_I] * 6 + [_F, _I, _I, _VP, _I, _I, _VP, _LL,
+                                                          _VP]),
+    "gqa_chunk_attn_window_paged": (_I, [_VP] * 6 + [_I] * 6 + [_F, _I, _I, _VP] + [_I] * 4 +
+                                    [_VP, _LL, _VP]),
+    "gqa_chunk_attn_prefix": (_I, [_VP] * 5 + [_I] * 6 + [_F, _I, _VP, _I, _I, _VP, _LL, _VP]),
+    "gqa_chunk_attn_prefix_paged": (_I, [_VP] * 6 + [_I] * 6 + [_F, _I, _VP] + [_I] * 4 +
+                                    [_VP, _LL, _VP]),
+    "gqa_chunk_attn_prefix_workspace": (_I, [_I] * 7 + [ctypes.POINTER(_LL)]),
+    "gqa_decode_attn_fp8_window_paged": (_I, [_VP] * 7 + [_I] * 6 + [_F, _I, _I, _VP] +
+                                         [_I] * 4 + [_VP, _LL, _VP]),
     "gqa_device_status": (_I, [_VP, ctypes.POINTER(ctypes.c_uint32)]),
     "gqa_selftest_wait_timeout": (_I, [_LL, _VP]),
     "gqa_status_string": (ctypes.c_char_p, [_I]),
@@ -676,12 +686,11 @@ def _workspace(ws, stream, dev, like, size, *shape):
     raise ValueError("workspace: must be a tensor")
 
 
-def gqa_chunk_attn(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, scale, out,
-                   total=None, cap=None, dtype=None, workspace=None, stream=None) -> None:
-    """Causal attention of packed chunks of new tokens (q [total, h, d_k], out
-    [total, h, d_v]) over caches that already hold their rows.  workspace:
-    a uint8 tensor of gqa_chunk_attn_workspace bytes to reuse between calls
-    (by default one is made per call)."""
+def _chunk(name, q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, scale, part, out,
+           total, cap, dtype, workspace, stream, size, *lead) -> None:
+    """The chunk calls over contiguous caches; `part`: the arguments between
+    scale and out, `size` and `lead`: the workspace's function and its
+    arguments before total."""
     dev, st = _here(q, stream)
     dt = _dtype(q, dtype)
     ty = _TORCH.get(dt, ())
@@ -689,35 +698,102 @@ def gqa_chunk_attn(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, 
         total = q.shape[0]
     if cap is None:
         cap = k_cache.shape[2]
-    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g,
-                               d_k, d_v)
-    _launch("gqa_chunk_attn", lib.gqa_chunk_attn, _tensor(q, "q", total * h * d_k, ty, dev),
+    wp, wn, _keep = _workspace(workspace, stream, dev, q, size, *lead, total, h, g, d_k, d_v)
+    _launch(name, getattr(lib, name), _tensor(q, "q", total * h * d_k, ty, dev),
             _tensor(k_cache, "k_cache", b * g * cap * d_k, ty, dev),
             _tensor(v_cache, "v_cache", b * g * cap * d_v, ty, dev),
             _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
             _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
-            int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev),
-            int(cap), dt, wp, wn, st)
+            int(d_k), int(d_v), float(scale), *part,
+            _tensor(out, "out", total * h * d_v, ty, dev), int(cap), dt, wp, wn, st)
 
 
-def gqa_chunk_attn_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k, d_v,
-                         scale, out, total=None, dtype=None, workspace=None,
-                         stream=None) -> None:
-    """gqa_chunk_attn over a paged cache."""
+def _chunk_paged(name, q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k, d_v,
+                 scale, part, out, total, dtype, workspace, stream, size, *lead) -> None:
+    """_chunk over a paged cache."""
     dev, st = _here(q, stream)
     dt = _dtype(q, dtype)
     ty = _TORCH.get(dt, ())
     if total is None:
         total = q.shape[0]
     kp, vp, tp, bs, mb, nb = _pools(k_pool, v_pool, block_table, b, g, d_k, d_v, ty, dev)
-    wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_chunk_attn_workspace, total, h, g,
-                               d_k, d_v)
-    _launch("gqa_chunk_attn_paged", lib.gqa_chunk_attn_paged,
-            _tensor(q, "q", total * h * d_k, ty, dev), kp, vp, tp,
+    wp, wn, _keep = _workspace(workspace, stream, dev, q, size, *lead, total, h, g, d_k, d_v)
+    _launch(name, getattr(lib, name), _tensor(q, "q", total * h * d_k, ty, dev), kp, vp, tp,
             _tensor(cu_tokens, "cu_tokens", b + 1, _I32, dev),
             _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(total), int(h), int(g),
-            int(d_k), int(d_v), float(scale), _tensor(out, "out", total * h * d_v, ty, dev), bs,
-            mb, nb, dt, wp, wn, st)
+            int(d_k), int(d_v), float(scale), *part,
+            _tensor(out, "out", total * h * d_v, ty, dev), bs, mb, nb, dt, wp, wn, st)
+
+
+def gqa_chunk_attn(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, scale, out,
+                   total=None, cap=None, dtype=None, workspace=None, stream=None) -> None:
+    """Causal attention of packed chunks of new tokens (q [total, h, d_k], out
+    [total, h, d_v]) over caches that already hold their rows.  workspace:
+    a uint8 tensor of gqa_chunk_attn_workspace bytes to reuse between calls
+    (by default one is made per call)."""
+    _chunk("gqa_chunk_attn", q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, scale,
+           (), out, total, cap, dtype, workspace, stream, gqa_chunk_attn_workspace)
+
+
+def gqa_chunk_attn_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k, d_v,
+                         scale, out, total=None, dtype=None, workspace=None,
+                         stream=None) -> None:
+    """gqa_chunk_attn over a paged cache."""
+    _chunk_paged("gqa_chunk_attn_paged", q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b,
+                 h, g, d_k, d_v, scale, (), out, total, dtype, workspace, stream,
+                 gqa_chunk_attn_workspace)
+
+
+def gqa_chunk_attn_window(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, scale,
+                          window, out, sinks=0, total=None, cap=None, dtype=None,
+                          workspace=None, stream=None) -> None:
+    """gqa_chunk_attn where a token sees its last `window` positions (its own
+    among them) and the first `sinks` of its sequence.  workspace: as for
+    gqa_chunk_attn."""
+    _chunk("gqa_chunk_attn_window", q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v,
+           scale, (int(window), int(sinks)), out, total, cap, dtype, workspace, stream,
+           gqa_chunk_attn_workspace)
+
+
+def gqa_chunk_attn_window_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k,
+                                d_v, scale, window, out, sinks=0, total=None, dtype=None,
+                                workspace=None, stream=None) -> None:
+    """gqa_chunk_attn_window over a paged cache; table entries of blocks that
+    hold no position that is seen are not looked at."""
+    _chunk_paged("gqa_chunk_attn_window_paged", q, k_pool, v_pool, block_table, cu_tokens,
+                 seq_lens, b, h, g, d_k, d_v, scale, (int(window), int(sinks)), out, total,
+                 dtype, workspace, stream, gqa_chunk_attn_workspace)
+
+
+def gqa_chunk_attn_prefix_workspace(b, total, h, g, d_k, d_v, num_sms=0) -> int:
+    """Bytes of workspace of gqa_chunk_attn_prefix(_paged) for b sequences and
+    up to `total` packed rows (host only when num_sms > 0)."""
+    n = ctypes.c_longlong(0)
+    _check("gqa_chunk_attn_prefix_workspace", lib.gqa_chunk_attn_prefix_workspace(
+        int(b), int(total), int(h), int(g), int(d_k), int(d_v), int(num_sms), ctypes.byref(n)))
+    return int(n.value)
+
+
+def gqa_chunk_attn_prefix(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v, scale,
+                          prefix_len, out, total=None, cap=None, dtype=None, workspace=None,
+                          stream=None) -> None:
+    """gqa_chunk_attn for sequences whose first prefix_len positions (counted
+    in seq_lens) are the same rows, read from sequence 0's.  workspace: a uint8
+    tensor of gqa_chunk_attn_prefix_workspace bytes (by default one is made
+    per call)."""
+    _chunk("gqa_chunk_attn_prefix", q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v,
+           scale, (int(prefix_len),), out, total, cap, dtype, workspace, stream,
+           gqa_chunk_attn_prefix_workspace, b)
+
+
+def gqa_chunk_attn_prefix_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_lens, b, h, g, d_k,
+                                d_v, scale, prefix_len, out, total=None, dtype=None,
+                                workspace=None, stream=None) -> None:
+    """gqa_chunk_attn_prefix over a paged cache: the prefix is found through
+    row 0 of the block table."""
+    _chunk_paged("gqa_chunk_attn_prefix_paged", q, k_pool, v_pool, block_table, cu_tokens,
+                 seq_lens, b, h, g, d_k, d_v, scale, (int(prefix_len),), out, total, dtype,
+                 workspace, stream, gqa_chunk_attn_prefix_workspace, b)
 
 
 def gqa_decode_attn_fp8_workspace(b, n, h, g, d_k, d_v, cap, num_sms=0) -> int:
@@ -730,13 +806,9 @@ def gqa_decode_attn_fp8_workspace(b, n, h, g, d_k, d_v, cap, num_sms=0) -> int:
     return int(out.value)
 
 
-def gqa_decode_attn_fp8_paged(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, b, h,
-                              g, d_k, d_v, scale, out, n=1, dtype=None, workspace=None,
-                              stream=None) -> None:
-    """gqa_decode_attn_paged over an 8-bit paged cache (e4m3 pools, one fp32
-    scale per row).  workspace: a uint8 tensor of
-    gqa_decode_attn_fp8_workspace bytes to reuse between calls (by default
-    one is made per call)."""
+def _decode_fp8(name, q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, b, h, g, d_k,
+                d_v, scale, part, out, n, dtype, workspace, stream) -> None:
+    """The 8-bit decode calls; `part`: the arguments between scale and out."""
     dev, st = _here(q, stream)
     dt = _dtype(q, dtype)
     ty = _TORCH.get(dt, ())
@@ -744,11 +816,34 @@ def gqa_decode_attn_fp8_paged(q, k_pool, v_pool, k_scale, v_scale, block_table, 
                                              d_k, d_v, dev)
     wp, wn, _keep = _workspace(workspace, stream, dev, q, gqa_decode_attn_fp8_workspace, b, n, h,
                                g, d_k, d_v, bs * mb)
-    _launch("gqa_decode_attn_fp8_paged", lib.gqa_decode_attn_fp8_paged,
+    _launch(name, getattr(lib, name),
             _tensor(q, "q", b * n * h * d_k, ty, dev), kp, vp, ks, vs, tp,
             _tensor(seq_lens, "seq_lens", b, _I32, dev), int(b), int(n), int(h), int(g),
-            int(d_k), int(d_v), float(scale), _tensor(out, "out", b * n * h * d_v, ty, dev), bs,
-            mb, nb, dt, wp, wn, st)
+            int(d_k), int(d_v), float(scale), *part,
+            _tensor(out, "out", b * n * h * d_v, ty, dev), bs, mb, nb, dt, wp, wn, st)
+
+
+def gqa_decode_attn_fp8_paged(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, b, h,
+                              g, d_k, d_v, scale, out, n=1, dtype=None, workspace=None,
+                              stream=None) -> None:
+    """gqa_decode_attn_paged over an 8-bit paged cache (e4m3 pools, one fp32
+    scale per row).  workspace: a uint8 tensor of
+    gqa_decode_attn_fp8_workspace bytes to reuse between calls (by default
+    one is made per call)."""
+    _decode_fp8("gqa_decode_attn_fp8_paged", q, k_pool, v_pool, k_scale, v_scale, block_table,
+                seq_lens, b, h, g, d_k, d_v, scale, (), out, n, dtype, workspace, stream)
+
+
+def gqa_decode_attn_fp8_window_paged(q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens,
+                                     b, h, g, d_k, d_v, scale, window, out, sinks=0, n=1,
+                                     dtype=None, workspace=None, stream=None) -> None:
+    """gqa_decode_attn_fp8_paged where a token sees its last `window` positions
+    (its own among them) and the first `sinks` of its sequence; table entries
+    of blocks that hold none of them are not looked at.  workspace: as for
+    gqa_decode_attn_fp8_paged."""
+    _decode_fp8("gqa_decode_attn_fp8_window_paged", q, k_pool, v_pool, k_scale, v_scale,
+                block_table, seq_lens, b, h, g, d_k, d_v, scale, (int(window), int(sinks)), out,
+                n, dtype, workspace, stream)
 
 
 def gqa_device_status(stream=None) -> int:

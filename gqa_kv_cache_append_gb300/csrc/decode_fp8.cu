@@ -56,9 +56,11 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/gqa.h"
 #include "gqa_internal.h"
+#include "part_device.cuh"
 #include "serve_device.cuh"
 
 namespace gqa {
@@ -68,6 +70,7 @@ constexpr int kTile = 256;   // positions per tile
 constexpr int kHalf = 128;   // positions per S product
 constexpr int kRing = 3;
 constexpr float kLo = 16.f;  // the low piece's factor
+constexpr int kGrain8 = 64;  // PART: positions of a box, at most
 
 template <int NR, int DK, int DV>
 struct F8Cfg {
@@ -121,6 +124,7 @@ struct F8Params {
   const int *lens, *table;
   int b, nq, h, g, r, cap;
   int bsz, max_blocks, num_blocks;
+  int window, sinks, gran;  // positions seen (PART), and those of a box
   float scale_log2;
   __nv_bfloat16* out;
   float *part_o, *part_ml;
@@ -162,7 +166,9 @@ __device__ __forceinline__ void split4(const float (&x)[4], uint32_t& hi, uint32
   lo = e4m3_pack4((x[0] - a.x) * kLo, (x[1] - a.y) * kLo, (x[2] - b.x) * kLo, (x[3] - b.y) * kLo);
 }
 
-template <int NR, int DK, int DV>
+// PART: a token sees its last p.window positions and the first p.sinks; tiles
+// are cut from the unit's span (part_device.cuh).
+template <int NR, int DK, int DV, bool PART>
 __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const F8Params p) {
@@ -217,8 +223,11 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
 
   float* qs_sm = reinterpret_cast<float*>(sm + C::OFF_QS);  // the query rows' factors [2][NR]
 
-  Walker w;
-  w.init(p.lens, p.b, p.g, p.nq, p.cap, kTile, blockIdx.x, gridDim.x);
+  using Span = std::conditional_t<PART, WindowSpan, FullSpan>;
+  SpanWalker<Span> w;
+  Span span;
+  if constexpr (PART) span = {p.window, p.sinks, p.gran};
+  w.init(p.lens, p.b, p.g, p.nq, p.cap, kTile, blockIdx.x, gridDim.x, 0, span);
   Segment seg;
   auto wait = [&](int k, uint32_t phase) -> bool {
     return mbar_wait(BAR(k), phase & 1u, abort_flag, p.status, p.budget);
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     // ============================ TMA producer ============================
     const uint64_t pol = policy_evict_first();
     const int oob_row = p.num_blocks * p.g * p.bsz;
-    const int box = min(p.bsz, kTile);
+    const int box = PART ? p.gran : min(p.bsz, kTile);
     const int sub = kTile / box;  // boxes a tile
     const int sh = __ffs(p.bsz) - 1, mask = p.bsz - 1;  // (a power of two)
     uint32_t n = 0;
@@ -237,15 +246,46 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
       // the sequence's table entries, 64 at a time ahead of their use: no load
       // stands before a tile's copies
       PageCursor pc;
-      pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
-               static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
-               (seg.lt0 * kTile) >> sh);
+      const int* const row = p.table + static_cast<size_t>(seg.i) * p.max_blocks;
+      // PART: the position of this lane's box of tile lt (-1: none), and its
+      // table entry, loaded a tile ahead (a tile's boxes may lie in two places)
+      PartSpan sp = {0, 0, 0};
+      auto box_at = [&](int lt) -> int {
+        if constexpr (PART) {
+          const int v = lt * kTile + lane * box;
+          const int pos = v < sp.sb ? v : v + sp.shift;
+          return lane < sub && pos < (v < sp.sb ? p.sinks : seg.L) ? pos : -1;
+        }
+        return -1;
+      };
+      auto entry = [&](int lt) -> int {
+        const int pos = box_at(lt);
+        return pos >= 0 ? __ldg(row + (pos >> sh)) : -1;
+      };
+      int ahead = -1;
+      if constexpr (PART) {
+        sp = span.at(seg.L, p.nq);
+        ahead = entry(seg.lt0);
+      } else {
+        pc.start(row, static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
+                 (seg.lt0 * kTile) >> sh);
+      }
       for (int lt = seg.lt0; lt < seg.lt1; ++lt, ++n) {
         // the tile's blocks, one a lane; lane mm < sub: the pool row of box mm
-        const int ent = pc.get_lanes((lt * kTile) >> sh);
-        const int pm = lt * kTile + lane * box;
+        int ent, pm;
+        bool live;
+        if constexpr (PART) {
+          ent = ahead;
+          if (lt + 1 < seg.lt1) ahead = entry(lt + 1);
+          pm = box_at(lt);
+          live = pm >= 0;
+        } else {
+          ent = pc.get_lanes((lt * kTile) >> sh);
+          pm = lt * kTile + lane * box;
+          live = lane < sub && pm < seg.L;
+        }
         int cur = oob_row;
-        if (lane < sub && pm < seg.L) {
+        if (live) {
           if (ent >= 0 && ent < p.num_blocks)
             cur = (ent * p.g + seg.j) * p.bsz + (pm & mask);
           else
@@ -268,8 +308,15 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         // bad entry: none).  Four instructions a tile; as two more bulk copies a
         // block (~100 cycles of the issuing warp each) they took as long, 41 to
         // 42 us with 32-row blocks.
-        const int pos = lt * kTile + lane * 8;
-        const int blk = __shfl_sync(0xffffffffu, ent, (lane * 8) >> sh);
+        int pos = lt * kTile + lane * 8, blk;
+        if constexpr (PART) {
+          const int from = lane * 8 / box;
+          const int p0 = __shfl_sync(0xffffffffu, pm, from);
+          blk = __shfl_sync(0xffffffffu, ent, from);
+          pos = p0 < 0 ? seg.L : p0 + (lane * 8 & (box - 1));
+        } else {
+          blk = __shfl_sync(0xffffffffu, ent, (lane * 8) >> sh);
+        }
         if (pos < seg.L && blk >= 0 && blk < p.num_blocks) {
           const size_t at = (static_cast<size_t>(blk) * p.g + seg.j) * p.bsz + (pos & mask);
           const uint32_t sd = s_base + C::OFF_SC + (st * 2 * kTile + lane * 8) * 4;
@@ -489,6 +536,18 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     while (w.next(seg)) {
       const uint32_t qb = k & 1;
       const int first_new = seg.L - p.nq;  // position of new token 0
+      PartSpan sp = {0, 0, 0};
+      int lo_all = 0;  // first position of the window of new token 0
+      if constexpr (PART) {
+        sp = span.at(seg.L, p.nq);
+        lo_all = max(first_new - p.window + 1, 0);
+      }
+      // PART: the position of index v, and whether some token sees it
+      auto pos_of = [&](int v) { return v < sp.sb ? v : v + sp.shift; };
+      auto used = [&](int v) {
+        const int pos = pos_of(v);
+        return pos < seg.L && (pos < p.sinks || pos >= lo_all);
+      };
       ok = __all_sync(0xffffffffu, ok && wait(C::Q_FULL + qb, k >> 1));  // (the rows' factors)
       m_own = -INFINITY;
 #pragma unroll
@@ -498,6 +557,16 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         const uint32_t nb = n & 1;
         const int st = n % kRing;
         const int valid = min(kTile, seg.L - lt * kTile);
+        const int v0 = lt * kTile;
+        // (uniform) every position of the tile is seen by some token; by all
+        bool all_used = valid == kTile, all_seen = (lt + 1) * kTile <= first_new + 1;
+        if constexpr (PART) {
+          const int end = seg.L - sp.shift;
+          all_used = v0 + kTile <= end &&
+                     !(p.sinks < v0 + kTile && sp.z > v0 && sp.z > p.sinks);
+          all_seen = v0 + kTile <= first_new + 1 - sp.shift &&
+                     (v0 >= max(seg.L - p.window, 0) - sp.shift || v0 + kTile <= p.sinks);
+        }
         ok = __all_sync(0xffffffffu, ok && wait(C::S_FULL + nb, n >> 1) &&
                                          wait(C::SC_FULL + st, n / kRing));
         tc_fence_after();
@@ -505,7 +574,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         float ks[2], vs[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const bool in = row + hf * kHalf < valid;
+          bool in = row + hf * kHalf < valid;
+          if constexpr (PART) in = all_used || used(v0 + row + hf * kHalf);
           ks[hf] = in ? sc[hf * kHalf] : 0.f;
           vs[hf] = in ? sc[kTile + hf * kHalf] : 0.f;
         }
@@ -526,10 +596,14 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           const int p0 = hf * kHalf + 4 * lane;
           const float4 v = *reinterpret_cast<const float4*>(
               reinterpret_cast<const float*>(sm + C::OFF_SC) + (st * 2 + 1) * kTile + p0);
-          vm = fmaxf(vm, p0 < valid ? fabsf(v.x) : 0.f);
-          vm = fmaxf(vm, p0 + 1 < valid ? fabsf(v.y) : 0.f);
-          vm = fmaxf(vm, p0 + 2 < valid ? fabsf(v.z) : 0.f);
-          vm = fmaxf(vm, p0 + 3 < valid ? fabsf(v.w) : 0.f);
+          auto in = [&](int k) {
+            if constexpr (PART) return all_used || used(v0 + k);
+            return k < valid;
+          };
+          vm = fmaxf(vm, in(p0) ? fabsf(v.x) : 0.f);
+          vm = fmaxf(vm, in(p0 + 1) ? fabsf(v.y) : 0.f);
+          vm = fmaxf(vm, in(p0 + 2) ? fabsf(v.z) : 0.f);
+          vm = fmaxf(vm, in(p0 + 3) ? fabsf(v.w) : 0.f);
         }
         vm = warp_max(vm);
         // (scales so small that the factor would overflow: scaled up first)
@@ -550,7 +624,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::S_FREE + nb));
         const float* qs = qs_sm + qb * NR + h0;
-        if ((lt + 1) * kTile <= first_new + 1) {
+        if (all_seen) {
           // (uniform) every query row sees every position of the tile
 #pragma unroll
           for (int e = 0; e < HP; ++e) {
@@ -565,7 +639,11 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
             const int last = first_new + col_tok[h0 + e];  // last position the row sees
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const bool seen = lt * kTile + row + hf * kHalf <= last;
+              bool seen = lt * kTile + row + hf * kHalf <= last;
+              if constexpr (PART) {
+                const int pos = pos_of(v0 + row + hf * kHalf), back = last - pos;
+                seen = back >= 0 && (back < p.window || pos < p.sinks);
+              }
               x[hf][e] = seen ? x[hf][e] * (ks[hf] * qs[e]) : -INFINITY;
             }
           }
@@ -638,12 +716,14 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           }
         }
         // ---- V rows past L_i hold anything: zero them ----
-        if (wg == 0 && valid < kTile) {
+        if (wg == 0 && !all_used) {
           ok = __all_sync(0xffffffffu, ok && wait(C::FULL_V + st, n / kRing));
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int pr = row + hf * kHalf;
-            if (ok && pr >= valid) {
+            bool unused = pr >= valid;
+            if constexpr (PART) unused = !used(v0 + pr);
+            if (ok && unused) {
               const uint32_t dst = s_base + st * C::STAGE + C::K_BYTES + pr * DV;
 #pragma unroll
               for (int c = 0; c < DV / 16; ++c)
@@ -734,6 +814,7 @@ struct F8Call {
   int bsz, max_blocks, num_blocks, dtype;
   void* ws;
   long long ws_bytes;
+  int window = 0, sinks = 0;  // window 0: every position is seen
 };
 
 struct F8Plan {
@@ -779,15 +860,15 @@ int f8_check(const F8Call& x) {
   return GQA_OK;
 }
 
-template <int NR, int DK, int DV>
+template <int NR, int DK, int DV, bool PART>
 cudaError_t launch_f8(const F8Call& x, const F8Plan& pl, F8Params& p, cudaStream_t st) {
   using C = F8Cfg<NR, DK, DV>;
   CUtensorMap mk, mv;
   const uint64_t rows = static_cast<uint64_t>(x.num_blocks) * x.g * x.bsz;
-  const uint32_t box_rows = x.bsz < kTile ? x.bsz : kTile;
+  const uint32_t box_rows = PART ? p.gran : x.bsz < kTile ? x.bsz : kTile;
   if (!encode_u8_map(&mk, x.k, DK, rows, box_rows) || !encode_u8_map(&mv, x.v, DV, rows, box_rows))
     return cudaErrorInvalidValue;
-  auto kern = decode_fp8_kernel<NR, DK, DV>;
+  auto kern = decode_fp8_kernel<NR, DK, DV, PART>;
   static std::atomic<unsigned long long> configured{0};  // devices done, this variant
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -810,12 +891,74 @@ cudaError_t launch_f8(const F8Call& x, const F8Plan& pl, F8Params& p, cudaStream
   return cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
 }
 
-template <int NR>
+template <int NR, bool PART>
 cudaError_t launch_f8_dims(const F8Call& x, const F8Plan& pl, F8Params& p, cudaStream_t st) {
   if (x.dk == 128)
-    return x.dv == 128 ? launch_f8<NR, 128, 128>(x, pl, p, st)
-                       : launch_f8<NR, 128, 64>(x, pl, p, st);
-  return x.dv == 128 ? launch_f8<NR, 64, 128>(x, pl, p, st) : launch_f8<NR, 64, 64>(x, pl, p, st);
+    return x.dv == 128 ? launch_f8<NR, 128, 128, PART>(x, pl, p, st)
+                       : launch_f8<NR, 128, 64, PART>(x, pl, p, st);
+  return x.dv == 128 ? launch_f8<NR, 64, 128, PART>(x, pl, p, st) : launch_f8<NR, 64, 64, PART>(x, pl, p, st);
+}
+
+template <bool PART>
+cudaError_t launch_f8_rows(const F8Call& x, const F8Plan& pl, F8Params& p, cudaStream_t st) {
+  const int rows = x.n * (x.h / x.g);
+  return rows <= 8    ? launch_f8_dims<8, PART>(x, pl, p, st)
+         : rows <= 16 ? launch_f8_dims<16, PART>(x, pl, p, st)
+                      : launch_f8_dims<32, PART>(x, pl, p, st);
+}
+
+int f8_run(const F8Call& x, void* stream) {
+  if (int e = f8_check(x)) return e;
+  int num_sms = 0;
+  F8Params p;
+  if (int e = device_query(&num_sms, &p.status)) return e;
+  const int cap = x.max_blocks * x.bsz;
+  const F8Plan pl = f8_plan(x.b, x.n, x.h, x.g, x.dv, cap, num_sms);
+  if (x.ws_bytes < static_cast<long long>(pl.bytes)) return GQA_ERR_SCRATCH_LIMIT;
+  p.q = static_cast<const __nv_bfloat16*>(x.q);
+  p.k_scale = x.k_scale;
+  p.v_scale = x.v_scale;
+  p.lens = x.lens;
+  p.table = x.table;
+  p.b = x.b;
+  p.nq = x.n;
+  p.h = x.h;
+  p.g = x.g;
+  p.r = x.h / x.g;
+  p.cap = cap;
+  p.bsz = x.bsz;
+  p.max_blocks = x.max_blocks;
+  p.num_blocks = x.num_blocks;
+  p.window = x.window;
+  p.sinks = x.sinks;
+  p.gran = x.bsz < kGrain8 ? x.bsz : kGrain8;
+  p.scale_log2 = static_cast<float>(static_cast<double>(x.scale) * 1.4426950408889634);
+  p.out = static_cast<__nv_bfloat16*>(x.out);
+  p.part_o = static_cast<float*>(x.ws);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(x.ws) + pl.ml_at);
+  p.budget = kKernelWaitBudget;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = x.window > 0 ? launch_f8_rows<true>(x, pl, p, st)
+                                     : launch_f8_rows<false>(x, pl, p, st);
+  if (e != cudaSuccess) return GQA_ERR_CUDA;
+  DecodeLaunch a = {};
+  a.seq_lens = x.lens;
+  a.b = x.b;
+  a.h = x.h;
+  a.g = x.g;
+  a.dv = x.dv;
+  a.nq = x.n;
+  a.cap = cap;
+  a.dtype = x.dtype;
+  a.out = x.out;
+  a.part_o = p.part_o;
+  a.part_ml = p.part_ml;
+  a.nc = static_cast<int>(pl.nc);
+  a.window = x.window;
+  a.sinks = x.sinks;
+  a.gran = p.gran;
+  a.stream = st;
+  return launch_unit_combine(a, kTile) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 }  // namespace
@@ -835,53 +978,25 @@ int gqa_decode_attn_fp8_paged(const void* q, const void* k_pool, const void* v_p
   const F8Call x = {q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, b, n, h, g, d_k,
                     d_v, scale, out, block_size, max_blocks, num_blocks, dtype, workspace,
                     workspace_bytes};
-  if (int e = f8_check(x)) return e;
-  int num_sms = 0;
-  F8Params p;
-  if (int e = device_query(&num_sms, &p.status)) return e;
+  return f8_run(x, stream);
+}
+
+int gqa_decode_attn_fp8_window_paged(const void* q, const void* k_pool, const void* v_pool,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* block_table, const int32_t* seq_lens, int b,
+                                     int n, int h, int g, int d_k, int d_v, float scale,
+                                     int window, int sinks, void* out, int block_size,
+                                     int max_blocks, int num_blocks, int dtype, void* workspace,
+                                     long long workspace_bytes, void* stream) {
+  if (int e = paged_args_check(block_table, g, block_size, max_blocks, num_blocks)) return e;
+  if (window < 1 || sinks < 0) return GQA_ERR_SHAPE;
+  F8Call x = {q, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, b, n, h, g, d_k,
+              d_v, scale, out, block_size, max_blocks, num_blocks, dtype, workspace,
+              workspace_bytes};
   const int cap = max_blocks * block_size;
-  const F8Plan pl = f8_plan(b, n, h, g, d_v, cap, num_sms);
-  if (workspace_bytes < static_cast<long long>(pl.bytes)) return GQA_ERR_SCRATCH_LIMIT;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.lens = seq_lens;
-  p.table = block_table;
-  p.b = b;
-  p.nq = n;
-  p.h = h;
-  p.g = g;
-  p.r = h / g;
-  p.cap = cap;
-  p.bsz = block_size;
-  p.max_blocks = max_blocks;
-  p.num_blocks = num_blocks;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  p.out = static_cast<__nv_bfloat16*>(out);
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.ml_at);
-  p.budget = kKernelWaitBudget;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int rows = n * (h / g);
-  cudaError_t e = rows <= 8    ? launch_f8_dims<8>(x, pl, p, st)
-                  : rows <= 16 ? launch_f8_dims<16>(x, pl, p, st)
-                               : launch_f8_dims<32>(x, pl, p, st);
-  if (e != cudaSuccess) return GQA_ERR_CUDA;
-  DecodeLaunch a = {};
-  a.seq_lens = seq_lens;
-  a.b = b;
-  a.h = h;
-  a.g = g;
-  a.dv = d_v;
-  a.nq = n;
-  a.cap = cap;
-  a.dtype = dtype;
-  a.out = out;
-  a.part_o = p.part_o;
-  a.part_ml = p.part_ml;
-  a.nc = static_cast<int>(pl.nc);
-  a.stream = st;
-  return launch_unit_combine(a, kTile) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+  x.window = window < cap ? window : cap;
+  x.sinks = sinks < cap ? sinks : cap;
+  return f8_run(x, stream);
 }
 
 int gqa_decode_attn_fp8_workspace(int b, int n, int h, int g, int d_k, int d_v, long long cap,

@@ -17,6 +17,7 @@
 #include "../../include/gqa.h"
 #include "gqa_device.cuh"
 #include "gqa_internal.h"
+#include "part_device.cuh"
 
 namespace gqa {
 
@@ -113,11 +114,11 @@ __global__ void kv_append_paged_kernel(const uint4* __restrict__ k_new,
 // ---------------------------------------------------------------------------
 constexpr int kCombineWarps = 4;
 
-template <typename DT, int CPL>
+template <typename DT, int CPL, class Span>
 __global__ void __launch_bounds__(32 * kCombineWarps)
     combine_kernel(const int* __restrict__ lens, int b, int h, int g, int cap, int tile, int nc,
                    int nq, const float* __restrict__ part_o, const float* __restrict__ part_ml,
-                   DT* __restrict__ out) {
+                   DT* __restrict__ out, const Span span) {
   constexpr int d = 32 * CPL;
   __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
   __shared__ float s_o[kCombineWarps][d];
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   int ti = 0;
   for (int base = 0; base < b; base += 32) {
     const int idx = base + lane;
-    const int tt = (idx < b) ? seq_tiles(__ldg(lens + idx), nq, cap, tile) : 0;
+    const int tt = (idx < b) ? span.tiles(__ldg(lens + idx), nq, cap, tile) : 0;
     all += tt;
     if (idx < i) before += tt;
     if (idx == i) ti = tt;
@@ -381,23 +382,27 @@ bool use_combine_kernel(long long nc, int b, int g) { return nc > 2ll * b * g; }
 
 // The combine kernel for the call's V head dim (d_v / 32 output columns a
 // lane).
-template <typename DT>
+template <typename DT, class Span>
 cudaError_t launch_combine(cudaLaunchConfig_t& cfg, const DecodeLaunch& a, int tile,
-                           const float* po, const float* pml) {
+                           const float* po, const float* pml, const Span& span) {
   DT* o = static_cast<DT*>(a.out);
   switch (a.dv) {
     case 64:
-      return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 2>, a.seq_lens, a.b, a.h, a.g, a.cap,
-                                tile, a.nc, a.nq, po, pml, o);
+      return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 2, Span>, a.seq_lens, a.b, a.h, a.g, a.cap,
+                                tile, a.nc, a.nq, po, pml, o, span);
     case 128:
-      return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 4>, a.seq_lens, a.b, a.h, a.g, a.cap,
-                                tile, a.nc, a.nq, po, pml, o);
+      return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 4, Span>, a.seq_lens, a.b, a.h, a.g, a.cap,
+                                tile, a.nc, a.nq, po, pml, o, span);
     case 192:
-      return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 6>, a.seq_lens, a.b, a.h, a.g, a.cap,
-                                tile, a.nc, a.nq, po, pml, o);
+      if constexpr (std::is_same<Span, FullSpan>::value)
+        return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 6, Span>, a.seq_lens, a.b, a.h, a.g,
+                                  a.cap, tile, a.nc, a.nq, po, pml, o, span);
+      return cudaErrorInvalidValue;
     case 256:
-      return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 8>, a.seq_lens, a.b, a.h, a.g, a.cap,
-                                tile, a.nc, a.nq, po, pml, o);
+      if constexpr (std::is_same<Span, FullSpan>::value)
+        return cudaLaunchKernelEx(&cfg, combine_kernel<DT, 8, Span>, a.seq_lens, a.b, a.h, a.g,
+                                  a.cap, tile, a.nc, a.nq, po, pml, o, span);
+      return cudaErrorInvalidValue;
     default:
       return cudaErrorInvalidValue;
   }
@@ -418,9 +423,14 @@ cudaError_t launch_unit_combine(const DecodeLaunch& a, int tile) {
   cfg.numAttrs = 1;
   const float* po = static_cast<const float*>(a.part_o);
   const float* pml = static_cast<const float*>(a.part_ml);
-  if (a.dtype == GQA_BF16) return launch_combine<__nv_bfloat16>(cfg, a, tile, po, pml);
-  if (a.dtype == GQA_F16) return launch_combine<__half>(cfg, a, tile, po, pml);
-  return launch_combine<float>(cfg, a, tile, po, pml);
+  if (a.window > 0) {  // (the 8-bit decode alone, whose outputs are bf16)
+    const WindowSpan span = {a.window, a.sinks, a.gran};
+    return launch_combine<__nv_bfloat16>(cfg, a, tile, po, pml, span);
+  }
+  const FullSpan span;
+  if (a.dtype == GQA_BF16) return launch_combine<__nv_bfloat16>(cfg, a, tile, po, pml, span);
+  if (a.dtype == GQA_F16) return launch_combine<__half>(cfg, a, tile, po, pml, span);
+  return launch_combine<float>(cfg, a, tile, po, pml, span);
 }
 
 namespace {

@@ -367,6 +367,14 @@ __device__ __forceinline__ int seq_tiles(int L, int lmin, int cap, int T) {
   return (L >= lmin && L >= 1 && L <= cap) ? (L + T - 1) / T : 0;
 }
 
+// The tiles that a unit holds: of all its positions, or (part_device.cuh) of
+// those that are seen.
+struct FullSpan {
+  __device__ __forceinline__ int tiles(int L, int lmin, int cap, int T) const {
+    return seq_tiles(L, lmin, cap, T);
+  }
+};
+
 struct Segment {
   int i, j;       // sequence, KV head
   int lt0, lt1;   // local tile range within the unit
@@ -477,7 +485,9 @@ struct PageCursor {
   }
 };
 
-struct Walker {
+template <class Span>
+struct SpanWalker {
+  Span span;
   const int* lens;
   int b, g, lmin, cap, T;
   long long W;         // total tiles of the launch
@@ -489,7 +499,7 @@ struct Walker {
   // total tiles W (warp-cooperative; all lanes get the result); `equal`:
   // every sequence has the same, nonzero, number of tiles
   __device__ static long long total_tiles(const int* lens, int b, int g, int lmin, int cap,
-                                         int T, bool* equal = nullptr) {
+                                         int T, bool* equal = nullptr, Span span = {}) {
     const int lane = threadIdx.x & 31;
     long long acc = 0;
     int tmin = 0x7fffffff, tmax = 0;
@@ -497,7 +507,7 @@ struct Walker {
       const int idx = base + lane;
       int t = 0;
       if (idx < b) {
-        t = seq_tiles(__ldg(lens + idx), lmin, cap, T);
+        t = span.tiles(__ldg(lens + idx), lmin, cap, T);
         tmin = min(tmin, t);
         tmax = max(tmax, t);
       }
@@ -518,7 +528,8 @@ struct Walker {
   // CTAs may take up to this many whole units each (0: never).
   // Warp-cooperative.
   __device__ void init(const int* lens_, int b_, int g_, int lmin_, int cap_, int T_, int c,
-                       int nc, int whole_max = 0) {
+                       int nc, int whole_max = 0, Span span_ = {}) {
+    span = span_;
     lens = lens_;
     b = b_;
     g = g_;
@@ -526,7 +537,7 @@ struct Walker {
     cap = cap_;
     T = T_;
     equal = false;
-    W = total_tiles(lens, b, g, lmin, cap, T, &equal);
+    W = total_tiles(lens, b, g, lmin, cap, T, &equal, span);
     // Equal lengths: k = 1 or 2 whole units per CTA when that still uses at
     // least 70 % of the CTAs, the rest idle (no piece to merge).  Measured on
     // the tensor-core kernel: 128 units on 152 SMs 46.9 -> 42.5 us per call
@@ -558,7 +569,7 @@ struct Walker {
       int Lx = 0, t = 0;
       if (idx < b) {
         Lx = __ldg(lens + idx);
-        t = seq_tiles(Lx, lmin, cap, T);
+        t = span.tiles(Lx, lmin, cap, T);
       }
       long long incl = static_cast<long long>(t) * g;
 #pragma unroll
@@ -607,12 +618,14 @@ struct Walker {
         do {
           ++i;
           L = (i < b) ? __ldg(lens + i) : 0;
-          ti = (i < b) ? seq_tiles(L, lmin, cap, T) : 0;
+          ti = (i < b) ? span.tiles(L, lmin, cap, T) : 0;
         } while (i < b && ti == 0);
       }
     }
     return true;
   }
 };
+
+using Walker = SpanWalker<FullSpan>;
 
 }  // namespace gqa

@@ -42,6 +42,8 @@ struct DecodeLaunch {
   // p % block_size of block block_table[i * max_blocks + p / block_size]
   const int* block_table = nullptr;
   int block_size = 0, max_blocks = 0, num_blocks = 0;
+  // positions seen (combine of a windowed launch; window 0: all), and of a box
+  int window = 0, sinks = 0, gran = 0;
 };
 
 // Tiled TMA map over a row-major bf16 tensor: dims[0] is the contiguous

@@ -585,6 +585,81 @@ int gqa_chunk_attn_workspace(int total, int h, int g, int d_k, int d_v, int num_
                              long long* bytes);
 
 /*
+ * gqa_chunk_attn_window - gqa_chunk_attn where a token sees the last `window`
+ * positions up to its own, and the first `sinks` positions of its sequence:
+ *     out[t, a, :] = sum over p <= P with p > P - window or p < sinks of
+ *                    softmax_p(scale * q[t, a, :] . k_cache[i, j, p, :])
+ *                    v_cache[i, j, p, :]
+ * (window >= 1: a token sees itself; sinks >= 0, 0 for a plain window; both may
+ * exceed the lengths).  Arguments, workspace (the bytes that
+ * gqa_chunk_attn_workspace gives), errors and supported shapes as for
+ * gqa_chunk_attn; cap (paged: max_blocks * block_size) up to 2^31 - 256.
+ * Only rows that some new token of the sequence sees are used: rows p >= L_i
+ * and rows sinks <= p <= L_i - n_i - window may hold anything.
+ *
+ * gqa_chunk_attn_window_paged - the same over a paged cache.  Entries of blocks
+ * that hold no row that is used are not looked at (an engine may have given
+ * those blocks to other sequences).
+ */
+int gqa_chunk_attn_window(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* cu_tokens, const int32_t* seq_lens, int b, int total,
+                          int h, int g, int d_k, int d_v, float scale, int window, int sinks,
+                          void* out, int cap, int dtype, void* workspace,
+                          long long workspace_bytes, void* stream);
+
+int gqa_chunk_attn_window_paged(const void* q, const void* k_pool, const void* v_pool,
+                                const int32_t* block_table, const int32_t* cu_tokens,
+                                const int32_t* seq_lens, int b, int total, int h, int g, int d_k,
+                                int d_v, float scale, int window, int sinks, void* out,
+                                int block_size, int max_blocks, int num_blocks, int dtype,
+                                void* workspace, long long workspace_bytes, void* stream);
+
+/*
+ * gqa_chunk_attn_prefix - gqa_chunk_attn for a batch whose sequences have their
+ * first prefix_len positions in common (a system prompt, a document): those
+ * rows are read from sequence 0's cache rows [0, prefix_len) for every
+ * sequence, the others from each sequence's own.
+ *   seq_lens  L_i counts the prefix: the new tokens of sequence i sit at
+ *             positions L_i - n_i .. L_i - 1, all behind the prefix.  A sequence
+ *             with n_i > 0 and L_i - n_i < prefix_len is skipped and sets
+ *             GQA_DEV_BAD_SEQ_LEN.  (L_0 does not matter when n_0 = 0: sequence
+ *             0 may be there for the prefix alone.)
+ *   prefix_len  0 <= prefix_len <= cap (GQA_ERR_SHAPE otherwise)
+ *   workspace: of the bytes that gqa_chunk_attn_prefix_workspace gives for this
+ *             b and this or a larger total
+ * Rows p < prefix_len of sequences other than 0 and rows p >= L_i may hold
+ * anything; the prefix and the rows prefix_len <= p < L_i hold finite values.
+ * Otherwise as gqa_chunk_attn; cap (paged: max_blocks * block_size) up to
+ * 2^31 - 256.  Where sequences bring few tokens each (total below b times 128 /
+ * (h / g)) the prefix is read once for many of them, with three kernels; else
+ * once for each, with the call's two kernels of gqa_chunk_attn.
+ *
+ * gqa_chunk_attn_prefix_paged - the same over a paged cache: the prefix is
+ * found through row 0 of the block table.  Entries of whole blocks of the
+ * prefix in the other rows are not looked at; where prefix_len is no multiple
+ * of the block size, the block that it ends in holds each sequence's own rows
+ * behind the prefix (row 0's, the prefix's last rows too).
+ *
+ * gqa_chunk_attn_prefix_workspace - host only when num_sms > 0 (0: the current
+ * device's SM count).
+ */
+int gqa_chunk_attn_prefix(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* cu_tokens, const int32_t* seq_lens, int b, int total,
+                          int h, int g, int d_k, int d_v, float scale, int prefix_len, void* out,
+                          int cap, int dtype, void* workspace, long long workspace_bytes,
+                          void* stream);
+
+int gqa_chunk_attn_prefix_paged(const void* q, const void* k_pool, const void* v_pool,
+                                const int32_t* block_table, const int32_t* cu_tokens,
+                                const int32_t* seq_lens, int b, int total, int h, int g, int d_k,
+                                int d_v, float scale, int prefix_len, void* out, int block_size,
+                                int max_blocks, int num_blocks, int dtype, void* workspace,
+                                long long workspace_bytes, void* stream);
+
+int gqa_chunk_attn_prefix_workspace(int b, int total, int h, int g, int d_k, int d_v, int num_sms,
+                                    long long* bytes);
+
+/*
  * gqa_decode_attn_fp8_paged - gqa_decode_attn_paged over an 8-bit paged cache
  * (the pools and scales of gqa_rope_append_fp8_paged): n new tokens per
  * sequence, causal, over rows scale * value of the cache, which already holds
@@ -620,6 +695,22 @@ int gqa_decode_attn_fp8_paged(const void* q, const void* k_pool, const void* v_p
 
 int gqa_decode_attn_fp8_workspace(int b, int n, int h, int g, int d_k, int d_v, long long cap,
                                   int num_sms, long long* bytes);
+
+/*
+ * gqa_decode_attn_fp8_window_paged - gqa_decode_attn_fp8_paged where a token sees
+ * the last `window` positions up to its own and the first `sinks` (as in
+ * gqa_chunk_attn_window: which rows may hold anything and which table entries
+ * are not looked at are the same).  Everything else, the workspace among it, as
+ * for gqa_decode_attn_fp8_paged; the tile of 256 positions is one of the
+ * positions that are seen, in their order.
+ */
+int gqa_decode_attn_fp8_window_paged(const void* q, const void* k_pool, const void* v_pool,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* block_table, const int32_t* seq_lens, int b,
+                                     int n, int h, int g, int d_k, int d_v, float scale,
+                                     int window, int sinks, void* out, int block_size,
+                                     int max_blocks, int num_blocks, int dtype, void* workspace,
+                                     long long workspace_bytes, void* stream);
 
 /* Name of a return code, for messages. */
 const char* gqa_status_string(int status);
