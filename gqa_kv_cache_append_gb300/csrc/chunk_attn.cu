@@ -55,6 +55,7 @@ struct ChunkWalk {
     return launch_join<T16, DV>(cfg, p, num_sms);
   }
 
+  const ChunkParams& p;
   const int *cu, *lens;
   int b, g, tq, total;
   long long cap;
@@ -146,9 +147,11 @@ struct ChunkWalk {
     return {b, 0, 0, 0};  // not reached for x < W
   }
 
+  __device__ explicit ChunkWalk(const ChunkParams& params) : p(params) {}
+
   // Run c's start: false when the launch has fewer runs than that (c = their
   // number: the end of the last one, behind every sequence).
-  __device__ bool start(const ChunkParams& p, int c, int nc, ChunkPos& r) {
+  __device__ bool start(int c, int nc, ChunkPos& r) {
     cu = p.cu;
     lens = p.lens;
     b = p.b;

@@ -127,6 +127,7 @@ struct ChunkParams {
   // the first `head` ones, which are read from sequence head_seq (-1: each
   // from its own); positions below base_min belong to the head alone
   int window, head, head_seq, base_min;
+  unsigned unit_inv;   // 2^32 / (2 tq), rounded up
   // the head is attended by units of its own, over the rows of all sequences,
   // and every unit leaves partial results
   bool grouped;
@@ -211,24 +212,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (blockIdx.x == 0) Walk::report(p);
-  } else if (warp == 11) {
+  } else if (warp >= 10) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    // the run's end, beside the TMA warp's look for its start
-    Walk w;
-    ChunkPos e;
-    w.start(p, blockIdx.x + 1, gridDim.x, e);
-    if (lane == 0) {
-      *run_end = e;
-      mbar_arrive(BAR(C::RUN_END));
-    }
-    __syncwarp();
-  } else if (warp == 10) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    // ============================ TMA producer ============================
-    Walk w;
-    Seg seg;
+    // the run's start, and in warp 11 its end, in the same instructions
+    Walk w(p);
     ChunkPos from;
-    const bool any = w.start(p, blockIdx.x, gridDim.x, from);
+    const bool any = w.start(blockIdx.x + (warp - 10), gridDim.x, from);
+    if (warp == 11) {
+      if (lane == 0) {
+        *run_end = from;
+        mbar_arrive(BAR(C::RUN_END));
+      }
+      __syncwarp();
+    } else {
+    // ============================ TMA producer ============================
+    Seg seg;
     const uint64_t pol = policy_evict_last();
     const int oob_row = PAGED  ? p.num_blocks * p.g * p.bsz
                         : PART ? static_cast<int>(static_cast<long long>(p.b) * p.g * p.cap)
@@ -468,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
+    }
   } else if (warp == 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // ============================ MMA issuer ==============================
@@ -1137,6 +1136,7 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   p.status = status;
   p.budget = kKernelWaitBudget;
   p.window = x.window;
+  p.unit_inv = static_cast<unsigned>(((1ull << 32) + 2 * p.tq - 1) / (2 * p.tq));
   p.head = x.head;
   p.head_seq = x.head_seq;
   p.base_min = x.base_min;

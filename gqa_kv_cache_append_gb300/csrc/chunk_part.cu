@@ -55,25 +55,31 @@ struct PartSeg {
 // the position of their last token until the window is full and are alike from
 // there on, so sums of their work are an arithmetic progression and a multiple.
 // Units of the head come before those of the sequences, as sequence -1.
-constexpr int kPartUnitCost = 320;
+//
+// Every instruction of the walk is fetched once a launch before any copy can
+// start, so it is written for few of them, not for few steps: one scan for the
+// sum and the search, the two warps that look for a run's ends in the same code,
+// divisions by multiplication.  (With five scans and 64-bit divisions inlined a
+// call took 5 us longer with one sequence, 15 with 64.)
+constexpr unsigned kPartUnitCost = 320;
 
 struct PartWalk {
   using Seg = PartSeg;
   using Visible = PartVisible;
   static constexpr bool kPart = true;
 
-  const int *cu, *lens;
-  int b, g, tq, total;
-  long long cap;
-  int window, head, head_seq, base_min, gran;
-  bool grouped, paged;
-  int heads_n;            // tokens of the head's units
-  long long head_f;       // their work, of one KV head
+  const ChunkParams& p;
+  int n_head;    // tokens of the head's units (0: it has none)
+  int gran, head_pad;
   ChunkPos at, end;
   int t0, n, L;  // of sequence at.i
   bool more;
-  int c_t0, c_n, c_L;     // as in chunk_attn.cu
-  long long c_f, c_incl;
+
+  __device__ explicit PartWalk(const ChunkParams& params) : p(params) {
+    n_head = head_tokens(p);
+    gran = p.table != nullptr ? min(p.bsz, kGrain) : kGrain;
+    head_pad = (p.head + gran - 1) & ~(gran - 1);
+  }
 
   __device__ static unsigned errors(int a0, int a1, int Lk, int total, long long cap,
                                     int base_min) {
@@ -95,222 +101,188 @@ struct PartWalk {
   template <typename T16, int DV>
   static cudaError_t join(cudaLaunchConfig_t& cfg, const ChunkParams& p, int num_sms);
 
+  // sequence k (-1: the head)
   __device__ bool seq(int k, int& a0, int& nn, int& Lk) const {
     a0 = nn = Lk = 0;
-    if (k >= b) return false;
-    a0 = __ldg(cu + k);
-    const int a1 = __ldg(cu + k + 1);
-    Lk = __ldg(lens + k);
-    if (errors(a0, a1, Lk, total, cap, base_min)) return false;
-    nn = a1 - a0;
+    if (k < 0) {
+      nn = n_head;
+      Lk = p.head;
+    } else if (k < p.b) {
+      a0 = __ldg(p.cu + k);
+      const int a1 = __ldg(p.cu + k + 1);
+      Lk = __ldg(p.lens + k);
+      if (!errors(a0, a1, Lk, p.total, p.cap, p.base_min)) nn = a1 - a0;
+    }
     return nn > 0;
   }
-  __device__ int units(int nn) const { return (nn + 2 * tq - 1) / (2 * tq); }
-  __device__ bool last_twin(int nn, int nu) const { return nn - (nu - 1) * 2 * tq <= tq; }
+  // x / (2 tq): 2^32 / (2 tq) rounded up is at most one too large
+  __device__ unsigned by_unit(unsigned x) const {
+    const unsigned q = __umulhi(x, p.unit_inv), d = 2 * p.tq;
+    return q * d > x ? q - 1 : q;
+  }
+  __device__ int units(int nn) const { return by_unit(static_cast<unsigned>(nn) + 2 * p.tq - 1); }
 
-  // A unit q has min(A + (q + 1) * 2 tq, B) positions.
+  // A unit q has min(A + (q + 1) * 2 tq, B) positions (as the split counts them:
+  // tiles are cut from the exact span).
   struct Shape {
-    long long A, B;
-    int q0;  // units before the window is full
+    unsigned A, B;
+    int nu, q0;  // units; those before the window is full
+    bool tw;     // the last one is a unit of twins
   };
-  __device__ Shape shape(bool of_head, int nn, int Lk) const {
+  __device__ Shape shape(int k, int nn, int Lk) const {
     Shape s;
-    const int hp = grouped ? 0 : (head + gran - 1) & ~(gran - 1);
-    if (of_head) {
-      s.A = s.B = head;
-    } else {
-      s.A = static_cast<long long>(Lk) - nn - base_min + (head_seq >= 0 ? hp : 0);
-      s.B = static_cast<long long>(window) + 2 * tq + hp;
-      if (head_seq >= 0) s.B = 1ll << 40;
-    }
-    s.q0 = s.B <= s.A ? 0
-                      : static_cast<int>(min(static_cast<long long>(units(nn)),
-                                             div_pos(s.B - s.A, 2 * tq)));
+    const unsigned pad = p.grouped ? 0 : head_pad;
+    s.nu = units(nn);
+    s.tw = nn - (s.nu - 1) * 2 * p.tq <= p.tq;
+    s.A = Lk - nn - p.base_min + (p.head_seq >= 0 ? pad : 0);
+    s.B = p.head_seq >= 0 ? 0xF0000000u : static_cast<unsigned>(p.window) + 2 * p.tq + pad;
+    if (k < 0) s.A = s.B = p.head;
+    s.q0 = s.B <= s.A ? 0 : min(s.nu, static_cast<int>(by_unit(s.B - s.A)));
     return s;
   }
-  __device__ long long prefix(long long q, const Shape& s) const {
-    const long long k = min(q, static_cast<long long>(s.q0));
-    return k * (s.A + kPartUnitCost) + tq * (k * (k + 1)) + (q - k) * (s.B + kPartUnitCost);
+  using U64 = unsigned long long;
+  __device__ U64 prefix(unsigned q, const Shape& s) const {
+    const unsigned k = min(q, static_cast<unsigned>(s.q0));
+    return static_cast<U64>(k) * (s.A + kPartUnitCost) + static_cast<U64>(k * p.tq) * (k + 1) +
+           static_cast<U64>(q - k) * (s.B + kPartUnitCost);
   }
-  __device__ long long work(bool of_head, int nn, int Lk) const {
-    const int nu = units(nn);
-    const Shape s = shape(of_head, nn, Lk);
-    if (!last_twin(nn, nu)) return prefix(nu, s);
-    const long long before = prefix(nu - 1, s);
-    return before + ((3 * (prefix(nu, s) - before - kPartUnitCost)) >> 2) + kPartUnitCost;
+  __device__ unsigned length(unsigned q, const Shape& s) const {
+    return static_cast<int>(q) < s.q0 ? s.A + (q + 1) * 2 * p.tq : s.B;
   }
 
-  // the span and the tiles of unit q of a sequence (of the head)
-  __device__ void span(Seg& s, bool of_head, int q, int nn, int Lk) const {
-    s.of_head = of_head;
-    s.pos0 = Lk - nn + q * 2 * tq;
-    s.ntok = min(nn - q * 2 * tq, 2 * tq);
+  // the span and the tiles of unit q of sequence k
+  __device__ void span(Seg& s, int k, int q, int nn, int Lk) const {
+    const int first = q * 2 * p.tq;
+    s.of_head = k < 0;
+    s.pos0 = Lk - nn + first;
+    s.ntok = min(nn - first, 2 * p.tq);
     s.L = Lk;
-    s.head = grouped && !of_head ? 0 : head;
-    int hi;
-    if (of_head) {
-      s.shift = 0;
-      s.sb = (head + gran - 1) & ~(gran - 1);
-      s.z = s.end = hi = head;
-    } else {
-      const int lo = max(base_min, s.pos0 - window + 1);
-      const int lo_all = max(base_min, Lk - nn - window + 1);
-      const PartSpan t = part_span(lo, lo_all, s.head, gran, paged, head_seq >= 0 || grouped);
-      s.shift = t.shift;
-      s.sb = t.sb;
-      s.z = t.z;
-      s.end = Lk - t.shift;
-      hi = s.pos0 + s.ntok - t.shift;
-    }
-    s.ti = (hi + kN - 1) / kN;
-  }
-  __device__ int tiles(bool of_head, int q, int nn, int Lk) const {
-    Seg s;
-    span(s, of_head, q, nn, Lk);
-    return s.ti;
+    s.head = p.grouped && k >= 0 ? 0 : p.head;
+    const int lo = max(p.base_min, s.pos0 - p.window + 1);
+    const int lo_all = max(p.base_min, Lk - nn - p.window + 1);
+    const PartSpan t = part_span(lo, lo_all, s.head, gran, p.table != nullptr,
+                                 p.head_seq >= 0);
+    s.shift = k < 0 ? 0 : t.shift;
+    s.sb = k < 0 ? head_pad : t.sb;
+    s.z = k < 0 ? 0 : t.z;
+    s.end = Lk - s.shift;
+    const int hi = k < 0 ? Lk : s.pos0 + s.ntok - t.shift;
+    s.ti = (hi + kN - 1) >> 7;
   }
 
-  __device__ void scan(int base, int& a0, int& nn, int& Lk, long long& f, long long& incl) const {
-    f = seq(base + (threadIdx.x & 31), a0, nn, Lk) ? work(false, nn, Lk) : 0;
-    incl = f;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if ((threadIdx.x & 31) >= o) incl += y;
-    }
-  }
-
-  // the place `off` of the work of sequence i (t0, n, L set), fs for a KV head
-  __device__ ChunkPos place(int i, long long off, long long fs, int near) const {
-    ChunkPos r;
-    r.i = i;
-    r.j = static_cast<int>(div_pos(off, fs));
-    const long long rem = off - r.j * fs;
-    const int nu = units(n);
-    const Shape s = shape(i < 0, n, L);
-    // the last unit q with prefix(q) <= rem: the root of the quadratic, or a
-    // division behind it, put right by steps of one
-    const long long full = prefix(s.q0, s);
-    int q;
-    if (rem < full) {
-      const float c1 = static_cast<float>(s.A) + (kPartUnitCost + tq);
-      const float rf = static_cast<float>(rem);
-      q = static_cast<int>(2.f * rf / (sqrtf(c1 * c1 + 4.f * tq * rf) + c1));
-    } else {
-      q = s.q0 + static_cast<int>(min(div_pos(rem - full, s.B + kPartUnitCost),
-                                      static_cast<long long>(nu)));
-    }
-    q = min(max(q, 0), nu - 1);
-    while (q > 0 && prefix(q, s) > rem) --q;
-    while (q + 1 < nu && prefix(q + 1, s) <= rem) ++q;
-    r.qt = q;
-    const int ti = tiles(i < 0, q, n, L);
-    const bool tw = q == nu - 1 && last_twin(n, nu);
-    const long long in = rem - prefix(q, s);
-    const int lt = static_cast<int>((tw ? (in + in / 3) : in) >> 7);
-    r.lt = lt <= near ? 0 : lt >= ti - near ? ti : lt;
-    return r;
-  }
-
-  __device__ ChunkPos locate(long long x, int near) {
-    if (x < head_f * g) {
-      t0 = 0;
-      n = heads_n;
-      L = head;
-      return place(-1, x, head_f, near);
-    }
-    long long carry = head_f;
-    for (int base = 0; base < b; base += 32) {
-      int a0 = c_t0, nn = c_n, Lk = c_L;
-      long long f = c_f, incl = c_incl;
-      if (base > 0) scan(base, a0, nn, Lk, f, incl);
-      const long long hi = (carry + incl) * g, lo = hi - f * g;
-      const unsigned hit = __ballot_sync(0xffffffffu, f > 0 && lo <= x && x < hi);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        t0 = __shfl_sync(0xffffffffu, a0, src);
-        n = __shfl_sync(0xffffffffu, nn, src);
-        L = __shfl_sync(0xffffffffu, Lk, src);
-        const long long off = x - __shfl_sync(0xffffffffu, lo, src);
-        return place(base + src, off, __shfl_sync(0xffffffffu, f, src), near);
+  // The place where run c begins (the end of the last run for c = their number):
+  // false when the launch has fewer runs than that.
+  __device__ bool start(int c, int nc, ChunkPos& r) {
+    const int lane = threadIdx.x & 31;
+    const int k0 = n_head > 0 ? -1 : 0;
+    U64 W = 0, x = 0;
+    unsigned near = 0;
+    r = {p.b, 0, 0, 0};
+    // the first pass sums the work, the second one finds the place of x
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      U64 before = 0;  // (of one KV head)
+#pragma unroll 1
+      for (int base = k0; base < p.b; base += 32) {
+        int a0, nn, Lk;
+        U64 f = 0;
+        if (seq(base + lane, a0, nn, Lk)) {
+          const Shape s = shape(base + lane, nn, Lk);
+          f = prefix(s.nu, s);
+          if (s.tw) f -= length(s.nu - 1, s) >> 2;  // (three quarters of it)
+        }
+        U64 incl = f;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const U64 y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        if (pass == 1) {
+          const U64 hi = (before + incl) * p.g, lo = hi - f * p.g;
+          const unsigned hit = __ballot_sync(0xffffffffu, f > 0 && lo <= x && x < hi);
+          if (hit) {
+            const int src = __ffs(hit) - 1;
+            t0 = __shfl_sync(0xffffffffu, a0, src);
+            n = __shfl_sync(0xffffffffu, nn, src);
+            L = __shfl_sync(0xffffffffu, Lk, src);
+            r.i = base + src;
+            U64 rem = x - __shfl_sync(0xffffffffu, lo, src);
+            const U64 fs = __shfl_sync(0xffffffffu, f, src);
+            // (g is small: steps instead of a 64-bit division)
+            r.j = 0;
+#pragma unroll 1
+            for (int step = 1 << 30; step > 0; step >>= 1)
+              if (r.j + step < p.g && (r.j + step) * fs <= rem) r.j += step;
+            rem -= r.j * fs;
+            // the last unit q with prefix(q) <= rem
+            const Shape s = shape(r.i, n, L);
+            int q = 0;
+#pragma unroll 1
+            for (int step = s.nu > 1 ? 1 << (31 - __clz(s.nu - 1)) : 0; step > 0; step >>= 1)
+              if (q + step < s.nu && prefix(q + step, s) <= rem) q += step;
+            r.qt = q;
+            unsigned in = static_cast<unsigned>(rem - prefix(q, s));
+            if (q == s.nu - 1 && s.tw) in += in / 3;
+            const unsigned lt = in >> 7, ti = (length(q, s) + kN - 1) >> 7;
+            r.lt = lt <= near ? 0 : lt + near >= ti ? 0x7FFFFFFF : static_cast<int>(lt);
+            if (c == 0) r.lt = 0;
+            return true;
+          }
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
       }
-      carry += __shfl_sync(0xffffffffu, incl, 31);
+      if (pass == 0) {
+        W = before * p.g;
+        // (a run is worth at least a tile, two with much work)
+        const U64 most = W / (2 * kN) + 1;
+        if (most < static_cast<U64>(nc)) nc = static_cast<int>(most);
+        if (W == 0 || c > nc) return false;
+        if (c == nc) return true;
+        const U64 run = div_pos(W, nc);
+        near = static_cast<unsigned>(run / (32 * kN));
+        const int left = static_cast<int>(W - run * nc);  // the first `left` runs are one longer
+        x = run * c + min(c, left);
+      }
     }
-    return {b, 0, 0, 0};  // not reached for x < W
-  }
-
-  __device__ bool start(const ChunkParams& p, int c, int nc, ChunkPos& r) {
-    cu = p.cu;
-    lens = p.lens;
-    b = p.b;
-    g = p.g;
-    tq = p.tq;
-    total = p.total;
-    cap = p.cap;
-    window = p.window;
-    head = p.head;
-    head_seq = p.head_seq;
-    base_min = p.base_min;
-    grouped = p.grouped;
-    paged = p.table != nullptr;
-    gran = paged ? min(p.bsz, kGrain) : kGrain;
-    heads_n = head_tokens(p);
-    head_f = heads_n > 0 ? work(true, heads_n, head) : 0;
-    scan(0, c_t0, c_n, c_L, c_f, c_incl);
-    long long W = head_f + __shfl_sync(0xffffffffu, c_incl, 31);
-    for (int base = 32; base < b; base += 32) {
-      int a0, nn, Lk;
-      long long f, incl;
-      scan(base, a0, nn, Lk, f, incl);
-      W += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    W *= g;
-    r = {b, 0, 0, 0};
-    nc = static_cast<int>(min(static_cast<long long>(nc), W / (2 * kN) + 1));
-    if (W == 0 || c > nc) return false;
-    if (c == nc) return true;
-    const long long run = div_pos(W, nc);
-    const int near = static_cast<int>(run / (32 * kN));
-    const int left = static_cast<int>(W - run * nc);
-    r = locate(run * c + min(c, left), near);
-    if (c == 0) r.lt = 0;
-    return true;
+    return true;  // not reached for x < W
   }
 
   __device__ void begin(const ChunkPos& from, const ChunkPos& e) {
     at = from;
     end = e;
-    more = at.i < b;
-    if (more && at.lt >= tiles(at.i < 0, at.qt, n, L)) advance();
-  }
-
-  __device__ void advance() {  // to the next unit's start
-    at.lt = 0;
-    if (++at.qt < units(n)) return;
-    at.qt = 0;
-    if (++at.j < g) return;
-    at.j = 0;
-    do {
-      ++at.i;
-    } while (at.i < b && !seq(at.i, t0, n, L));
+    more = at.i < p.b;
   }
 
   __device__ bool next(Seg& s) {
-    if (!more || at.i >= b) return false;
-    const bool last = at.i == end.i && at.j == end.j && at.qt == end.qt;
-    const bool past = at.i > end.i || (at.i == end.i && (at.j > end.j ||
-                                       (at.j == end.j && at.qt > end.qt)));
-    if (past || (last && end.lt <= at.lt)) return false;
-    span(s, at.i < 0, at.qt, n, L);
-    s.i = max(at.i, 0);
-    s.j = at.j;
-    s.t0 = t0 + at.qt * 2 * tq;
-    s.lt0 = at.lt;
-    s.lt1 = last ? end.lt : s.ti;
-    if (last)
-      more = false;
-    else
-      advance();
-    return true;
+    while (more) {
+      const bool last = at.i == end.i && at.j == end.j && at.qt == end.qt;
+      const bool past = at.i > end.i || (at.i == end.i && (at.j > end.j ||
+                                         (at.j == end.j && at.qt > end.qt)));
+      if (past || (last && end.lt <= at.lt)) break;
+      span(s, at.i, at.qt, n, L);
+      s.i = max(at.i, 0);
+      s.j = at.j;
+      s.t0 = t0 + at.qt * 2 * p.tq;
+      s.lt0 = at.lt;
+      s.lt1 = last ? min(end.lt, s.ti) : s.ti;
+      more = !last;
+      if (!last) {  // to the next unit's start
+        at.lt = 0;
+        if (++at.qt >= units(n)) {
+          at.qt = 0;
+          if (++at.j >= p.g) {
+            at.j = 0;
+            do {
+              ++at.i;
+            } while (at.i < p.b && !seq(at.i, t0, n, L));
+            more = at.i < p.b;
+          }
+        }
+      }
+      if (s.lt0 < s.lt1) return true;
+    }
+    more = false;
+    return false;
   }
 };
 
@@ -461,14 +433,14 @@ int part_run(const ChunkCall& x, void* stream) {
 // (cap: positions that the cache can hold)
 int window_run(ChunkCall& x, int window, int sinks, void* stream) {
   if (window < 1 || sinks < 0) return GQA_ERR_SHAPE;
-  x.window = window;
+  x.window = std::min(window, std::max(x.cap, 1));
   x.head = std::min(sinks, std::max(x.cap, 0));
   return part_run(x, stream);
 }
 
 int prefix_run(ChunkCall& x, int prefix_len, void* stream) {
   if (prefix_len < 0 || (x.cap >= 1 && prefix_len > x.cap)) return GQA_ERR_SHAPE;
-  x.window = 0x7FFFFFFF;
+  x.window = std::max(x.cap, 1);
   x.head = x.base_min = prefix_len;
   x.head_seq = 0;
   if (x.g > 0 && x.h > 0 && x.h / x.g >= 1 && x.h / x.g <= kM)
