@@ -10,15 +10,17 @@ struct ChunkSeg {
   int t0;          // packed row of the unit's first token
   int pos0;        // its position
   int ntok;        // tokens of the unit
-  int L;
+  int L, end;      // (the same: no row behind it is used)
   int lt0, lt1;    // tiles of the unit taken here
   int ti;          // tiles of the unit
+  int ph, qb;      // twins: the side of the first tile, the query rows' buffer
+  static constexpr int head = 0, z = 0;
   // A unit whose rows fit side A alone runs as twins: both sides hold the same
   // rows and take the tiles by turns, and their results are joined at the end.
   __device__ bool twin(int tq) const { return ntok <= tq; }
   // tiles that each side works on of [lt0, lt1)
   __device__ int side_tiles(int side, int tq) const {
-    if (twin(tq)) return (lt1 - lt0 + 1 - side) >> 1;
+    if (twin(tq)) return (lt1 - lt0 + 1 - (side ^ ph)) >> 1;
     const int nt = min(ntok - side * tq, tq);
     const int ext = pos0 + side * tq + nt;
     return max(0, min(lt1, (ext + kN - 1) / kN) - lt0);
@@ -214,7 +216,7 @@ struct ChunkWalk {
     s.t0 = t0 + at.qt * 2 * tq;
     s.pos0 = L - n + at.qt * 2 * tq;
     s.ntok = min(n - at.qt * 2 * tq, 2 * tq);
-    s.L = L;
+    s.L = s.end = L;
     s.ti = ti;
     s.lt0 = at.lt;
     s.lt1 = last ? end.lt : ti;

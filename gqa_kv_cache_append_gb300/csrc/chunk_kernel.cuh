@@ -78,7 +78,8 @@ constexpr int kThreads = 384;     // two softmax warpgroups, one of single warps
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kDescInts = 8;      // per CTA, see below
 constexpr int kSegs = 4;          // segments announced ahead
-constexpr int kSegBytes = 64;
+constexpr int kSegBytes = 80;
+constexpr int kEdges = 8;         // V tiles to be zeroed in part: more than a ring holds of V
 constexpr int kGrain = 64;        // positions of a box where a part of the cache is read, at most
 // A row's reference maximum is raised when the new one is this much larger, and
 // P is taken this much higher (both base 2).
@@ -100,11 +101,13 @@ struct ChunkCfg {
                        S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs,
                        V_EDGE = SEG_EMPTY + kSegs,
-                       TWIN = V_EDGE + 1, RUN_END = TWIN + 2, DRAIN = RUN_END + 1, NBAR = DRAIN + 1;
+                       TWIN = V_EDGE + kEdges, RUN_END = TWIN + 2, DRAIN = RUN_END + 1, NBAR = DRAIN + 1;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
   static constexpr int OFF_ML = OFF_SEG + kSegs * kSegBytes;  // float2 [2][kM]: twins' maxima, sums
   static constexpr int OFF_MISC = OFF_ML + 2 * kM * 8;  // TMEM address, abort flag; the run's end
-  static constexpr int SMEM = OFF_MISC + 32;
+  static constexpr int OFF_EDGE = OFF_MISC + 32;        // int4 [kEdges]
+  static constexpr int SMEM = OFF_EDGE + 16 * kEdges;
+  static_assert(NS / 2 < kEdges, "edges in flight");
   static constexpr int T_S = 0, T_O = 256;  // TMEM columns, 128 to a side
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -154,6 +157,7 @@ enum { D_HEAD = 0, D_TOK0 = 1, D_NTOK = 2, D_J = 3, D_END = 4 };
 template <typename T16, int DK, int DV, bool PAGED, class Walk>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_q1,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
   using C = ChunkCfg<DK, DV>;
@@ -185,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 10 && lane == 0) {
     prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_q1);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
@@ -223,6 +228,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         *run_end = from;
         mbar_arrive(BAR(C::RUN_END));
       }
+      // V tiles some of whose rows nobody sees: rows [x, y) and from z on are
+      // zeroed before the products may read them.  (By the TMA warp it cost a
+      // microsecond of its copies for each.)
+      for (uint32_t e = 0;; ++e) {
+        if (!__all_sync(0xffffffffu, wait(C::V_EDGE + e % kEdges, e / kEdges))) break;
+        const int4 v = *reinterpret_cast<const int4*>(sm + C::OFF_EDGE + 16 * (e % kEdges));
+        if (v.w < 0) break;
+        const uint32_t dst = s_base + C::OFF_RING + v.w * C::SLOT;
+        for (int idx = lane; idx < kN * 8; idx += 32) {
+          const int r8 = idx >> 3;
+          if ((r8 < v.x || r8 >= v.y) && r8 < v.z) continue;
+#pragma unroll
+          for (int c = 0; c < DV / 64; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             dst + c * (kN * 128) + idx * 16),
+                         "r"(0u)
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::FULL + v.w));
+      }
       __syncwarp();
     } else {
     // ============================ TMA producer ============================
@@ -236,89 +263,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sh = PAGED ? __ffs(p.bsz) - 1 : 0, mask = p.bsz - 1;  // (a power of two)
     uint32_t slot_n = 0, qn[2] = {0, 0}, edge_n = 0;
     uint32_t kn = 0;  // segments announced
+    uint32_t twins = 0, twin_q = 0;  // tiles of twins so far; the next twins' query rows
     bool ok = __all_sync(0xffffffffu, wait(C::RUN_END, 0));
     w.begin(any ? from : ChunkPos{p.b, 0, 0, 0}, ok ? *run_end : ChunkPos{p.b, 0, 0, 0});
-    // PART: a V tile whose rows that nobody sees are still to be zeroed: its
-    // slot and segment.  The copies behind it go on meanwhile; it is dealt with
-    // when it has landed, at the latest before this warp would wait.
-    int edge_slot = -1, edge_at = 0, edge_head = 0, edge_z = 0, edge_end = 0;
-    auto zero_edge = [&]() {
-      if (edge_slot < 0) return;
-      ok = __all_sync(0xffffffffu, ok && wait(C::V_EDGE, edge_n & 1));
-      ++edge_n;
-      if (ok) {
-        const uint32_t dst = s_base + C::OFF_RING + edge_slot * C::SLOT;
-        const int a0 = max(edge_head - edge_at, 0), a1 = min(edge_z - edge_at, kN);
-        const int b0 = max(edge_end - edge_at, 0);
-        auto clear = [&](int r0, int r1) {
-          for (int idx = r0 * 8 + lane; idx < r1 * 8; idx += 32)
-#pragma unroll
-            for (int c = 0; c < DV / 64; ++c)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               dst + c * (kN * 128) + idx * 16),
-                           "r"(0u)
-                           : "memory");
-        };
-        clear(a0, a1);
-        clear(b0, kN);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::FULL + edge_slot));
-        __syncwarp();
+    while (true) {
+      const bool more = ok && w.next(seg);
+      if (!more) seg.lt0 = seg.lt1 = 0;
+      const int T = seg.lt1 - seg.lt0;
+      const bool twin = seg.twin(p.tq);
+      if (more) {
+        seg.ph = twins & 1;
+        if (twin) {
+          seg.qb = twin_q;
+          twins += T;
+          twin_q ^= 1;
+        } else {
+          twin_q = 0;
+        }
       }
-      edge_slot = -1;
-    };
-    // (a wait of this warp)
-    auto hold = [&](int k, uint32_t phase) {
-      if constexpr (PART) {
-        if (edge_slot >= 0 && (!__all_sync(0xffffffffu, mbar_try_wait(BAR(k), phase & 1u)) ||
-                               __any_sync(0xffffffffu, mbar_try_wait(BAR(C::V_EDGE), edge_n & 1))))
-          zero_edge();
-      }
-      ok = __all_sync(0xffffffffu, ok && wait(k, phase));
-    };
-    auto announce = [&](const Seg& sg) {
-      hold(C::SEG_EMPTY + kn % kSegs, ((kn / kSegs) & 1) ^ 1);
-      if (!ok) return;
-      if (lane == 0) {
-        *seg_at(kn) = sg;
-        mbar_arrive(BAR(C::SEG_FULL + kn % kSegs));
-      }
-      __syncwarp();
-      ++kn;
-    };
-    while (ok && w.next(seg)) {
-      announce(seg);
       // the sequence's table entries, 64 at a time ahead of their use: no load
       // stands before a tile's copies
       PageCursor pc;
       if constexpr (PAGED && !PART)
-        pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
-                 static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
-                 (seg.lt0 * kN) >> sh);
-      // lane mm < sub: the pool row of box mm of tile lt
-      auto lookup = [&](int lt) -> int {
-        if constexpr (PART) return 0;
-        const int pm = lt * kN + lane * box;
-        const int blk = pc.get_lanes((lt * kN) >> sh);
-        if (lane >= sub || pm >= seg.L) return oob_row;
-        if (blk < 0 || blk >= p.num_blocks) {
-          atomicOr(p.status, GQA_DEV_BAD_BLOCK);
-          return oob_row;
-        }
-        return (blk * p.g + seg.j) * p.bsz + (pm & mask);
-      };
+        if (more)
+          pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
+                   static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
+                   (seg.lt0 * kN) >> sh);
       // PART: the position of this lane's box of tile lt (-1: none), and the
       // table entry that holds it.  (One load a box, a tile ahead of its use:
       // a tile's boxes may lie in two places.)
       auto box_at = [&](int lt) -> int {
+        const int v = lt * kN + lane * box;
         if constexpr (PART) {
-          const int v = lt * kN + lane * box;
           const bool in_head = v < seg.sb;
           const int pos = in_head ? v : v + seg.shift;
           return lane < sub && pos < (in_head ? seg.head : seg.L) ? pos : -1;
         }
-        return -1;
+        return lane < sub && v < seg.L ? v : -1;
       };
       auto source = [&](int lt) -> int {
         if constexpr (PART)
@@ -326,131 +307,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         return seg.i;
       };
       auto entry = [&](int lt) -> int {
-        const int pos = box_at(lt);
-        if (!PAGED || pos < 0) return 0;
-        return __ldg(p.table + static_cast<size_t>(source(lt)) * p.max_blocks + (pos >> sh));
-      };
-      auto box_row = [&](int lt, int ent) -> int {
-        const int pos = box_at(lt);
-        if (pos < 0) return oob_row;
-        if (!PAGED)
-          return static_cast<int>((static_cast<long long>(source(lt)) * p.g + seg.j) * p.cap) + pos;
-        if (ent < 0 || ent >= p.num_blocks) {
-          atomicOr(p.status, GQA_DEV_BAD_BLOCK);
-          return oob_row;
+        if constexpr (PAGED && PART) {
+          const int pos = box_at(lt);
+          if (pos >= 0)
+            return __ldg(p.table + static_cast<size_t>(source(lt)) * p.max_blocks + (pos >> sh));
         }
-        return (ent * p.g + seg.j) * p.bsz + (pos & mask);
+        return 0;
       };
+      int ent = more ? entry(seg.lt0) : 0, row = 0;
+      auto hold = [&](int k, uint32_t phase) {
+        ok = __all_sync(0xffffffffu, ok && wait(k, phase));
+        return ok;
+      };
+      if (!hold(C::SEG_EMPTY + kn % kSegs, (kn / kSegs) ^ 1)) break;
+      if (lane == 0) {
+        *seg_at(kn) = seg;
+        mbar_arrive(BAR(C::SEG_FULL + kn % kSegs));
+      }
+      __syncwarp();
+      ++kn;
+      if (!more) break;
+      // query rows of a side (twins: of both)
       auto load_q = [&](int side) {
-        if (!ok || seg.side_tiles(side, p.tq) == 0) return;
-        hold(C::Q_EMPTY + side, (qn[side] & 1) ^ 1);
-        if (!ok) return;
+        const int qb = twin ? seg.qb : side;
+        if (seg.side_tiles(side, p.tq) == 0 && !twin) return;
+        if (!hold(C::Q_EMPTY + qb, (qb ? qn[1] : qn[0]) ^ 1)) return;
+        // (a twin's rows from one token: one box of its heads, the rest of the
+        // tile holds anything)
+        const bool one = twin && seg.ntok == 1;
         if (lane == 0) {
-          mbar_arrive_expect_tx(BAR(C::Q_FULL + side), p.tq * p.r * DK * 2);
+          const uint32_t dst = s_base + qb * C::Q_BYTES;
+          mbar_arrive_expect_tx(BAR(C::Q_FULL + qb), (one ? 1 : p.tq) * p.r * DK * 2);
+#pragma unroll 1
           for (int c = 0; c < DK / 64; ++c)
-            tma_load_3d(s_base + side * C::Q_BYTES + c * (kM * 128), &tm_q, BAR(C::Q_FULL + side),
-                        64 * c, seg.j * p.r, seg.t0 + (seg.twin(p.tq) ? 0 : side * p.tq), pol);
+            tma_load_3d(dst + c * (kM * 128), one ? &tm_q1 : &tm_q, BAR(C::Q_FULL + qb), 64 * c,
+                        seg.j * p.r, seg.t0 + side * p.tq, pol);
         }
-        ++qn[side];
+        if (qb)
+          ++qn[1];
+        else
+          ++qn[0];
       };
-      auto load_kv = [&](bool is_v, int lt, int prow) {
-        if (!ok) return;
-        const int slot = slot_n % C::NS;
-        hold(C::EMPTY + slot, ((slot_n / C::NS) & 1) ^ 1);
-        if (!ok) return;
-        const int nbox = (is_v ? DV : DK) / 64;
-        if constexpr (PART) {
-          const int v0 = lt * kN;
-          const bool edge = is_v && (v0 + kN > seg.end || (seg.head < v0 + kN && seg.z > v0 &&
-                                                           seg.z > seg.head));
-          if (edge) {
-            zero_edge();  // (the one before)
-            if (!ok) return;
+      load_q(0);
+      // K and V of the tiles by turns: the order the products need them
+      for (int lt = seg.lt0; lt < seg.lt1 && ok; ++lt) {
+        // the pool or cache row of this lane's box, for the tile's K and V
+        const int pos = box_at(lt);
+        row = oob_row;
+        if constexpr (PAGED) {
+          if constexpr (!PART) ent = pc.get_lanes((lt * kN) >> sh);
+          if (pos >= 0) {
+            if (ent >= 0 && ent < p.num_blocks)
+              row = (ent * p.g + seg.j) * p.bsz + (pos & mask);
+            else
+              atomicOr(p.status, GQA_DEV_BAD_BLOCK);
           }
-          const uint32_t bar = BAR(edge ? C::V_EDGE : C::FULL + slot);
-          const uint32_t dst = s_base + C::OFF_RING + slot * C::SLOT;
-          if (lane == 0) mbar_arrive_expect_tx(bar, nbox * kN * 128);
-          __syncwarp();
-          if (lane < sub)
-            for (int c = 0; c < nbox; ++c)
-              tma_load_2d(dst + c * (kN * 128) + lane * box * 128, is_v ? &tm_v : &tm_k, bar,
-                          64 * c, prow, pol);
-          if (edge) {
-            edge_slot = slot;
-            edge_at = v0;
-            edge_head = seg.head;
-            edge_z = seg.z;
-            edge_end = seg.end;
-          }
-          ++slot_n;
-          return;
+          if (PART && lt + 1 < seg.lt1) ent = entry(lt + 1);
+        } else if (pos >= 0) {
+          row = static_cast<int>((static_cast<long long>(source(lt)) * p.g + seg.j) * p.cap) + pos;
         }
-        // a V tile that runs past L_i: its rows there are zeroed first
-        const bool edge = is_v && (lt + 1) * kN > seg.L;
-        const uint32_t bar = BAR(edge ? C::V_EDGE : C::FULL + slot);
-        const uint32_t dst = s_base + C::OFF_RING + slot * C::SLOT;
-        if (lane == 0) mbar_arrive_expect_tx(bar, nbox * kN * 128);
+        int slot = slot_n % C::NS;
+        if (!hold(C::EMPTY + slot, (slot_n / C::NS) ^ 1)) break;
+        uint32_t to = BAR(C::FULL + slot), dst = s_base + C::OFF_RING + slot * C::SLOT;
+        if (lane == 0) mbar_arrive_expect_tx(to, DK / 64 * kN * 128);
         __syncwarp();
-        if (PAGED ? lane < sub : lane == 0) {
-          const int row = PAGED ? prow
-                                : static_cast<int>((static_cast<long long>(seg.i) * p.g + seg.j) *
-                                                   p.cap) + lt * kN;
-          for (int c = 0; c < nbox; ++c)
-            tma_load_2d(dst + c * (kN * 128) + lane * box * 128, is_v ? &tm_v : &tm_k, bar, 64 * c,
-                        row, pol);
-        }
-        if (edge) {
-          ok = __all_sync(0xffffffffu, wait(C::V_EDGE, edge_n & 1));
-          ++edge_n;
-          if (ok) {
-            const int first = seg.L - lt * kN;
-            for (int idx = first * 8 + lane; idx < kN * 8; idx += 32)
-              for (int c = 0; c < nbox; ++c)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 dst + c * (kN * 128) + idx * 16),
-                             "r"(0u)
-                             : "memory");
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::FULL + slot));
-          }
+        if (lane < sub) {
+#pragma unroll
+          for (int c = 0; c < DK / 64; ++c)
+            tma_load_2d(dst + c * (kN * 128) + lane * box * 128, &tm_k, to, 64 * c, row, pol);
         }
         ++slot_n;
-      };
-      if constexpr (PART) {
-        int ent = entry(seg.lt0);
-        load_q(0);
-        int row = box_row(seg.lt0, ent);
-        if (seg.lt0 + 1 < seg.lt1) ent = entry(seg.lt0 + 1);
-        load_kv(false, seg.lt0, row);
-        load_q(1);
-        for (int lt = seg.lt0; lt < seg.lt1 && ok; ++lt) {
-          load_kv(true, lt, row);
-          if (lt + 1 < seg.lt1) {
-            row = box_row(lt + 1, ent);
-            if (lt + 2 < seg.lt1) ent = entry(lt + 2);
-            load_kv(false, lt + 1, row);
-          }
+        if (lt == seg.lt0 && !twin) load_q(1);
+        slot = slot_n % C::NS;
+        if (!hold(C::EMPTY + slot, (slot_n / C::NS) ^ 1)) break;
+        to = BAR(C::FULL + slot), dst = s_base + C::OFF_RING + slot * C::SLOT;
+        const int v0 = lt * kN;
+        if (v0 + kN > seg.end || (seg.head < v0 + kN && seg.z > v0 && seg.z > seg.head)) {
+          if (lane == 0)
+            *reinterpret_cast<int4*>(sm + C::OFF_EDGE + 16 * (edge_n % kEdges)) =
+                make_int4(max(seg.head - v0, 0), seg.z - v0, max(seg.end - v0, 0), slot);
+          to = BAR(C::V_EDGE + edge_n % kEdges);
+          ++edge_n;
         }
-        continue;
+        if (lane == 0) mbar_arrive_expect_tx(to, DV / 64 * kN * 128);
+        __syncwarp();
+        if (lane < sub) {
+#pragma unroll
+          for (int c = 0; c < DV / 64; ++c)
+            tma_load_2d(dst + c * (kN * 128) + lane * box * 128, &tm_v, to, 64 * c, row, pol);
+        }
+        ++slot_n;
       }
-      int row = PAGED ? lookup(seg.lt0) : 0;
-      load_q(0);
-      load_kv(false, seg.lt0, row);
-      load_q(1);
-      for (int lt = seg.lt0; lt < seg.lt1 && ok; ++lt) {
-        const int cur = row;
-        if (PAGED && lt + 1 < seg.lt1) row = lookup(lt + 1);
-        // tile lt's V, then tile lt + 1's K: the order the products need them
-        load_kv(true, lt, cur);
-        if (lt + 1 < seg.lt1) load_kv(false, lt + 1, row);
-      }
+      if (!ok) break;
     }
-    if (ok) {
-      seg.lt0 = seg.lt1 = 0;  // no more
-      announce(seg);
+    if (ok && lane == 0) {  // no more edges
+      *reinterpret_cast<int4*>(sm + C::OFF_EDGE + 16 * (edge_n % kEdges)) = make_int4(0, 0, 0, -1);
+      mbar_arrive(BAR(C::V_EDGE + edge_n % kEdges));
     }
-    if constexpr (PART) zero_edge();
+    __syncwarp();
     if (!ok) {
       // copies in flight must land before the CTA exits (bounded)
       const long long t0 = clock64();
@@ -493,169 +447,208 @@ __global__ void __launch_bounds__(kThreads, 1)
         return r;
       }
     };
-    Ring at;  // next position to be used
-    uint32_t kn = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
     bool ok = true;
     auto all_wait = [&](int k, uint32_t phase) {
       ok = __all_sync(0xffffffffu, ok && wait(k, phase));
     };
+    uint32_t kn = 0;                // segments read
+    uint32_t q_ph = 0, p_ph = 0;    // a bit for each query buffer, each side
     // the next segment: its tiles (0: no more), and the sides'
     struct Todo {
-      int T, nt[2];
+      int T, nt0, nt1, qb;
       bool twin;
     };
     auto next_seg = [&]() -> Todo {
-      Todo r = {0, {0, 0}, false};
-      all_wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1);
+      Todo r = {0, 0, 0, 0, false};
+      all_wait(C::SEG_FULL + kn % kSegs, kn / kSegs);
       if (!ok) return r;
-      const Seg seg = *seg_at(kn);
-      r.nt[0] = __shfl_sync(0xffffffffu, seg.side_tiles(0, p.tq), 0);
-      r.nt[1] = __shfl_sync(0xffffffffu, seg.side_tiles(1, p.tq), 0);
+      const Seg& seg = *seg_at(kn);
       r.T = __shfl_sync(0xffffffffu, seg.lt1 - seg.lt0, 0);
       r.twin = __shfl_sync(0xffffffffu, seg.twin(p.tq) ? 1 : 0, 0) != 0;
+      r.qb = __shfl_sync(0xffffffffu, seg.qb, 0);
+      r.nt0 = __shfl_sync(0xffffffffu, seg.side_tiles(0, p.tq), 0);
+      r.nt1 = r.T;  // (the later tokens: they see what the unit sees)
+      __syncwarp();
       if (elect_one()) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
       ++kn;
       return r;
     };
-    // S of side s with the K tile at ring position x
-    auto issue_s = [&](int s, Ring x, bool first, bool last) {
-      if (first) {
-        all_wait(C::Q_FULL + s, qn[s] & 1);
-        ++qn[s];
-      }
-      all_wait(C::FULL + x.slot, x.phase);
-      if (!ok) return;
-      tc_fence_after();
-      const uint64_t a0 = q0 + ((s * C::Q_BYTES) >> 4);
-      const uint64_t b0 = k0 + x.slot * (C::SLOT >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-          const uint32_t o = ((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4;
-          mma_bf16(C::T_S + s * 128, a0 + o, b0 + o, kIdescS, k > 0 ? 1u : 0u);
+    // Two-sided units: in round t side A's P.V of tile t - 1 and its S of tile t,
+    // then side B's; at a unit's end the S of the next unit's first tile.
+    Ring at;               // V of tile t - 1 (t = 0: K of tile 0)
+    int t = 0, s = 0;
+    bool primed = false;   // the next unit's first S are out
+    // Twins: tiles by turns, without a break between units, S two tiles ahead of P.V.
+    bool stream = false, have = false, ended = false;
+    Ring ks, vo;           // K of the next S, V of the next P.V
+    uint32_t n_s = 0, n_o = 0, flags = 0;  // tiles so far; first, last of a side (two bits each)
+    int ts = 0;
+    Todo cur = next_seg(), nx = cur;
+    // One loop for everything but the steady rounds of two-sided units, with one
+    // place for either product: what runs once a unit is fetched each time.
+    while (ok) {
+      bool do_o = false, do_s = false, o_first = false, o_last = false, s_first = false,
+           s_last = false, o_free = false, s_free = false;
+      int side_o = 0, side_s = 0, qb = 0;
+      Ring ov, sk;
+      if (stream) {
+        // S of tiles 0 and 1, then P.V of a tile and S of the one after next
+        if (!have && !ended) {
+          nx = next_seg();
+          if (!ok) break;
+          have = nx.T > 0 && nx.twin;
+          ended = !have;
+          if (have) cur = nx;
+          ts = 0;
         }
-        mma_commit(BAR(C::S_FULL + s));
-        if (last) mma_commit(BAR(C::Q_EMPTY + s));
-      }
-      __syncwarp();
-    };
-    auto issue_o = [&](int s, Ring x, bool first, bool last) {
-      const uint64_t b0 = v0 + x.slot * (C::SLOT >> 4);
-      all_wait(C::FULL + x.slot, x.phase);
-      all_wait(C::P_READY + s, pn[s] & 1);
-      ++pn[s];
-      if (!ok) return;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kN / 16; ++k)
-          mma_16_ts(C::T_O + s * 128, C::T_S + s * 128 + 8 * k, b0 + k * (2048 >> 4), kIdescO,
-                    (first && k == 0) ? 0u : 1u);
-        if (last) mma_commit(BAR(C::O_DONE + s));
-      }
-      __syncwarp();
-    };
-    auto give_back = [&](Ring x) {  // (some side has waited for its copy)
-      if (elect_one()) mma_commit(BAR(C::EMPTY + x.slot));
-      __syncwarp();
-    };
-    Todo cur = next_seg();
-    bool primed = false;  // the segment's first S are out already
-    while (cur.T > 0 && ok) {
-      if (cur.twin) {
-        // (K, V of tile t at positions 2 t, 2 t + 1; tile t is side t & 1's)
-        Ring k = at;
-        issue_s(0, k, true, cur.nt[0] == 1);
-        give_back(k);
-        if (cur.nt[1] > 0) {
-          k = at.next().next();
-          issue_s(1, k, true, cur.nt[1] == 1);
-          give_back(k);
+        if (ended && n_o == n_s) {
+          stream = false;
+          cur = nx;
+          at = ks;
+          primed = false;
+          t = s = 0;
+          continue;
         }
-        for (int t = 0; t < cur.T && ok; t += 2) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (t + s >= cur.T) break;
-            at = at.next();
-            issue_o(s, at, t == 0, t + s + 2 >= cur.T);
-            give_back(at);
-            at = at.next();
-            k = at.next().next();
-            if (t + s + 2 < cur.T) {
-              issue_s(s, k, false, t + s + 4 >= cur.T);
-              give_back(k);
-            }
-          }
+        sk = ks;
+        ov = vo;
+        qb = cur.qb;
+        side_s = n_s & 1;
+        side_o = n_o & 1;
+        do_o = n_s - n_o == 2 || !have;
+        do_s = have;
+        s_first = ts == 0;
+        s_last = ts == cur.T - 1;
+        o_first = (flags >> (2 * side_o)) & 1u;  // (of the tile whose S went out before)
+        o_last = (flags >> (2 * side_o + 1)) & 1u;
+        o_free = s_free = true;
+      } else {
+        if (cur.T == 0) break;
+        if (cur.twin) {
+          stream = have = true;
+          ended = false;
+          ks = at;
+          vo = at.next();
+          ts = 0;
+          continue;
         }
-        cur = next_seg();
-        continue;
-      }
-      if (!primed) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (cur.nt[s] > 0) issue_s(s, at, true, cur.nt[s] == 1);
-        give_back(at);
-        at = at.next();
-      }
-      Todo nx = {0, {0, 0}, false};
-      // rounds in which both sides have a P.V and an S that is not their last
-      const int inner = min(cur.nt[0], cur.nt[1]) - 1;
-      for (int t = 1; t <= cur.T && ok; ++t) {
-        const Ring v = at, k = at.next();
-        if (t >= 2 && t < inner) {
+        // rounds in which both sides have a P.V and an S that is not their last
+        if (s == 0 && t >= 2 && t < cur.nt0 - 1) {
           // as below, with as little as can be between one side's products
           // and the other's
+          const Ring v = at, k = at.next();
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
+          for (int sd = 0; sd < 2; ++sd) {
             ok = __all_sync(0xffffffffu,
-                            ok && (s == 1 || (wait(C::FULL + v.slot, v.phase) &&
-                                              wait(C::FULL + k.slot, k.phase))) &&
-                                wait(C::P_READY + s, pn[s] & 1));
-            ++pn[s];
+                            ok && (sd == 1 || (wait(C::FULL + v.slot, v.phase) &&
+                                               wait(C::FULL + k.slot, k.phase))) &&
+                                wait(C::P_READY + sd, p_ph >> sd));
+            p_ph ^= 1u << sd;
             if (!ok) break;
             tc_fence_after();
             const uint64_t vb = v0 + v.slot * (C::SLOT >> 4), kb = k0 + k.slot * (C::SLOT >> 4);
-            const uint64_t qa = q0 + ((s * C::Q_BYTES) >> 4);
+            const uint64_t qa = q0 + ((sd * C::Q_BYTES) >> 4);
             if (elect_one()) {
 #pragma unroll
               for (int e = 0; e < kN / 16; ++e)
-                mma_16_ts(C::T_O + s * 128, C::T_S + s * 128 + 8 * e, vb + e * (2048 >> 4), kIdescO,
-                          1u);
-              if (s == 1) mma_commit(BAR(C::EMPTY + v.slot));
+                mma_16_ts(C::T_O + sd * 128, C::T_S + sd * 128 + 8 * e, vb + e * (2048 >> 4),
+                          kIdescO, 1u);
+              if (sd == 1) mma_commit(BAR(C::EMPTY + v.slot));
 #pragma unroll
               for (int e = 0; e < DK / 16; ++e) {
                 const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
-                mma_bf16(C::T_S + s * 128, qa + o, kb + o, kIdescS, e > 0 ? 1u : 0u);
+                mma_bf16(C::T_S + sd * 128, qa + o, kb + o, kIdescS, e > 0 ? 1u : 0u);
               }
-              mma_commit(BAR(C::S_FULL + s));
-              if (s == 1) mma_commit(BAR(C::EMPTY + k.slot));
+              mma_commit(BAR(C::S_FULL + sd));
+              if (sd == 1) mma_commit(BAR(C::EMPTY + k.slot));
             }
             __syncwarp();
           }
           at = k.next();
+          ++t;
           continue;
         }
-        if (t == cur.T) {
+        if (s == 0 && t == cur.T) {
           nx = next_seg();
+          if (!ok) break;
           primed = nx.T > 0 && !nx.twin;
         }
+        const int nt = s ? cur.nt1 : cur.nt0, nxt = s ? nx.nt1 : nx.nt0;
+        ov = at;
+        sk = t > 0 ? at.next() : at;
+        side_o = side_s = qb = s;
+        do_o = t > 0 && t <= nt;
+        o_first = t == 1;
+        o_last = t == nt;
+        do_s = t < cur.T ? t < nt : primed && nxt > 0;
+        s_first = t == 0 || t == cur.T;
+        s_last = t < cur.T ? t == nt - 1 : nxt == 1;
+        o_free = s_free = s == 1;
+      }
+      if (do_o) {
+        all_wait(C::FULL + ov.slot, ov.phase);
+        all_wait(C::P_READY + side_o, p_ph >> side_o);
+        p_ph ^= 1u << side_o;
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t b0 = v0 + ov.slot * (C::SLOT >> 4);
+        const uint32_t d = C::T_O + side_o * 128, a0 = C::T_S + side_o * 128;
+        if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (t <= cur.nt[s]) issue_o(s, v, t == 1, t == cur.nt[s]);
-          if (t < cur.T) {
-            if (t < cur.nt[s]) issue_s(s, k, false, t == cur.nt[s] - 1);
-          } else if (primed && nx.nt[s] > 0) {
-            issue_s(s, k, true, nx.nt[s] == 1);
+          for (int e = 0; e < kN / 16; ++e)
+            mma_16_ts(d, a0 + 8 * e, b0 + e * (2048 >> 4), kIdescO, (o_first && e == 0) ? 0u : 1u);
+          if (o_last) mma_commit(BAR(C::O_DONE + side_o));
+          if (o_free) mma_commit(BAR(C::EMPTY + ov.slot));
+        }
+        __syncwarp();
+      }
+      if (do_s) {
+        if (s_first) {
+          all_wait(C::Q_FULL + qb, q_ph >> qb);
+          q_ph ^= 1u << qb;
+        }
+        all_wait(C::FULL + sk.slot, sk.phase);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a0 = q0 + ((qb * C::Q_BYTES) >> 4);
+        const uint64_t b0 = k0 + sk.slot * (C::SLOT >> 4);
+        const uint32_t d = C::T_S + side_s * 128;
+        if (elect_one()) {
+#pragma unroll
+          for (int e = 0; e < DK / 16; ++e) {
+            const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
+            mma_bf16(d, a0 + o, b0 + o, kIdescS, e > 0 ? 1u : 0u);
+          }
+          mma_commit(BAR(C::S_FULL + side_s));
+          if (s_last) mma_commit(BAR(C::Q_EMPTY + qb));
+          if (s_free) mma_commit(BAR(C::EMPTY + sk.slot));
+        }
+        __syncwarp();
+      }
+      if (stream) {
+        if (do_o) {
+          vo = vo.next().next();
+          ++n_o;
+        }
+        if (do_s) {
+          const uint32_t f = (ts < 2 ? 1u : 0u) | (ts + 2 >= cur.T ? 2u : 0u);
+          flags = (flags & ~(3u << (2 * side_s))) | (f << (2 * side_s));
+          ks = ks.next().next();
+          ++n_s;
+          if (++ts == cur.T) have = false;
+        }
+      } else {
+        if (s == 1) {
+          at = t < cur.T || primed ? sk.next() : sk;
+          if (t == cur.T) {
+            cur = nx;
+            t = primed ? 1 : 0;
+            primed = false;
+          } else {
+            ++t;
           }
         }
-        give_back(v);
-        at = k;
-        if (t < cur.T || primed) {
-          give_back(k);
-          at = k.next();
-        }
+        s ^= 1;
       }
-      cur = nx;
     }
     // every product has to be finished before tensor memory is released
     if (elect_one()) {
@@ -695,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok0 = twin ? 0 : side * p.tq;
       const int my_tok = tok0 + tok;  // token of the unit
       const bool live = tok < p.tq && my_tok < seg.ntok;
+      const bool warp_live = (warp & 3) * 32 < (seg.ntok - tok0) * p.r;  // (some row is)
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0);
       if (seg.lt0 == 0 && !whole) {
         d_head = 1;
@@ -719,6 +713,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++sn;
         if (!ok) break;
         tc_fence_after();
+        if (!warp_live) {  // (nothing here is read)
+          if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
+          continue;
+        }
         float x[kN];
 #pragma unroll
         for (int c = 0; c < kN / 32; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
@@ -727,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
         }
-        const int base = (seg.lt0 + (twin ? 2 * t + side : t)) * kN;
+        const int base = (seg.lt0 + (twin ? 2 * t + (side ^ seg.ph) : t)) * kN;
         if constexpr (PART) {
           if (!side_vis.all(base, kN)) {
 #pragma unroll
@@ -866,8 +864,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // single tokens where this took 142.)
       T16* const dst = static_cast<T16*>(p.out) + out_row * DV;
       const float fo = last ? wo * inv : wo, ft = last ? wt * inv : wt;
-      for (int c = c0; c < c1; ++c) {
-        if (nt == 0 && other == 0) break;  // (a side without tokens)
+      // (nothing where no row is live or the side has no tokens)
+      const int c_end = warp_live && (nt > 0 || other > 0) ? c1 : c0;
+#pragma unroll 1
+      for (int c = c0; c < c_end; ++c) {
+        __syncwarp();  // (the loads of tensor memory are the whole warp's)
         float o[32];
         if (nt > 0) {
           tmem_ld32(tO + 32 * c, o);
@@ -885,19 +886,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], ft, o[e]);
         }
-        if (!live) continue;
-        if (last) {
-          uint32_t u[16];
+        if (live) {
+          if (last) {
+            uint32_t u[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = Half16<T16>::pack2(o[2 * e], o[2 * e + 1]);
-          store_sectors<2>(dst + 32 * c, u, p.out_sectors);
-        } else {
-          uint32_t u[32];
+            for (int e = 0; e < 16; ++e) u[e] = Half16<T16>::pack2(o[2 * e], o[2 * e + 1]);
+            store_sectors<2>(dst + 32 * c, u, p.out_sectors);
+          } else {
+            uint32_t u[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e]);
-          store_sectors<4>(pdst + 32 * c, u, true);
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e]);
+            store_sectors<4>(pdst + 32 * c, u, true);
+          }
         }
       }
+      __syncwarp();
       tc_fence_before();
       if (twin) {  // both O and ml_sm are free again
         __syncwarp();
@@ -1145,7 +1148,7 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   p.row_ml = reinterpret_cast<float*>(ws + pl.row_ml_at);
   p.row_o = reinterpret_cast<float*>(ws + pl.row_o_at);
 
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mq1, mk, mv;
   const uint64_t rows = PAGED ? static_cast<uint64_t>(x.num_blocks) * x.g * x.bsz
                               : static_cast<uint64_t>(x.b) * x.g * x.cap;
   constexpr int kBox = Walk::kPart ? kGrain : kN;
@@ -1153,10 +1156,12 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   const uint64_t qd[3] = {DK, static_cast<uint64_t>(x.h), static_cast<uint64_t>(x.total)};
   const uint64_t qs[2] = {DK * 2, static_cast<uint64_t>(x.h) * DK * 2};
   const uint32_t qb[3] = {64u, static_cast<uint32_t>(p.r), static_cast<uint32_t>(p.tq)};
+  const uint32_t qb1[3] = {64u, static_cast<uint32_t>(p.r), 1u};
   const uint64_t kd[2] = {DK, rows}, ks[1] = {DK * 2};
   const uint64_t vd[2] = {DV, rows}, vs[1] = {DV * 2};
   const uint32_t kb[2] = {64u, box_rows};
   if (!encode_bf16_map(&mq, x.q, 3, qd, qs, qb, kBf16) ||
+      !encode_bf16_map(&mq1, x.q, 3, qd, qs, qb1, kBf16) ||
       !encode_bf16_map(&mk, x.k, 2, kd, ks, kb, kBf16) ||
       !encode_bf16_map(&mv, x.v, 2, vd, vs, kb, kBf16))
     return cudaErrorInvalidValue;
@@ -1186,7 +1191,7 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p)) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mq1, mk, mv, p)) return e;
   return Walk::template join<T16, DV>(cfg, p, num_sms);
 }
 

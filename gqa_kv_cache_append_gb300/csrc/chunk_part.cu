@@ -32,9 +32,10 @@ struct PartSeg {
   int head;        // positions of the span's head
   int shift, sb, z, end;  // the span (end: of its last position seen by the sequence)
   bool of_head;    // a unit over the head alone, for rows of all sequences
+  int ph, qb;      // as in chunk_attn.cu
   __device__ bool twin(int tq) const { return ntok <= tq; }
   __device__ int side_tiles(int side, int tq) const {
-    if (twin(tq)) return (lt1 - lt0 + 1 - side) >> 1;
+    if (twin(tq)) return (lt1 - lt0 + 1 - (side ^ ph)) >> 1;
     const int nt = min(ntok - side * tq, tq);
     const int ext = of_head ? head : pos0 + side * tq + nt - shift;
     return max(0, min(lt1, (ext + kN - 1) / kN) - lt0);
