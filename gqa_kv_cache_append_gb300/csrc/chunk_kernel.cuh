@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
     // ============================ TMA producer ============================
     Seg seg;
-    const uint64_t pol = policy_evict_last();
+    const uint64_t pol_keep = policy_evict_last(), pol_once = policy_evict_first();
     const int oob_row = PAGED  ? p.num_blocks * p.g * p.bsz
                         : PART ? static_cast<int>(static_cast<long long>(p.b) * p.g * p.cap)
                                : 0;
@@ -327,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ++kn;
       if (!more) break;
+      // (twins of single tokens read rows that nobody else reads)
+      const uint64_t pol = PART && twin ? pol_once : pol_keep;
       // query rows of a side (twins: of both)
       auto load_q = [&](int side) {
         const int qb = twin ? seg.qb : side;
@@ -478,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring at;               // V of tile t - 1 (t = 0: K of tile 0)
     int t = 0, s = 0;
     bool primed = false;   // the next unit's first S are out
+    bool ahead = false;    // the next unit is known
     // Twins: tiles by turns, without a break between units, S two tiles ahead of P.V.
     bool stream = false, have = false, ended = false;
     Ring ks, vo;           // K of the next S, V of the next P.V
@@ -567,11 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++t;
           continue;
         }
-        if (s == 0 && t == cur.T) {
+        if (s == 0 && (t == cur.T - 1 || (t == cur.T && !ahead))) {
+          // (a round early where there is one: its copies are under way by then)
           nx = next_seg();
           if (!ok) break;
-          primed = nx.T > 0 && !nx.twin;
+          ahead = true;
         }
+        if (t == cur.T) primed = nx.T > 0 && !nx.twin;
         const int nt = s ? cur.nt1 : cur.nt0, nxt = s ? nx.nt1 : nx.nt0;
         ov = at;
         sk = t > 0 ? at.next() : at;
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t == cur.T) {
             cur = nx;
             t = primed ? 1 : 0;
-            primed = false;
+            primed = ahead = false;
           } else {
             ++t;
           }
@@ -760,8 +765,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[k] = e + 4 < kN ? max3(mx[k], x[e + k], x[e + 4 + k]) : fmaxf(mx[k], x[e + k]);
         const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         // S_FULL also covers the products issued before it: O is complete
-        // up to the last tile
-        if (__any_sync(0xffffffffu, (mn - m) * sl > PRange<T16>::kRaise)) {
+        // up to the last tile.  (Lanes without a row hold anything: they have no
+        // say in when the others round.)
+        if (__any_sync(0xffffffffu, live && (mn - m) * sl > PRange<T16>::kRaise)) {
           const float ref = mn == -INFINITY ? 0.f : mn;
           const float alpha = ex2((m - ref) * sl);
           m = mn;

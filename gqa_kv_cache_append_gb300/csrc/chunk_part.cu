@@ -62,7 +62,8 @@ struct PartSeg {
 // sum and the search, the two warps that look for a run's ends in the same code,
 // divisions by multiplication.  (With five scans and 64-bit divisions inlined a
 // call took 5 us longer with one sequence, 15 with 64.)
-constexpr unsigned kPartUnitCost = 320;
+constexpr unsigned kPartUnitCost = 400;
+constexpr unsigned kPartNear = 2;  // tiles
 
 struct PartWalk {
   using Seg = PartSeg;
@@ -212,7 +213,7 @@ struct PartWalk {
             // (g is small: steps instead of a 64-bit division)
             r.j = 0;
 #pragma unroll 1
-            for (int step = 1 << 30; step > 0; step >>= 1)
+            for (int step = 1 << (31 - __clz(p.g)); step > 0; step >>= 1)
               if (r.j + step < p.g && (r.j + step) * fs <= rem) r.j += step;
             rem -= r.j * fs;
             // the last unit q with prefix(q) <= rem
@@ -240,7 +241,7 @@ struct PartWalk {
         if (W == 0 || c > nc) return false;
         if (c == nc) return true;
         const U64 run = div_pos(W, nc);
-        near = static_cast<unsigned>(run / (32 * kN));
+        near = min(static_cast<unsigned>(run / (32 * kN)), kPartNear);
         const int left = static_cast<int>(W - run * nc);  // the first `left` runs are one longer
         x = run * c + min(c, left);
       }
