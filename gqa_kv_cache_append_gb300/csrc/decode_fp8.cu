@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
     const int oob_row = p.num_blocks * p.g * p.bsz;
     const int box = PART ? p.gran : min(p.bsz, kTile);
     const int sub = kTile / box;  // boxes a tile
+    const int box_sh = __ffs(box) - 1;
     const int sh = __ffs(p.bsz) - 1, mask = p.bsz - 1;  // (a power of two)
     uint32_t n = 0;
     bool ok = true;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         // 42 us with 32-row blocks.
         int pos = lt * kTile + lane * 8, blk;
         if constexpr (PART) {
-          const int from = lane * 8 / box;
+          const int from = (lane * 8) >> box_sh;
           const int p0 = __shfl_sync(0xffffffffu, pm, from);
           blk = __shfl_sync(0xffffffffu, ent, from);
           pos = p0 < 0 ? seg.L : p0 + (lane * 8 & (box - 1));
@@ -574,8 +575,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         float ks[2], vs[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          bool in = row + hf * kHalf < valid;
-          if constexpr (PART) in = all_used || used(v0 + row + hf * kHalf);
+          const bool in = PART || row + hf * kHalf < valid;
           ks[hf] = in ? sc[hf * kHalf] : 0.f;
           vs[hf] = in ? sc[kTile + hf * kHalf] : 0.f;
         }
@@ -596,14 +596,28 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           const int p0 = hf * kHalf + 4 * lane;
           const float4 v = *reinterpret_cast<const float4*>(
               reinterpret_cast<const float*>(sm + C::OFF_SC) + (st * 2 + 1) * kTile + p0);
-          auto in = [&](int k) {
-            if constexpr (PART) return all_used || used(v0 + k);
-            return k < valid;
-          };
-          vm = fmaxf(vm, in(p0) ? fabsf(v.x) : 0.f);
-          vm = fmaxf(vm, in(p0 + 1) ? fabsf(v.y) : 0.f);
-          vm = fmaxf(vm, in(p0 + 2) ? fabsf(v.z) : 0.f);
-          vm = fmaxf(vm, in(p0 + 3) ? fabsf(v.w) : 0.f);
+          if constexpr (PART) {
+            vm = fmaxf(vm, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+          } else {
+            vm = fmaxf(vm, p0 < valid ? fabsf(v.x) : 0.f);
+            vm = fmaxf(vm, p0 + 1 < valid ? fabsf(v.y) : 0.f);
+            vm = fmaxf(vm, p0 + 2 < valid ? fabsf(v.z) : 0.f);
+            vm = fmaxf(vm, p0 + 3 < valid ? fabsf(v.w) : 0.f);
+          }
+        }
+        if constexpr (PART) {
+          if (!all_used) {  // (uniform) scales of rows that no token sees may be anything
+            vm = 0.f;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              if (!used(v0 + row + hf * kHalf)) ks[hf] = vs[hf] = 0.f;
+#pragma unroll 1
+              for (int k = hf * kHalf + 4 * lane; k < hf * kHalf + 4 * lane + 4; ++k)
+                if (used(v0 + k))
+                  vm = fmaxf(vm, fabsf(reinterpret_cast<const float*>(
+                                 sm + C::OFF_SC)[(st * 2 + 1) * kTile + k]));
+            }
+          }
         }
         vm = warp_max(vm);
         // (scales so small that the factor would overflow: scaled up first)
