@@ -13,17 +13,21 @@ struct ChunkSeg {
   int L, end;      // (the same: no row behind it is used)
   int lt0, lt1;    // tiles of the unit taken here
   int ti;          // tiles of the unit
-  int ph, qb;      // twins: the side of the first tile, the query rows' buffer
   static constexpr int head = 0, z = 0;
   // A unit whose rows fit side A alone runs as twins: both sides hold the same
   // rows and take the tiles by turns, and their results are joined at the end.
   __device__ bool twin(int tq) const { return ntok <= tq; }
-  // tiles that each side works on of [lt0, lt1)
+  // tiles that a side of two works on of [lt0, lt1)
   __device__ int side_tiles(int side, int tq) const {
-    if (twin(tq)) return (lt1 - lt0 + 1 - (side ^ ph)) >> 1;
     const int nt = min(ntok - side * tq, tq);
     const int ext = pos0 + side * tq + nt;
     return max(0, min(lt1, (ext + kN - 1) / kN) - lt0);
+  }
+  // what the tokens from tok0 on see
+  __device__ void sees(const ChunkParams&, int tok0, SegPlan::Side& v, int& lo_min) const {
+    v.lo = lo_min = 0;
+    v.hi = v.all_hi = pos0 + tok0 + 1;
+    v.all_head = v.all_lo = 0;
   }
 };
 
@@ -47,7 +51,6 @@ constexpr int kUnitCost = 320;
 
 struct ChunkWalk {
   using Seg = ChunkSeg;
-  struct Visible {};
   static constexpr bool kPart = false;
   __device__ static void report(const ChunkParams& p) {
     report_bad_packed(p.cu, p.lens, p.b, p.total, p.cap, p.status);

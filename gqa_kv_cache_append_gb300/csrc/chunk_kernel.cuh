@@ -65,6 +65,7 @@
 
 #include "../../include/gqa.h"
 #include "gqa_internal.h"
+#include "part_device.cuh"
 #include "serve_device.cuh"
 
 namespace gqa {
@@ -78,7 +79,7 @@ constexpr int kThreads = 384;     // two softmax warpgroups, one of single warps
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kDescInts = 8;      // per CTA, see below
 constexpr int kSegs = 4;          // segments announced ahead
-constexpr int kSegBytes = 80;
+constexpr int kSegBytes = 112;
 constexpr int kEdges = 8;         // V tiles to be zeroed in part: more than a ring holds of V
 constexpr int kGrain = 64;        // positions of a box where a part of the cache is read, at most
 // A row's reference maximum is raised when the new one is this much larger, and
@@ -101,7 +102,8 @@ struct ChunkCfg {
                        S_FULL = Q_EMPTY + 2, P_READY = S_FULL + 2, O_DONE = P_READY + 2,
                        SEG_FULL = O_DONE + 2, SEG_EMPTY = SEG_FULL + kSegs,
                        V_EDGE = SEG_EMPTY + kSegs,
-                       TWIN = V_EDGE + kEdges, RUN_END = TWIN + 2, DRAIN = RUN_END + 1, NBAR = DRAIN + 1;
+                       TWIN = V_EDGE + kEdges, RUN_END = TWIN + 2, DRAIN = RUN_END + 1,
+                       NBAR = DRAIN + 1;
   static constexpr int OFF_SEG = (OFF_BAR + 8 * NBAR + 15) / 16 * 16;
   static constexpr int OFF_ML = OFF_SEG + kSegs * kSegBytes;  // float2 [2][kM]: twins' maxima, sums
   static constexpr int OFF_MISC = OFF_ML + 2 * kM * 8;  // TMEM address, abort flag; the run's end
@@ -151,6 +153,31 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {  // a >
                                 static_cast<unsigned long long>(b));
 }
 
+// What the products and the softmax need of a segment, worked out by the TMA warp
+// ahead of time: what they would compute between two units stands on their
+// critical path, and as code that runs once a unit it is fetched each time (1.5
+// us from one unit to the next).
+struct SegPlan {
+  int T;         // tiles (0: no more)
+  int twin, qb;  // a unit of twins; their query rows' buffer
+  int step;      // positions from one of a side's tiles to its next
+  int j;         // KV head
+  int last;      // 1: the results are final
+  int part;      // else the first partial row of the CTA's two units
+  int by_row;    // 0: by CTA, 1, 2: by row, over the head, over the sequence's own
+  int head, lo_min;
+  struct Side {
+    int nt;      // tiles
+    int first;   // position of the first one
+    int tokens;  // tokens with rows
+    int row0;    // packed row of the first
+    // (PART) token k sees [0, min(head, hi)) and [max(lo + k, lo_min), hi + k) of
+    // the span; every token [0, all_head) and [all_lo, all_hi)
+    int lo, hi, all_head, all_lo, all_hi;
+  } side[2];
+};
+static_assert(sizeof(SegPlan) <= kSegBytes, "segment ring");
+
 // desc of CTA c: a unit cut at its run's end (head) or start (tail / middle)
 enum { D_HEAD = 0, D_TOK0 = 1, D_NTOK = 2, D_J = 3, D_END = 4 };
 
@@ -162,9 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
   using C = ChunkCfg<DK, DV>;
   using Seg = typename Walk::Seg;
+  using Plan = SegPlan;
   constexpr bool PART = Walk::kPart;
   constexpr bool kBf16 = Half16<T16>::kBf16;
-  static_assert(sizeof(Seg) <= kSegBytes, "segment ring");
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t s_base = smem_u32(sm);
   if (s_base & 1023u) {  // never seen; the swizzled layouts need it
@@ -206,463 +233,518 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait_then_release();
 
-  auto seg_at = [&](uint32_t k) -> Seg* {
-    return reinterpret_cast<Seg*>(sm + C::OFF_SEG + (k % kSegs) * kSegBytes);
+  auto seg_at = [&](uint32_t k) -> Plan* {
+    return reinterpret_cast<Plan*>(sm + C::OFF_SEG + (k % kSegs) * kSegBytes);
   };
   auto wait = [&](int k, uint32_t phase) -> bool {
     return mbar_wait(BAR(k), phase & 1u, abort_flag, p.status, p.budget);
   };
 
   ChunkPos* const run_end = reinterpret_cast<ChunkPos*>(sm + C::OFF_MISC + 16);
-  if (warp == 9) {
+  if (warp >= 8) {
+    // (a warpgroup's four warps at the same instruction, as it has to be)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (blockIdx.x == 0) Walk::report(p);
-  } else if (warp >= 10) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    // the run's start, and in warp 11 its end, in the same instructions
-    Walk w(p);
-    ChunkPos from;
-    const bool any = w.start(blockIdx.x + (warp - 10), gridDim.x, from);
-    if (warp == 11) {
-      if (lane == 0) {
-        *run_end = from;
-        mbar_arrive(BAR(C::RUN_END));
-      }
-      // V tiles some of whose rows nobody sees: rows [x, y) and from z on are
-      // zeroed before the products may read them.  (By the TMA warp it cost a
-      // microsecond of its copies for each.)
-      for (uint32_t e = 0;; ++e) {
-        if (!__all_sync(0xffffffffu, wait(C::V_EDGE + e % kEdges, e / kEdges))) break;
-        const int4 v = *reinterpret_cast<const int4*>(sm + C::OFF_EDGE + 16 * (e % kEdges));
-        if (v.w < 0) break;
-        const uint32_t dst = s_base + C::OFF_RING + v.w * C::SLOT;
-        for (int idx = lane; idx < kN * 8; idx += 32) {
-          const int r8 = idx >> 3;
-          if ((r8 < v.x || r8 >= v.y) && r8 < v.z) continue;
-#pragma unroll
-          for (int c = 0; c < DV / 64; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             dst + c * (kN * 128) + idx * 16),
-                         "r"(0u)
-                         : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::FULL + v.w));
-      }
-      __syncwarp();
-    } else {
-    // ============================ TMA producer ============================
-    Seg seg;
-    const uint64_t pol_keep = policy_evict_last(), pol_once = policy_evict_first();
-    const int oob_row = PAGED  ? p.num_blocks * p.g * p.bsz
-                        : PART ? static_cast<int>(static_cast<long long>(p.b) * p.g * p.cap)
-                               : 0;
-    const int box = PART ? (PAGED ? min(p.bsz, kGrain) : kGrain) : PAGED ? min(p.bsz, kN) : kN;
-    const int sub = kN / box;  // boxes a tile and 64-column half
-    const int sh = PAGED ? __ffs(p.bsz) - 1 : 0, mask = p.bsz - 1;  // (a power of two)
-    uint32_t slot_n = 0, qn[2] = {0, 0}, edge_n = 0;
-    uint32_t kn = 0;  // segments announced
-    uint32_t twins = 0, twin_q = 0;  // tiles of twins so far; the next twins' query rows
-    bool ok = __all_sync(0xffffffffu, wait(C::RUN_END, 0));
-    w.begin(any ? from : ChunkPos{p.b, 0, 0, 0}, ok ? *run_end : ChunkPos{p.b, 0, 0, 0});
-    while (true) {
-      const bool more = ok && w.next(seg);
-      if (!more) seg.lt0 = seg.lt1 = 0;
-      const int T = seg.lt1 - seg.lt0;
-      const bool twin = seg.twin(p.tq);
-      if (more) {
-        seg.ph = twins & 1;
-        if (twin) {
-          seg.qb = twin_q;
-          twins += T;
-          twin_q ^= 1;
-        } else {
-          twin_q = 0;
-        }
-      }
-      // the sequence's table entries, 64 at a time ahead of their use: no load
-      // stands before a tile's copies
-      PageCursor pc;
-      if constexpr (PAGED && !PART)
-        if (more)
-          pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
-                   static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
-                   (seg.lt0 * kN) >> sh);
-      // PART: the position of this lane's box of tile lt (-1: none), and the
-      // table entry that holds it.  (One load a box, a tile ahead of its use:
-      // a tile's boxes may lie in two places.)
-      auto box_at = [&](int lt) -> int {
-        const int v = lt * kN + lane * box;
-        if constexpr (PART) {
-          const bool in_head = v < seg.sb;
-          const int pos = in_head ? v : v + seg.shift;
-          return lane < sub && pos < (in_head ? seg.head : seg.L) ? pos : -1;
-        }
-        return lane < sub && v < seg.L ? v : -1;
-      };
-      auto source = [&](int lt) -> int {
-        if constexpr (PART)
-          if (p.head_seq >= 0 && lt * kN + lane * box < seg.sb) return p.head_seq;
-        return seg.i;
-      };
-      auto entry = [&](int lt) -> int {
-        if constexpr (PAGED && PART) {
-          const int pos = box_at(lt);
-          if (pos >= 0)
-            return __ldg(p.table + static_cast<size_t>(source(lt)) * p.max_blocks + (pos >> sh));
-        }
-        return 0;
-      };
-      int ent = more ? entry(seg.lt0) : 0, row = 0;
-      auto hold = [&](int k, uint32_t phase) {
-        ok = __all_sync(0xffffffffu, ok && wait(k, phase));
-        return ok;
-      };
-      if (!hold(C::SEG_EMPTY + kn % kSegs, (kn / kSegs) ^ 1)) break;
-      if (lane == 0) {
-        *seg_at(kn) = seg;
-        mbar_arrive(BAR(C::SEG_FULL + kn % kSegs));
-      }
-      __syncwarp();
-      ++kn;
-      if (!more) break;
-      // (twins of single tokens read rows that nobody else reads)
-      const uint64_t pol = PART && twin ? pol_once : pol_keep;
-      // query rows of a side (twins: of both)
-      auto load_q = [&](int side) {
-        const int qb = twin ? seg.qb : side;
-        if (seg.side_tiles(side, p.tq) == 0 && !twin) return;
-        if (!hold(C::Q_EMPTY + qb, (qb ? qn[1] : qn[0]) ^ 1)) return;
-        // (a twin's rows from one token: one box of its heads, the rest of the
-        // tile holds anything)
-        const bool one = twin && seg.ntok == 1;
+    if (warp == 9) {
+      if (blockIdx.x == 0) Walk::report(p);
+    } else if (warp >= 10) {
+      // the run's start, and in warp 11 its end, in the same instructions
+      Walk w(p);
+      ChunkPos from;
+      const bool any = w.start(blockIdx.x + (warp - 10), gridDim.x, from);
+      if (warp == 11) {
         if (lane == 0) {
-          const uint32_t dst = s_base + qb * C::Q_BYTES;
-          mbar_arrive_expect_tx(BAR(C::Q_FULL + qb), (one ? 1 : p.tq) * p.r * DK * 2);
-#pragma unroll 1
-          for (int c = 0; c < DK / 64; ++c)
-            tma_load_3d(dst + c * (kM * 128), one ? &tm_q1 : &tm_q, BAR(C::Q_FULL + qb), 64 * c,
-                        seg.j * p.r, seg.t0 + side * p.tq, pol);
+          *run_end = from;
+          mbar_arrive(BAR(C::RUN_END));
         }
-        if (qb)
-          ++qn[1];
-        else
-          ++qn[0];
-      };
-      load_q(0);
-      // K and V of the tiles by turns: the order the products need them
-      for (int lt = seg.lt0; lt < seg.lt1 && ok; ++lt) {
-        // the pool or cache row of this lane's box, for the tile's K and V
-        const int pos = box_at(lt);
-        row = oob_row;
-        if constexpr (PAGED) {
-          if constexpr (!PART) ent = pc.get_lanes((lt * kN) >> sh);
-          if (pos >= 0) {
-            if (ent >= 0 && ent < p.num_blocks)
-              row = (ent * p.g + seg.j) * p.bsz + (pos & mask);
-            else
-              atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+        __syncwarp();
+        // V tiles some of whose rows nobody sees: rows [x, y) and from z on are
+        // zeroed before the products may read them.  (By the TMA warp it cost a
+        // microsecond of its copies for each.)
+        for (uint32_t e = 0;; ++e) {
+          if (!__all_sync(0xffffffffu, wait(C::V_EDGE + e % kEdges, e / kEdges))) break;
+          const int4 v = *reinterpret_cast<const int4*>(sm + C::OFF_EDGE + 16 * (e % kEdges));
+          if (v.w < 0) break;
+          const uint32_t dst = s_base + C::OFF_RING + v.w * C::SLOT;
+          for (int idx = lane; idx < kN * 8; idx += 32) {
+            const int r8 = idx >> 3;
+            if ((r8 < v.x || r8 >= v.y) && r8 < v.z) continue;
+#pragma unroll
+            for (int c = 0; c < DV / 64; ++c)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               dst + c * (kN * 128) + idx * 16),
+                           "r"(0u)
+                           : "memory");
           }
-          if (PART && lt + 1 < seg.lt1) ent = entry(lt + 1);
-        } else if (pos >= 0) {
-          row = static_cast<int>((static_cast<long long>(source(lt)) * p.g + seg.j) * p.cap) + pos;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(C::FULL + v.w));
+          __syncwarp();
         }
-        int slot = slot_n % C::NS;
-        if (!hold(C::EMPTY + slot, (slot_n / C::NS) ^ 1)) break;
-        uint32_t to = BAR(C::FULL + slot), dst = s_base + C::OFF_RING + slot * C::SLOT;
-        if (lane == 0) mbar_arrive_expect_tx(to, DK / 64 * kN * 128);
         __syncwarp();
-        if (lane < sub) {
-#pragma unroll
-          for (int c = 0; c < DK / 64; ++c)
-            tma_load_2d(dst + c * (kN * 128) + lane * box * 128, &tm_k, to, 64 * c, row, pol);
-        }
-        ++slot_n;
-        if (lt == seg.lt0 && !twin) load_q(1);
-        slot = slot_n % C::NS;
-        if (!hold(C::EMPTY + slot, (slot_n / C::NS) ^ 1)) break;
-        to = BAR(C::FULL + slot), dst = s_base + C::OFF_RING + slot * C::SLOT;
-        const int v0 = lt * kN;
-        if (v0 + kN > seg.end || (seg.head < v0 + kN && seg.z > v0 && seg.z > seg.head)) {
-          if (lane == 0)
-            *reinterpret_cast<int4*>(sm + C::OFF_EDGE + 16 * (edge_n % kEdges)) =
-                make_int4(max(seg.head - v0, 0), seg.z - v0, max(seg.end - v0, 0), slot);
-          to = BAR(C::V_EDGE + edge_n % kEdges);
-          ++edge_n;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(to, DV / 64 * kN * 128);
-        __syncwarp();
-        if (lane < sub) {
-#pragma unroll
-          for (int c = 0; c < DV / 64; ++c)
-            tma_load_2d(dst + c * (kN * 128) + lane * box * 128, &tm_v, to, 64 * c, row, pol);
-        }
-        ++slot_n;
-      }
-      if (!ok) break;
-    }
-    if (ok && lane == 0) {  // no more edges
-      *reinterpret_cast<int4*>(sm + C::OFF_EDGE + 16 * (edge_n % kEdges)) = make_int4(0, 0, 0, -1);
-      mbar_arrive(BAR(C::V_EDGE + edge_n % kEdges));
-    }
-    __syncwarp();
-    if (!ok) {
-      // copies in flight must land before the CTA exits (bounded)
-      const long long t0 = clock64();
-      for (int s = 0; s < C::NS; ++s) {
-        if (slot_n <= static_cast<uint32_t>(s)) continue;
-        const uint32_t last = (slot_n - 1 - s) / C::NS;  // fills of slot s, less one
-        while (!mbar_try_wait(BAR(C::FULL + s), last & 1) && clock64() - t0 < p.budget) {
-        }
-      }
-      for (int s = 0; s < 2; ++s)
-        while (qn[s] > 0 && !mbar_try_wait(BAR(C::Q_FULL + s), (qn[s] - 1) & 1) &&
-               clock64() - t0 < p.budget) {
-        }
-    }
-    __syncwarp();
-    }
-  } else if (warp == 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    // ============================ MMA issuer ==============================
-    // The sides by turns: P.V of the side's last tile, then S of its next
-    // (of the next unit's first at a unit's end).  One warp issues both sides'
-    // products, so each side's run back to back; with an issuer per side they
-    // interleave and both sides wait longer.  The whole warp walks through
-    // this code with warp-uniform values and one elected lane issues: from a
-    // single lane's branch the operands take a detour into the uniform
-    // registers that costs as long as a product runs.
-    constexpr uint32_t kIdescS = idesc_bf16(kM, kN, 0, 0, kBf16);   // both K-major
-    constexpr uint32_t kIdescO = idesc_bf16(kM, DV, 0, 1, kBf16);   // V: MN-major
-    const uint64_t q0 = smem_desc(s_base, 16, 1024, SWZ_128B);
-    const uint64_t k0 = smem_desc(s_base + C::OFF_RING, 16, 1024, SWZ_128B);
-    const uint64_t v0 = smem_desc(s_base + C::OFF_RING, kN * 128, 1024, SWZ_128B);
-    struct Ring {  // a ring position: slot and phase
-      uint32_t slot = 0, phase = 0;
-      __device__ Ring next() const {
-        Ring r = *this;
-        if (++r.slot == C::NS) {
-          r.slot = 0;
-          r.phase ^= 1;
-        }
-        return r;
-      }
-    };
-    bool ok = true;
-    auto all_wait = [&](int k, uint32_t phase) {
-      ok = __all_sync(0xffffffffu, ok && wait(k, phase));
-    };
-    uint32_t kn = 0;                // segments read
-    uint32_t q_ph = 0, p_ph = 0;    // a bit for each query buffer, each side
-    // the next segment: its tiles (0: no more), and the sides'
-    struct Todo {
-      int T, nt0, nt1, qb;
-      bool twin;
-    };
-    auto next_seg = [&]() -> Todo {
-      Todo r = {0, 0, 0, 0, false};
-      all_wait(C::SEG_FULL + kn % kSegs, kn / kSegs);
-      if (!ok) return r;
-      const Seg& seg = *seg_at(kn);
-      r.T = __shfl_sync(0xffffffffu, seg.lt1 - seg.lt0, 0);
-      r.twin = __shfl_sync(0xffffffffu, seg.twin(p.tq) ? 1 : 0, 0) != 0;
-      r.qb = __shfl_sync(0xffffffffu, seg.qb, 0);
-      r.nt0 = __shfl_sync(0xffffffffu, seg.side_tiles(0, p.tq), 0);
-      r.nt1 = r.T;  // (the later tokens: they see what the unit sees)
-      __syncwarp();
-      if (elect_one()) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
-      ++kn;
-      return r;
-    };
-    // Two-sided units: in round t side A's P.V of tile t - 1 and its S of tile t,
-    // then side B's; at a unit's end the S of the next unit's first tile.
-    Ring at;               // V of tile t - 1 (t = 0: K of tile 0)
-    int t = 0, s = 0;
-    bool primed = false;   // the next unit's first S are out
-    bool ahead = false;    // the next unit is known
-    // Twins: tiles by turns, without a break between units, S two tiles ahead of P.V.
-    bool stream = false, have = false, ended = false;
-    Ring ks, vo;           // K of the next S, V of the next P.V
-    uint32_t n_s = 0, n_o = 0, flags = 0;  // tiles so far; first, last of a side (two bits each)
-    int ts = 0;
-    Todo cur = next_seg(), nx = cur;
-    // One loop for everything but the steady rounds of two-sided units, with one
-    // place for either product: what runs once a unit is fetched each time.
-    while (ok) {
-      bool do_o = false, do_s = false, o_first = false, o_last = false, s_first = false,
-           s_last = false, o_free = false, s_free = false;
-      int side_o = 0, side_s = 0, qb = 0;
-      Ring ov, sk;
-      if (stream) {
-        // S of tiles 0 and 1, then P.V of a tile and S of the one after next
-        if (!have && !ended) {
-          nx = next_seg();
-          if (!ok) break;
-          have = nx.T > 0 && nx.twin;
-          ended = !have;
-          if (have) cur = nx;
-          ts = 0;
-        }
-        if (ended && n_o == n_s) {
-          stream = false;
-          cur = nx;
-          at = ks;
-          primed = false;
-          t = s = 0;
-          continue;
-        }
-        sk = ks;
-        ov = vo;
-        qb = cur.qb;
-        side_s = n_s & 1;
-        side_o = n_o & 1;
-        do_o = n_s - n_o == 2 || !have;
-        do_s = have;
-        s_first = ts == 0;
-        s_last = ts == cur.T - 1;
-        o_first = (flags >> (2 * side_o)) & 1u;  // (of the tile whose S went out before)
-        o_last = (flags >> (2 * side_o + 1)) & 1u;
-        o_free = s_free = true;
       } else {
-        if (cur.T == 0) break;
-        if (cur.twin) {
-          stream = have = true;
-          ended = false;
-          ks = at;
-          vo = at.next();
-          ts = 0;
-          continue;
-        }
-        // rounds in which both sides have a P.V and an S that is not their last
-        if (s == 0 && t >= 2 && t < cur.nt0 - 1) {
-          // as below, with as little as can be between one side's products
-          // and the other's
-          const Ring v = at, k = at.next();
-#pragma unroll
-          for (int sd = 0; sd < 2; ++sd) {
-            ok = __all_sync(0xffffffffu,
-                            ok && (sd == 1 || (wait(C::FULL + v.slot, v.phase) &&
-                                               wait(C::FULL + k.slot, k.phase))) &&
-                                wait(C::P_READY + sd, p_ph >> sd));
-            p_ph ^= 1u << sd;
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vb = v0 + v.slot * (C::SLOT >> 4), kb = k0 + k.slot * (C::SLOT >> 4);
-            const uint64_t qa = q0 + ((sd * C::Q_BYTES) >> 4);
-            if (elect_one()) {
-#pragma unroll
-              for (int e = 0; e < kN / 16; ++e)
-                mma_16_ts(C::T_O + sd * 128, C::T_S + sd * 128 + 8 * e, vb + e * (2048 >> 4),
-                          kIdescO, 1u);
-              if (sd == 1) mma_commit(BAR(C::EMPTY + v.slot));
-#pragma unroll
-              for (int e = 0; e < DK / 16; ++e) {
-                const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
-                mma_bf16(C::T_S + sd * 128, qa + o, kb + o, kIdescS, e > 0 ? 1u : 0u);
+        // ============================ TMA producer ============================
+        Seg seg;
+        const uint64_t pol_keep = policy_evict_last(), pol_once = policy_evict_first();
+        const int oob_row = PAGED  ? p.num_blocks * p.g * p.bsz
+                            : PART ? static_cast<int>(static_cast<long long>(p.b) * p.g * p.cap)
+                                   : 0;
+        const int box = PART ? (PAGED ? min(p.bsz, kGrain) : kGrain) : PAGED ? min(p.bsz, kN) : kN;
+        const int sub = kN / box;  // boxes a tile and 64-column half
+        const int sh = PAGED ? __ffs(p.bsz) - 1 : 0, mask = p.bsz - 1;  // (a power of two)
+        uint32_t slot_n = 0, qn[2] = {0, 0}, edge_n = 0;
+        uint32_t kn = 0;  // segments announced
+        uint32_t twins = 0, twin_q = 0;  // tiles of twins so far; the next twins' query rows
+        int d_head = 0, d_tok0 = 0, d_ntok = 0, d_j = 0, d_end = 0;  // (desc)
+        bool ok = __all_sync(0xffffffffu, wait(C::RUN_END, 0));
+        w.begin(any ? from : ChunkPos{p.b, 0, 0, 0}, ok ? *run_end : ChunkPos{p.b, 0, 0, 0});
+        while (true) {
+          const bool more = ok && w.next(seg);
+          if (!more) seg.lt0 = seg.lt1 = 0;
+          const int T = seg.lt1 - seg.lt0;
+          const bool twin = seg.twin(p.tq);
+          // the sequence's table entries, 64 at a time ahead of their use: no load
+          // stands before a tile's copies
+          PageCursor pc;
+          if constexpr (PAGED && !PART)
+            if (more)
+              pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
+                       static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
+                       (seg.lt0 * kN) >> sh);
+          // PART: the position of this lane's box of tile lt (-1: none), and the
+          // table entry that holds it.  (One load a box, a tile ahead of its use:
+          // a tile's boxes may lie in two places.)
+          auto box_at = [&](int lt) -> int {
+            const int v = lt * kN + lane * box;
+            if constexpr (PART) {
+              const bool in_head = v < seg.sb;
+              const int pos = in_head ? v : v + seg.shift;
+              return lane < sub && pos < (in_head ? seg.head : seg.L) ? pos : -1;
+            }
+            return lane < sub && v < seg.L ? v : -1;
+          };
+          auto source = [&](int lt) -> int {
+            if constexpr (PART)
+              if (p.head_seq >= 0 && lt * kN + lane * box < seg.sb) return p.head_seq;
+            return seg.i;
+          };
+          auto entry = [&](int lt) -> int {
+            if constexpr (PAGED && PART) {
+              const int pos = box_at(lt);
+              if (pos >= 0)
+                return __ldg(p.table + static_cast<size_t>(source(lt)) * p.max_blocks +
+                             (pos >> sh));
+            }
+            return 0;
+          };
+          int ent = more ? entry(seg.lt0) : 0, row = 0;
+          auto hold = [&](int k, uint32_t phase) {
+            ok = __all_sync(0xffffffffu, ok && wait(k, phase));
+            return ok;
+          };
+          if (!hold(C::SEG_EMPTY + kn % kSegs, (kn / kSegs) ^ 1)) break;
+          const int ph = twins & 1;  // the side of the twins' first tile
+          const uint32_t unit_q = twin_q;
+          if (lane == 0) {
+            Plan& plan = *seg_at(kn);
+            plan.T = T;
+            if (more) {
+              const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
+              plan.twin = twin;
+              plan.qb = unit_q;
+              plan.step = twin ? 2 * kN : kN;
+              plan.j = seg.j;
+              plan.last = whole;
+              plan.part = (2 * static_cast<int>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0)) * p.srows;
+              plan.by_row = 0;
+              plan.head = seg.head;
+#pragma unroll 1
+              for (int sd = 0; sd < 2; ++sd) {
+                typename Plan::Side& v = plan.side[sd];
+                const int tok0 = twin ? 0 : sd * p.tq;
+                v.nt = twin ? (T + 1 - (sd ^ ph)) >> 1 : seg.side_tiles(sd, p.tq);
+                v.first = (seg.lt0 + (twin ? sd ^ ph : 0)) * kN;
+                v.tokens = max(min(seg.ntok - tok0, p.tq), 0);
+                v.row0 = seg.t0 + tok0;
+                seg.sees(p, tok0, v, plan.lo_min);
               }
-              mma_commit(BAR(C::S_FULL + sd));
-              if (sd == 1) mma_commit(BAR(C::EMPTY + k.slot));
+              if constexpr (PART) {
+                if (p.grouped) {  // a unit that is whole leaves its result by row, for the join
+                  const int half = seg.of_head ? 0 : 1;
+                  if (whole) plan.by_row = 1 + half;
+                  plan.last = 0;
+                  const size_t units = static_cast<size_t>(p.total) * p.g;
+                  int* cut = p.cut + (2 * half) * units + static_cast<size_t>(seg.t0) * p.g + seg.j;
+                  if (seg.lt0 == 0) cut[0] = whole ? -1 : static_cast<int>(blockIdx.x);
+                  if (seg.lt0 > 0 && seg.lt1 == seg.ti) cut[units] = static_cast<int>(blockIdx.x);
+                }
+              }
+              if (seg.lt0 == 0 && !whole) {
+                d_head = 1;
+                d_tok0 = seg.t0;
+                d_ntok = seg.ntok;
+                d_j = seg.j;
+              } else if (seg.lt0 > 0) {
+                d_end = seg.lt1 == seg.ti;
+              }
+            }
+            mbar_arrive(BAR(C::SEG_FULL + kn % kSegs));
+          }
+          __syncwarp();
+          ++kn;
+          if (!more) break;
+          if (twin) twins += T;
+          twin_q = twin ? twin_q ^ 1 : 0;
+          // (twins of single tokens read rows that nobody else reads)
+          const uint64_t pol = PART && twin ? pol_once : pol_keep;
+          // query rows of a side (twins: of both)
+          auto load_q = [&](int side) {
+            const int qb = twin ? unit_q : side;
+            if (!twin && seg.side_tiles(side, p.tq) == 0) return;
+            if (!hold(C::Q_EMPTY + qb, (qb ? qn[1] : qn[0]) ^ 1)) return;
+            // (a twin's rows from one token: one box of its heads, the rest of the
+            // tile holds anything)
+            const bool one = twin && seg.ntok == 1;
+            if (lane == 0) {
+              const uint32_t dst = s_base + qb * C::Q_BYTES;
+              mbar_arrive_expect_tx(BAR(C::Q_FULL + qb), (one ? 1 : p.tq) * p.r * DK * 2);
+#pragma unroll 1
+              for (int c = 0; c < DK / 64; ++c)
+                tma_load_3d(dst + c * (kM * 128), one ? &tm_q1 : &tm_q, BAR(C::Q_FULL + qb), 64 * c,
+                            seg.j * p.r, seg.t0 + side * p.tq, pol);
             }
             __syncwarp();
+            if (qb)
+              ++qn[1];
+            else
+              ++qn[0];
+          };
+          load_q(0);
+          // K and V of the tiles by turns: the order the products need them
+          for (int lt = seg.lt0; lt < seg.lt1 && ok; ++lt) {
+            // the pool or cache row of this lane's box, for the tile's K and V
+            const int pos = box_at(lt);
+            row = oob_row;
+            if constexpr (PAGED) {
+              if constexpr (!PART) ent = pc.get_lanes((lt * kN) >> sh);
+              if (pos >= 0) {
+                if (ent >= 0 && ent < p.num_blocks)
+                  row = (ent * p.g + seg.j) * p.bsz + (pos & mask);
+                else
+                  atomicOr(p.status, GQA_DEV_BAD_BLOCK);
+              }
+              if (PART && lt + 1 < seg.lt1) ent = entry(lt + 1);
+            } else if (pos >= 0) {
+              row = pos + static_cast<int>(
+                              (static_cast<long long>(source(lt)) * p.g + seg.j) * p.cap);
+            }
+            int slot = slot_n % C::NS;
+            if (!hold(C::EMPTY + slot, (slot_n / C::NS) ^ 1)) break;
+            uint32_t to = BAR(C::FULL + slot), dst = s_base + C::OFF_RING + slot * C::SLOT;
+            if (lane == 0) mbar_arrive_expect_tx(to, DK / 64 * kN * 128);
+            __syncwarp();
+            if (lane < sub) {
+#pragma unroll
+              for (int c = 0; c < DK / 64; ++c)
+                tma_load_2d(dst + c * (kN * 128) + lane * box * 128, &tm_k, to, 64 * c, row, pol);
+            }
+            __syncwarp();
+            ++slot_n;
+            if (lt == seg.lt0 && !twin) load_q(1);
+            slot = slot_n % C::NS;
+            if (!hold(C::EMPTY + slot, (slot_n / C::NS) ^ 1)) break;
+            to = BAR(C::FULL + slot), dst = s_base + C::OFF_RING + slot * C::SLOT;
+            const int v0 = lt * kN;
+            if (v0 + kN > seg.end || (seg.head < v0 + kN && seg.z > v0 && seg.z > seg.head)) {
+              if (lane == 0)
+                *reinterpret_cast<int4*>(sm + C::OFF_EDGE + 16 * (edge_n % kEdges)) =
+                    make_int4(max(seg.head - v0, 0), seg.z - v0, max(seg.end - v0, 0), slot);
+              to = BAR(C::V_EDGE + edge_n % kEdges);
+              ++edge_n;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(to, DV / 64 * kN * 128);
+            __syncwarp();
+            if (lane < sub) {
+#pragma unroll
+              for (int c = 0; c < DV / 64; ++c)
+                tma_load_2d(dst + c * (kN * 128) + lane * box * 128, &tm_v, to, 64 * c, row, pol);
+            }
+            __syncwarp();
+            ++slot_n;
           }
-          at = k.next();
-          ++t;
-          continue;
-        }
-        if (s == 0 && (t == cur.T - 1 || (t == cur.T && !ahead))) {
-          // (a round early where there is one: its copies are under way by then)
-          nx = next_seg();
           if (!ok) break;
-          ahead = true;
         }
-        if (t == cur.T) primed = nx.T > 0 && !nx.twin;
-        const int nt = s ? cur.nt1 : cur.nt0, nxt = s ? nx.nt1 : nx.nt0;
-        ov = at;
-        sk = t > 0 ? at.next() : at;
-        side_o = side_s = qb = s;
-        do_o = t > 0 && t <= nt;
-        o_first = t == 1;
-        o_last = t == nt;
-        do_s = t < cur.T ? t < nt : primed && nxt > 0;
-        s_first = t == 0 || t == cur.T;
-        s_last = t < cur.T ? t == nt - 1 : nxt == 1;
-        o_free = s_free = s == 1;
-      }
-      if (do_o) {
-        all_wait(C::FULL + ov.slot, ov.phase);
-        all_wait(C::P_READY + side_o, p_ph >> side_o);
-        p_ph ^= 1u << side_o;
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t b0 = v0 + ov.slot * (C::SLOT >> 4);
-        const uint32_t d = C::T_O + side_o * 128, a0 = C::T_S + side_o * 128;
-        if (elect_one()) {
-#pragma unroll
-          for (int e = 0; e < kN / 16; ++e)
-            mma_16_ts(d, a0 + 8 * e, b0 + e * (2048 >> 4), kIdescO, (o_first && e == 0) ? 0u : 1u);
-          if (o_last) mma_commit(BAR(C::O_DONE + side_o));
-          if (o_free) mma_commit(BAR(C::EMPTY + ov.slot));
+        if (lane == 0) {
+          int* d = p.desc + static_cast<size_t>(blockIdx.x) * kDescInts;
+          d[D_HEAD] = ok ? d_head : 0;
+          d[D_TOK0] = d_tok0;
+          d[D_NTOK] = d_ntok;
+          d[D_J] = d_j;
+          d[D_END] = ok ? d_end : 1;
+        }
+        if (ok && lane == 0) {  // no more edges
+          *reinterpret_cast<int4*>(sm + C::OFF_EDGE + 16 * (edge_n % kEdges)) =
+              make_int4(0, 0, 0, -1);
+          mbar_arrive(BAR(C::V_EDGE + edge_n % kEdges));
         }
         __syncwarp();
-      }
-      if (do_s) {
-        if (s_first) {
-          all_wait(C::Q_FULL + qb, q_ph >> qb);
-          q_ph ^= 1u << qb;
-        }
-        all_wait(C::FULL + sk.slot, sk.phase);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t a0 = q0 + ((qb * C::Q_BYTES) >> 4);
-        const uint64_t b0 = k0 + sk.slot * (C::SLOT >> 4);
-        const uint32_t d = C::T_S + side_s * 128;
-        if (elect_one()) {
-#pragma unroll
-          for (int e = 0; e < DK / 16; ++e) {
-            const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
-            mma_bf16(d, a0 + o, b0 + o, kIdescS, e > 0 ? 1u : 0u);
+        if (!ok) {
+          // copies in flight must land before the CTA exits (bounded)
+          const long long t0 = clock64();
+          for (int s = 0; s < C::NS; ++s) {
+            if (slot_n <= static_cast<uint32_t>(s)) continue;
+            const uint32_t last = (slot_n - 1 - s) / C::NS;  // fills of slot s, less one
+            while (!mbar_try_wait(BAR(C::FULL + s), last & 1) && clock64() - t0 < p.budget) {
+            }
           }
-          mma_commit(BAR(C::S_FULL + side_s));
-          if (s_last) mma_commit(BAR(C::Q_EMPTY + qb));
-          if (s_free) mma_commit(BAR(C::EMPTY + sk.slot));
+          for (int s = 0; s < 2; ++s)
+            while (qn[s] > 0 && !mbar_try_wait(BAR(C::Q_FULL + s), (qn[s] - 1) & 1) &&
+                   clock64() - t0 < p.budget) {
+            }
         }
         __syncwarp();
       }
-      if (stream) {
+    } else {
+      // ============================ MMA issuer ==============================
+      // The sides by turns: P.V of the side's last tile, then S of its next
+      // (of the next unit's first at a unit's end).  One warp issues both sides'
+      // products, so each side's run back to back; with an issuer per side they
+      // interleave and both sides wait longer.  The whole warp walks through
+      // this code with warp-uniform values and one elected lane issues: from a
+      // single lane's branch the operands take a detour into the uniform
+      // registers that costs as long as a product runs.
+      constexpr uint32_t kIdescS = idesc_bf16(kM, kN, 0, 0, kBf16);   // both K-major
+      constexpr uint32_t kIdescO = idesc_bf16(kM, DV, 0, 1, kBf16);   // V: MN-major
+      const uint64_t q0 = smem_desc(s_base, 16, 1024, SWZ_128B);
+      const uint64_t k0 = smem_desc(s_base + C::OFF_RING, 16, 1024, SWZ_128B);
+      const uint64_t v0 = smem_desc(s_base + C::OFF_RING, kN * 128, 1024, SWZ_128B);
+      struct Ring {  // a ring position: slot and phase
+        uint32_t slot = 0, phase = 0;
+        __device__ Ring next() const {
+          Ring r = *this;
+          if (++r.slot == C::NS) {
+            r.slot = 0;
+            r.phase ^= 1;
+          }
+          return r;
+        }
+      };
+      bool ok = true;
+      auto all_wait = [&](int k, uint32_t phase) {
+        ok = __all_sync(0xffffffffu, ok && wait(k, phase));
+      };
+      uint32_t kn = 0;                // segments read
+      uint32_t q_ph = 0, p_ph = 0;    // a bit for each query buffer, each side
+      // the next segment: its tiles (0: no more), and the sides'
+      struct Todo {
+        int T, nt0, nt1, qb;
+        bool twin;
+      };
+      auto next_seg = [&]() -> Todo {
+        Todo r = {0, 0, 0, 0, false};
+        all_wait(C::SEG_FULL + kn % kSegs, kn / kSegs);
+        if (!ok) return r;
+        const Plan* sp = seg_at(kn);
+        r.T = __shfl_sync(0xffffffffu, sp->T, 0);
+        r.twin = __shfl_sync(0xffffffffu, sp->twin, 0) != 0;
+        r.qb = __shfl_sync(0xffffffffu, sp->qb, 0);
+        r.nt0 = __shfl_sync(0xffffffffu, sp->side[0].nt, 0);
+        r.nt1 = r.T;  // (the later tokens: they see what the unit sees)
+        __syncwarp();
+        if (elect_one()) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+        __syncwarp();
+        ++kn;
+        return r;
+      };
+      // Two-sided units: in round t side A's P.V of tile t - 1 and its S of tile t,
+      // then side B's; at a unit's end the S of the next unit's first tile.
+      Ring at;               // V of tile t - 1 (t = 0: K of tile 0)
+      int t = 0, s = 0;
+      bool primed = false;   // the next unit's first S are out
+      bool ahead = false;    // the next unit is known
+      // Twins: tiles by turns, without a break between units, S two tiles ahead of P.V.
+      bool stream = false, have = false, ended = false;
+      Ring ks, vo;           // K of the next S, V of the next P.V
+      uint32_t n_s = 0, n_o = 0, flags = 0;  // tiles so far; first, last of a side (two bits each)
+      int ts = 0;
+      Todo cur = next_seg(), nx = cur;
+      // One loop for everything but the steady rounds of two-sided units, with one
+      // place for either product: what runs once a unit is fetched each time.
+      while (ok) {
+        bool do_o = false, do_s = false, o_first = false, o_last = false, s_first = false,
+             s_last = false, o_free = false, s_free = false;
+        int side_o = 0, side_s = 0, qb = 0;
+        Ring ov, sk;
+        if (stream) {
+          // S of tiles 0 and 1, then P.V of a tile and S of the one after next
+          if (!have && !ended) {
+            nx = next_seg();
+            if (!ok) break;
+            have = nx.T > 0 && nx.twin;
+            ended = !have;
+            if (have) cur = nx;
+            ts = 0;
+          }
+          if (ended && n_o == n_s) {
+            stream = false;
+            cur = nx;
+            at = ks;
+            primed = false;
+            t = s = 0;
+            continue;
+          }
+          sk = ks;
+          ov = vo;
+          qb = cur.qb;
+          side_s = n_s & 1;
+          side_o = n_o & 1;
+          do_o = n_s - n_o == 2 || !have;
+          do_s = have;
+          s_first = ts == 0;
+          s_last = ts == cur.T - 1;
+          o_first = (flags >> (2 * side_o)) & 1u;  // (of the tile whose S went out before)
+          o_last = (flags >> (2 * side_o + 1)) & 1u;
+          o_free = s_free = true;
+        } else {
+          if (cur.T == 0) break;
+          if (cur.twin) {
+            stream = have = true;
+            ended = false;
+            ks = at;
+            vo = at.next();
+            ts = 0;
+            continue;
+          }
+          // rounds in which both sides have a P.V and an S that is not their last
+          if (s == 0 && t >= 2 && t < cur.nt0 - 1) {
+            // as below, with as little as can be between one side's products
+            // and the other's
+            const Ring v = at, k = at.next();
+#pragma unroll
+            for (int sd = 0; sd < 2; ++sd) {
+              ok = __all_sync(0xffffffffu,
+                              ok && (sd == 1 || (wait(C::FULL + v.slot, v.phase) &&
+                                                 wait(C::FULL + k.slot, k.phase))) &&
+                                  wait(C::P_READY + sd, p_ph >> sd));
+              p_ph ^= 1u << sd;
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t vb = v0 + v.slot * (C::SLOT >> 4), kb = k0 + k.slot * (C::SLOT >> 4);
+              const uint64_t qa = q0 + ((sd * C::Q_BYTES) >> 4);
+              if (elect_one()) {
+#pragma unroll
+                for (int e = 0; e < kN / 16; ++e)
+                  mma_16_ts(C::T_O + sd * 128, C::T_S + sd * 128 + 8 * e, vb + e * (2048 >> 4),
+                            kIdescO, 1u);
+                if (sd == 1) mma_commit(BAR(C::EMPTY + v.slot));
+#pragma unroll
+                for (int e = 0; e < DK / 16; ++e) {
+                  const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
+                  mma_bf16(C::T_S + sd * 128, qa + o, kb + o, kIdescS, e > 0 ? 1u : 0u);
+                }
+                mma_commit(BAR(C::S_FULL + sd));
+                if (sd == 1) mma_commit(BAR(C::EMPTY + k.slot));
+              }
+              __syncwarp();
+            }
+            at = k.next();
+            ++t;
+            continue;
+          }
+          if (s == 0 && (t == cur.T - 1 || (t == cur.T && !ahead))) {
+            // (a round early where there is one: its copies are under way by then)
+            nx = next_seg();
+            if (!ok) break;
+            ahead = true;
+          }
+          if (t == cur.T) primed = nx.T > 0 && !nx.twin;
+          const int nt = s ? cur.nt1 : cur.nt0, nxt = s ? nx.nt1 : nx.nt0;
+          ov = at;
+          sk = t > 0 ? at.next() : at;
+          side_o = side_s = qb = s;
+          do_o = t > 0 && t <= nt;
+          o_first = t == 1;
+          o_last = t == nt;
+          do_s = t < cur.T ? t < nt : primed && nxt > 0;
+          s_first = t == 0 || t == cur.T;
+          s_last = t < cur.T ? t == nt - 1 : nxt == 1;
+          o_free = s_free = s == 1;
+        }
         if (do_o) {
-          vo = vo.next().next();
-          ++n_o;
+          all_wait(C::FULL + ov.slot, ov.phase);
+          all_wait(C::P_READY + side_o, p_ph >> side_o);
+          p_ph ^= 1u << side_o;
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b0 = v0 + ov.slot * (C::SLOT >> 4);
+          const uint32_t d = C::T_O + side_o * 128, a0 = C::T_S + side_o * 128;
+          if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < kN / 16; ++e)
+              mma_16_ts(d, a0 + 8 * e, b0 + e * (2048 >> 4), kIdescO,
+                        (o_first && e == 0) ? 0u : 1u);
+            if (o_last) mma_commit(BAR(C::O_DONE + side_o));
+            if (o_free) mma_commit(BAR(C::EMPTY + ov.slot));
+          }
+          __syncwarp();
         }
         if (do_s) {
-          const uint32_t f = (ts < 2 ? 1u : 0u) | (ts + 2 >= cur.T ? 2u : 0u);
-          flags = (flags & ~(3u << (2 * side_s))) | (f << (2 * side_s));
-          ks = ks.next().next();
-          ++n_s;
-          if (++ts == cur.T) have = false;
-        }
-      } else {
-        if (s == 1) {
-          at = t < cur.T || primed ? sk.next() : sk;
-          if (t == cur.T) {
-            cur = nx;
-            t = primed ? 1 : 0;
-            primed = ahead = false;
-          } else {
-            ++t;
+          if (s_first) {
+            all_wait(C::Q_FULL + qb, q_ph >> qb);
+            q_ph ^= 1u << qb;
           }
+          all_wait(C::FULL + sk.slot, sk.phase);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a0 = q0 + ((qb * C::Q_BYTES) >> 4);
+          const uint64_t b0 = k0 + sk.slot * (C::SLOT >> 4);
+          const uint32_t d = C::T_S + side_s * 128;
+          if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < DK / 16; ++e) {
+              const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
+              mma_bf16(d, a0 + o, b0 + o, kIdescS, e > 0 ? 1u : 0u);
+            }
+            mma_commit(BAR(C::S_FULL + side_s));
+            if (s_last) mma_commit(BAR(C::Q_EMPTY + qb));
+            if (s_free) mma_commit(BAR(C::EMPTY + sk.slot));
+          }
+          __syncwarp();
         }
-        s ^= 1;
+        if (stream) {
+          if (do_o) {
+            vo = vo.next().next();
+            ++n_o;
+          }
+          if (do_s) {
+            const uint32_t f = (ts < 2 ? 1u : 0u) | (ts + 2 >= cur.T ? 2u : 0u);
+            flags = (flags & ~(3u << (2 * side_s))) | (f << (2 * side_s));
+            ks = ks.next().next();
+            ++n_s;
+            if (++ts == cur.T) have = false;
+          }
+        } else {
+          if (s == 1) {
+            at = t < cur.T || primed ? sk.next() : sk;
+            if (t == cur.T) {
+              cur = nx;
+              t = primed ? 1 : 0;
+              primed = ahead = false;
+            } else {
+              ++t;
+            }
+          }
+          s ^= 1;
+        }
       }
-    }
-    // every product has to be finished before tensor memory is released
-    if (elect_one()) {
-      mma_commit(BAR(C::DRAIN));
-      const long long t0 = clock64();
-      while (!mbar_try_wait(BAR(C::DRAIN), 0) && clock64() - t0 < p.budget) {
+      // every product has to be finished before tensor memory is released
+      if (elect_one()) {
+        mma_commit(BAR(C::DRAIN));
+        const long long t0 = clock64();
+        while (!mbar_try_wait(BAR(C::DRAIN), 0) && clock64() - t0 < p.budget) {
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ======================= softmax, output ==============================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -678,138 +760,131 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool pre = !(p.scale_log2 > 0.f);
     const float sl = pre ? 1.f : p.scale_log2;
     uint32_t sn = 0, on = 0, tn = 0;
-    int d_head = 0, d_tok0 = 0, d_ntok = 0, d_j = 0, d_end = 0;
     bool ok = true;
     for (uint32_t kn = 0;; ++kn) {
       ok = ok && __all_sync(0xffffffffu, wait(C::SEG_FULL + kn % kSegs, (kn / kSegs) & 1));
       if (!ok) break;
-      const Seg seg = *seg_at(kn);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
-      if (seg.lt1 == seg.lt0) break;
-      const int nt = seg.side_tiles(side, p.tq);
-      const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
-      const bool twin = seg.twin(p.tq);
-      const int tok0 = twin ? 0 : side * p.tq;
-      const int my_tok = tok0 + tok;  // token of the unit
-      const bool live = tok < p.tq && my_tok < seg.ntok;
-      const bool warp_live = (warp & 3) * 32 < (seg.ntok - tok0) * p.r;  // (some row is)
-      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0);
-      if (seg.lt0 == 0 && !whole) {
-        d_head = 1;
-        d_tok0 = seg.t0;
-        d_ntok = seg.ntok;
-        d_j = seg.j;
-      } else if (seg.lt0 > 0) {
-        d_end = seg.lt1 == seg.ti;
-      }
-      float m = -INFINITY, l = 0.f;
-      const int my_pos = seg.pos0 + my_tok;
-      const int first_pos = seg.pos0 + tok0;  // the side's first token
+      const Plan* const sp = seg_at(kn);
+      const typename Plan::Side& my = sp->side[side];
+      const int nt = my.nt, first = my.first, step = sp->step, see = my.hi + tok;
+      const bool live = tok < my.tokens;
+      const bool warp_live = (warp & 3) * 32 < my.tokens * p.r;  // (some row is)
       // PART: this row sees [0, vis.head) and [vis.lo, vis.hi) of the unit's
       // span; `side_vis`: what every row of the side sees
-      typename Walk::Visible vis, side_vis;
+      PartVisible vis = {0, 0, see}, side_vis = {0, 0, my.all_hi};
       if constexpr (PART) {
-        vis = seg.visible(p, my_pos, my_pos);
-        side_vis = seg.visible(p, first_pos, seg.pos0 + min(tok0 + p.tq, seg.ntok) - 1);
+        side_vis = {my.all_head, my.all_lo, my.all_hi};
+        vis.lo = max(my.lo + tok, sp->lo_min);
+        vis.head = min(sp->head, see);
+        if (vis.lo <= vis.head) vis.lo = 0;
       }
+      if (sp->T == 0) break;
+      float m = -INFINITY, l = 0.f;
       for (int t = 0; t < nt; ++t) {
         ok = __all_sync(0xffffffffu, wait(C::S_FULL + side, sn & 1));
         ++sn;
         if (!ok) break;
         tc_fence_after();
-        if (!warp_live) {  // (nothing here is read)
-          if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
-          continue;
-        }
-        float x[kN];
+        if (warp_live) {  // (else nothing here is read)
+          float x[kN];
 #pragma unroll
-        for (int c = 0; c < kN / 32; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
-        tmem_wait_ld();
-        if (pre) {
+          for (int c = 0; c < kN / 32; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
+          tmem_wait_ld();
+          if (pre) {
 #pragma unroll
-          for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
-        }
-        const int base = (seg.lt0 + (twin ? 2 * t + (side ^ seg.ph) : t)) * kN;
-        if constexpr (PART) {
-          if (!side_vis.all(base, kN)) {
+            for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
+          }
+          const int base = first + t * step;
+          if constexpr (PART) {
+            if (!side_vis.all(base, kN)) {
+#pragma unroll
+              for (int c = 0; c < kN / 32; ++c) {
+                const int x0 = base + 32 * c;
+                if (side_vis.all(x0, 32)) continue;  // (uniform)
+                const uint32_t bits = vis.bits(x0);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
+              }
+            }
+          } else if (base + kN > side_vis.hi) {
+            // positions past this row's token, 32 at a time (those that the
+            // side's first token sees need no mask)
+            const int lim = see - 1 - base;
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) {
-              const int x0 = base + 32 * c;
-              if (side_vis.all(x0, 32)) continue;  // (uniform)
-              const uint32_t bits = vis.bits(x0);
+              if (base + 32 * c + 32 <= side_vis.hi) continue;  // (uniform)
+              const int see = lim + 1 - 32 * c;
+              const uint32_t bits = see >= 32 ? ~0u : see <= 0 ? 0u : (1u << see) - 1u;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
             }
           }
-        } else if (base + kN - 1 > first_pos) {
-          // positions past this row's token, 32 at a time (those that the
-          // side's first token sees need no mask)
-          const int lim = my_pos - base;
+          float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 0; c < kN / 32; ++c) {
-            if (base + 32 * c + 31 <= first_pos) continue;  // (uniform)
-            const int see = lim + 1 - 32 * c;
-            const uint32_t bits = see >= 32 ? ~0u : see <= 0 ? 0u : (1u << see) - 1u;
+          for (int e = 4; e < kN; e += 8)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
-          }
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+            for (int k = 0; k < 4; ++k)
+              mx[k] = e + 4 < kN ? max3(mx[k], x[e + k], x[e + 4 + k]) : fmaxf(mx[k], x[e + k]);
+          const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          // S_FULL also covers the products issued before it: O is complete
+          // up to the last tile.  (Lanes without a row hold anything: they have no
+          // say in when the others round.)
+          if (__any_sync(0xffffffffu, live && (mn - m) * sl > PRange<T16>::kRaise)) {
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            const float alpha = ex2((m - ref) * sl);
+            m = mn;
+            l *= alpha;
+            if (t > 0) {
 #pragma unroll
-        for (int e = 4; e < kN; e += 8)
+              for (int c = 0; c < DV / 8; ++c) {
+                float o[8];
+                tmem_ld8(tO + 8 * c, o);
+                tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx[k] = e + 4 < kN ? max3(mx[k], x[e + k], x[e + 4 + k]) : fmaxf(mx[k], x[e + k]);
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        // S_FULL also covers the products issued before it: O is complete
-        // up to the last tile.  (Lanes without a row hold anything: they have no
-        // say in when the others round.)
-        if (__any_sync(0xffffffffu, live && (mn - m) * sl > PRange<T16>::kRaise)) {
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          const float alpha = ex2((m - ref) * sl);
-          m = mn;
-          l *= alpha;
-          if (t > 0) {
-#pragma unroll
-            for (int c = 0; c < DV / 8; ++c) {
-              float o[8];
-              tmem_ld8(tO + 8 * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= alpha;
-              tmem_st8(tO + 8 * c, o);
+                for (int e = 0; e < 8; ++e) o[e] *= alpha;
+                tmem_st8(tO + 8 * c, o);
+              }
             }
           }
-        }
-        const float off = m == -INFINITY ? 0.f : PRange<T16>::kLift - m * sl;
-        const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float off = m == -INFINITY ? 0.f : PRange<T16>::kLift - m * sl;
+          const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t u[32];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t u[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 y = fma2(make_float2(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]), sl2, off2);
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-            sum[e & 1] = add2(sum[e & 1], y);
-            u[e] = Half16<T16>::pack2(y.x, y.y);
+            for (int e = 0; e < 32; ++e) {
+              float2 y = fma2(make_float2(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]), sl2, off2);
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum[e & 1] = add2(sum[e & 1], y);
+              u[e] = Half16<T16>::pack2(y.x, y.y);
+            }
+            tmem_st32(tS + 32 * c, u);
           }
-          tmem_st32(tS + 32 * c, u);
+          tmem_wait_st();
+          tc_fence_before();
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
-        tmem_wait_st();
-        tc_fence_before();
+        // (both times: a lane that arrives has to come back to the others before
+        // the next wait, which is the whole warp's)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        __syncwarp();
       }
       if (!ok) break;
       // ---- unit's end: O / l, or a partial (maximum, sum, O) ----
+      const bool twin = sp->twin, last = sp->last;
+      const int other = twin ? sp->T - nt : 0;  // tiles of the other side
+      const int by_row = sp->by_row;
+      const size_t at = sp->part + (twin ? 0 : side * kM);
+      const size_t out_row = static_cast<size_t>(my.row0 + tok) * p.h + sp->j * p.r + head;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+      __syncwarp();
       // (twins: each side joins and writes half of the columns of both)
-      const int other = twin ? seg.side_tiles(side ^ 1, p.tq) : 0;
       if (nt > 0) {
         ok = __all_sync(0xffffffffu, wait(C::O_DONE + side, on & 1));
         ++on;
@@ -825,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ml_sm[side * kM + row] = make_float2(ms, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::TWIN));
+        __syncwarp();
         ok = __all_sync(0xffffffffu, wait(C::TWIN, tn & 1));
         if (!ok) break;
         tc_fence_after();
@@ -838,26 +914,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int c0 = twin ? side * (DV / 64) : 0, c1 = twin ? c0 + DV / 64 : DV / 32;
       const float inv = 1.f / l;
-      const bool last = PART ? whole && !p.grouped : whole;  // nothing left to join
-      const size_t at = slot * p.srows + (twin ? 0 : side * kM);
-      const size_t out_row = static_cast<size_t>(seg.t0 + my_tok) * p.h + seg.j * p.r + head;
       float* pml = p.part_ml + 2 * (at + row);
       float* pdst = p.part_o + (at + row) * DV;
-      if constexpr (PART) {
-        if (p.grouped) {
-          const size_t half = seg.of_head ? 0 : 1;
-          if (whole) {
-            const size_t x = half * p.total * p.h + out_row;
-            pml = p.row_ml + 2 * x;
-            pdst = p.row_o + x * DV;
-          }
-          if (row == 0 && side == 0) {
-            const size_t units = static_cast<size_t>(p.total) * p.g;
-            int* cut = p.cut + (2 * half) * units + static_cast<size_t>(seg.t0) * p.g + seg.j;
-            if (seg.lt0 == 0) cut[0] = whole ? -1 : static_cast<int>(blockIdx.x);
-            if (seg.lt0 > 0 && seg.lt1 == seg.ti) cut[units] = static_cast<int>(blockIdx.x);
-          }
-        }
+      if (PART && by_row) {
+        const size_t x = (by_row - 1) * static_cast<size_t>(p.total) * p.h + out_row;
+        pml = p.row_ml + 2 * x;
+        pdst = p.row_o + x * DV;
       }
       if (!last && live && (!twin || side == 0)) {
         pml[0] = ms;
@@ -911,17 +973,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (twin) {  // both O and ml_sm are free again
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::TWIN + 1));
+        __syncwarp();
         ok = __all_sync(0xffffffffu, wait(C::TWIN + 1, tn & 1));
         ++tn;
       }
-    }
-    if (threadIdx.x == 0) {
-      int* d = p.desc + static_cast<size_t>(blockIdx.x) * kDescInts;
-      d[D_HEAD] = ok ? d_head : 0;
-      d[D_TOK0] = d_tok0;
-      d[D_NTOK] = d_ntok;
-      d[D_J] = d_j;
-      d[D_END] = ok ? d_end : 1;
     }
   }
 

@@ -16,7 +16,6 @@
 // units that one sequence fills the prefix is the head of the unit's span: the
 // tiles read are the same and nothing has to be joined.
 #include "chunk_kernel.cuh"
-#include "part_device.cuh"
 
 namespace gqa {
 namespace {
@@ -32,23 +31,27 @@ struct PartSeg {
   int head;        // positions of the span's head
   int shift, sb, z, end;  // the span (end: of its last position seen by the sequence)
   bool of_head;    // a unit over the head alone, for rows of all sequences
-  int ph, qb;      // as in chunk_attn.cu
   __device__ bool twin(int tq) const { return ntok <= tq; }
   __device__ int side_tiles(int side, int tq) const {
-    if (twin(tq)) return (lt1 - lt0 + 1 - (side ^ ph)) >> 1;
     const int nt = min(ntok - side * tq, tq);
     const int ext = of_head ? head : pos0 + side * tq + nt - shift;
     return max(0, min(lt1, (ext + kN - 1) / kN) - lt0);
   }
-  // what every token at positions first .. last sees
-  __device__ PartVisible visible(const ChunkParams& p, int first, int last) const {
-    if (of_head) return {head, 0, 0};
-    PartVisible v;
-    v.hi = first + 1 - shift;
-    v.lo = max(last - p.window + 1, p.base_min) - shift;
-    v.head = min(head, v.hi);
-    if (v.lo <= v.head) v.lo = 0;
-    return v;
+  // what the tokens from tok0 on see, the side's last one being tq tokens on
+  __device__ void sees(const ChunkParams& p, int tok0, SegPlan::Side& v, int& lo_min) const {
+    const int last = min(tok0 + p.tq, ntok) - 1;
+    v.hi = pos0 + tok0 + 1 - shift;
+    v.lo = pos0 + tok0 - p.window + 1 - shift;
+    lo_min = p.base_min - shift;
+    if (of_head) {  // (no index of it is behind the head)
+      v.hi = 0x7FFFFF00;
+      v.lo = 0;
+      lo_min = 0x7FFFFFFF;
+    }
+    v.all_hi = v.hi;
+    v.all_head = min(head, v.hi);
+    v.all_lo = max(v.lo + last - tok0, lo_min);
+    if (v.all_lo <= v.all_head) v.all_lo = 0;
   }
 };
 
@@ -67,7 +70,6 @@ constexpr unsigned kPartNear = 2;  // tiles
 
 struct PartWalk {
   using Seg = PartSeg;
-  using Visible = PartVisible;
   static constexpr bool kPart = true;
 
   const ChunkParams& p;
