@@ -277,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(C::FULL + v.w));
-          __syncwarp();
+          mbar_arrive_if(BAR(C::FULL + v.w), lane == 0);
         }
         __syncwarp();
       } else {
@@ -618,36 +617,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (s == 0 && t >= 2 && t < cur.nt0 - 1) {
             // as below, with as little as can be between one side's products
             // and the other's
-            const Ring v = at, k = at.next();
+            do {
+              const Ring v = at, k = at.next();
 #pragma unroll
-            for (int sd = 0; sd < 2; ++sd) {
-              ok = __all_sync(0xffffffffu,
-                              ok && (sd == 1 || (wait(C::FULL + v.slot, v.phase) &&
-                                                 wait(C::FULL + k.slot, k.phase))) &&
-                                  wait(C::P_READY + sd, p_ph >> sd));
-              p_ph ^= 1u << sd;
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t vb = v0 + v.slot * (C::SLOT >> 4), kb = k0 + k.slot * (C::SLOT >> 4);
-              const uint64_t qa = q0 + ((sd * C::Q_BYTES) >> 4);
-              if (elect_one()) {
+              for (int sd = 0; sd < 2; ++sd) {
+                ok = __all_sync(0xffffffffu,
+                                ok && (sd == 1 || (wait(C::FULL + v.slot, v.phase) &&
+                                                   wait(C::FULL + k.slot, k.phase))) &&
+                                    wait(C::P_READY + sd, p_ph >> sd));
+                p_ph ^= 1u << sd;
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vb = v0 + v.slot * (C::SLOT >> 4), kb = k0 + k.slot * (C::SLOT >> 4);
+                const uint64_t qa = q0 + ((sd * C::Q_BYTES) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int e = 0; e < kN / 16; ++e)
-                  mma_16_ts(C::T_O + sd * 128, C::T_S + sd * 128 + 8 * e, vb + e * (2048 >> 4),
-                            kIdescO, 1u);
-                if (sd == 1) mma_commit(BAR(C::EMPTY + v.slot));
+                  for (int e = 0; e < kN / 16; ++e)
+                    mma_16_ts(C::T_O + sd * 128, C::T_S + sd * 128 + 8 * e, vb + e * (2048 >> 4),
+                              kIdescO, 1u);
+                  if (sd == 1) mma_commit(BAR(C::EMPTY + v.slot));
 #pragma unroll
-                for (int e = 0; e < DK / 16; ++e) {
-                  const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
-                  mma_bf16(C::T_S + sd * 128, qa + o, kb + o, kIdescS, e > 0 ? 1u : 0u);
+                  for (int e = 0; e < DK / 16; ++e) {
+                    const uint32_t o = ((e >> 2) * (kM * 128) + (e & 3) * 32) >> 4;
+                    mma_bf16(C::T_S + sd * 128, qa + o, kb + o, kIdescS, e > 0 ? 1u : 0u);
+                  }
+                  mma_commit(BAR(C::S_FULL + sd));
+                  if (sd == 1) mma_commit(BAR(C::EMPTY + k.slot));
                 }
-                mma_commit(BAR(C::S_FULL + sd));
-                if (sd == 1) mma_commit(BAR(C::EMPTY + k.slot));
+                __syncwarp();
               }
-              __syncwarp();
-            }
-            at = k.next();
-            ++t;
+              at = k.next();
+              ++t;
+            } while (ok && t < cur.nt0 - 1);
             continue;
           }
           if (s == 0 && (t == cur.T - 1 || (t == cur.T && !ahead))) {
@@ -779,100 +780,101 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (vis.lo <= vis.head) vis.lo = 0;
       }
       if (sp->T == 0) break;
-      float m = -INFINITY, l = 0.f;
-      for (int t = 0; t < nt; ++t) {
+      // (lanes without a row hold anything: with their maximum at infinity they
+      // have no say in when the others' is raised)
+      float m = live ? -INFINITY : INFINITY, l = 0.f;
+      for (int t = 0; t < (warp_live ? 0 : nt); ++t) {  // nothing here is read
+        ok = __all_sync(0xffffffffu, ok && wait(C::S_FULL + side, sn & 1));
+        ++sn;
+        mbar_arrive_if(BAR(C::P_READY + side), lane == 0);
+      }
+      for (int t = 0; t < (warp_live ? nt : 0); ++t) {
         ok = __all_sync(0xffffffffu, wait(C::S_FULL + side, sn & 1));
         ++sn;
         if (!ok) break;
         tc_fence_after();
-        if (warp_live) {  // (else nothing here is read)
-          float x[kN];
+        float x[kN];
 #pragma unroll
-          for (int c = 0; c < kN / 32; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
-          tmem_wait_ld();
-          if (pre) {
+        for (int c = 0; c < kN / 32; ++c) tmem_ld32(tS + 32 * c, x + 32 * c);
+        tmem_wait_ld();
+        if (pre) {
 #pragma unroll
-            for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
-          }
-          const int base = first + t * step;
-          if constexpr (PART) {
-            if (!side_vis.all(base, kN)) {
-#pragma unroll
-              for (int c = 0; c < kN / 32; ++c) {
-                const int x0 = base + 32 * c;
-                if (side_vis.all(x0, 32)) continue;  // (uniform)
-                const uint32_t bits = vis.bits(x0);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
-              }
-            }
-          } else if (base + kN > side_vis.hi) {
-            // positions past this row's token, 32 at a time (those that the
-            // side's first token sees need no mask)
-            const int lim = see - 1 - base;
+          for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
+        }
+        const int base = first + t * step;
+        if constexpr (PART) {
+          if (!side_vis.all(base, kN)) {
 #pragma unroll
             for (int c = 0; c < kN / 32; ++c) {
-              if (base + 32 * c + 32 <= side_vis.hi) continue;  // (uniform)
-              const int see = lim + 1 - 32 * c;
-              const uint32_t bits = see >= 32 ? ~0u : see <= 0 ? 0u : (1u << see) - 1u;
+              const int x0 = base + 32 * c;
+              if (side_vis.all(x0, 32)) continue;  // (uniform)
+              const uint32_t bits = vis.bits(x0);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
             }
           }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
+        } else if (base + kN > side_vis.hi) {
+          // positions past this row's token, 32 at a time (those that the
+          // side's first token sees need no mask)
+          const int lim = see - 1 - base;
 #pragma unroll
-          for (int e = 4; e < kN; e += 8)
+          for (int c = 0; c < kN / 32; ++c) {
+            if (base + 32 * c + 32 <= side_vis.hi) continue;  // (uniform)
+            const int see = lim + 1 - 32 * c;
+            const uint32_t bits = see >= 32 ? ~0u : see <= 0 ? 0u : (1u << see) - 1u;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = e + 4 < kN ? max3(mx[k], x[e + k], x[e + 4 + k]) : fmaxf(mx[k], x[e + k]);
-          const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          // S_FULL also covers the products issued before it: O is complete
-          // up to the last tile.  (Lanes without a row hold anything: they have no
-          // say in when the others round.)
-          if (__any_sync(0xffffffffu, live && (mn - m) * sl > PRange<T16>::kRaise)) {
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            const float alpha = ex2((m - ref) * sl);
-            m = mn;
-            l *= alpha;
-            if (t > 0) {
-#pragma unroll
-              for (int c = 0; c < DV / 8; ++c) {
-                float o[8];
-                tmem_ld8(tO + 8 * c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= alpha;
-                tmem_st8(tO + 8 * c, o);
-              }
-            }
+            for (int e = 0; e < 32; ++e)
+              if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
           }
-          const float off = m == -INFINITY ? 0.f : PRange<T16>::kLift - m * sl;
-          const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t u[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float2 y = fma2(make_float2(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]), sl2, off2);
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              sum[e & 1] = add2(sum[e & 1], y);
-              u[e] = Half16<T16>::pack2(y.x, y.y);
-            }
-            tmem_st32(tS + 32 * c, u);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
-        // (both times: a lane that arrives has to come back to the others before
-        // the next wait, which is the whole warp's)
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int e = 4; e < kN; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = e + 4 < kN ? max3(mx[k], x[e + k], x[e + 4 + k]) : fmaxf(mx[k], x[e + k]);
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        // S_FULL also covers the products issued before it: O is complete
+        // up to the last tile.
+        if (__any_sync(0xffffffffu, (mn - m) * sl > PRange<T16>::kRaise)) {
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          const float alpha = ex2((m - ref) * sl);
+          m = mn;
+          l *= alpha;
+          if (t > 0) {
+#pragma unroll
+            for (int c = 0; c < DV / 8; ++c) {
+              float o[8];
+              tmem_ld8(tO + 8 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= alpha;
+              tmem_st8(tO + 8 * c, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : PRange<T16>::kLift - m * sl;
+        const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t u[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float2 y = fma2(make_float2(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]), sl2, off2);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum[e & 1] = add2(sum[e & 1], y);
+            u[e] = Half16<T16>::pack2(y.x, y.y);
+          }
+          tmem_st32(tS + 32 * c, u);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
-        __syncwarp();
+        mbar_arrive_if(BAR(C::P_READY + side), lane == 0);
       }
       if (!ok) break;
       // ---- unit's end: O / l, or a partial (maximum, sum, O) ----
@@ -882,8 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t at = sp->part + (twin ? 0 : side * kM);
       const size_t out_row = static_cast<size_t>(my.row0 + tok) * p.h + sp->j * p.r + head;
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
-      __syncwarp();
+      mbar_arrive_if(BAR(C::SEG_EMPTY + kn % kSegs), lane == 0);
       // (twins: each side joins and writes half of the columns of both)
       if (nt > 0) {
         ok = __all_sync(0xffffffffu, wait(C::O_DONE + side, on & 1));
@@ -899,8 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // complete too)
         ml_sm[side * kM + row] = make_float2(ms, l);
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::TWIN));
-        __syncwarp();
+        mbar_arrive_if(BAR(C::TWIN), lane == 0);
         ok = __all_sync(0xffffffffu, wait(C::TWIN, tn & 1));
         if (!ok) break;
         tc_fence_after();
@@ -972,8 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       if (twin) {  // both O and ml_sm are free again
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::TWIN + 1));
-        __syncwarp();
+        mbar_arrive_if(BAR(C::TWIN + 1), lane == 0);
         ok = __all_sync(0xffffffffu, wait(C::TWIN + 1, tn & 1));
         ++tn;
       }
