@@ -30,9 +30,23 @@
 //              elected lane issues (from one lane's branch eight products took
 //              460 cycles to issue, as long as they run)
 //   warp 10    TMA: the sides' query rows once per unit, K and V tiles into a
-//              ring (64-column boxes, 128-byte swizzle)
-//   warp 11    the run's end (the TMA warp finds its start meanwhile)
+//              ring (64-column boxes, 128-byte swizzle); finds the run's start
+//              and works out each unit for the others (SegPlan)
+//   warp 11    the run's end (in the same instructions as its start), then the V
+//              rows that nobody sees: zeroed in shared memory
 //   (warp 9 checks the lengths: registers are dealt out by warpgroups)
+// A unit whose rows fit one side runs as twins: both sides hold its rows and take
+// its tiles by turns.  Units of twins follow one another without a break (their
+// query rows are staged once, in the two buffers by turns), and softmax warps
+// without a row only pass the barriers.
+//
+// What runs once a unit or once a launch is written for few instructions: it is
+// fetched anew each time, at a few hundred cycles a line, and stands on the
+// critical path between two units.  (The walk of chunk_part.cu with its scans and
+// divisions inlined five times cost 15 us a launch; the softmax's own look at a
+// new unit 1.5 us from one unit to the next.)  The warps' waits are the whole
+// warp's, so a single lane arrives by a predicated instruction, not behind a
+// branch: with the branch one lane ran ahead of the others in some builds.
 // TMEM columns: S_A 0-127, S_B 128-255 (each holds P, two 16-bit values a
 // column, once its S has been read), O_A 256.., O_B 384...
 //
@@ -43,9 +57,14 @@
 // end leaves partial results (row maximum, sum, unnormalised
 // output, all fp32) in the workspace, and a second small kernel joins them.
 //
-// Rows >= L_i: masked out of S, their V rows zeroed in shared memory.
+// Rows that no token of the sequence sees: masked out of S, their V rows zeroed in
+// shared memory.
 //
-// Bound by the tensor cores where units are long: a prompt of 8,192 tokens,
+// Two users: chunk_attn.cu (causal, the whole cache) and chunk_part.cu (a window
+// and the first positions, or a prefix that the batch shares: PART), which differ
+// in the split of the work, where a tile's boxes lie and the masks.
+//
+// Bound by the tensor cores where units are long: a causal prompt of 8,192 tokens,
 // h = 64, g = 8, d = 128, bf16: 649 to 653 us, 1,690 TFLOP/s, in a short graph
 // replay, 704 to 718 us, 1,530 to 1,560, among other passes, as the clock falls
 // under the power limit.  What the pipe still waits for is a side's own chain
@@ -340,59 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok && wait(k, phase));
             return ok;
           };
-          if (!hold(C::SEG_EMPTY + kn % kSegs, (kn / kSegs) ^ 1)) break;
           const int ph = twins & 1;  // the side of the twins' first tile
           const uint32_t unit_q = twin_q;
-          if (lane == 0) {
-            Plan& plan = *seg_at(kn);
-            plan.T = T;
-            if (more) {
-              const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
-              plan.twin = twin;
-              plan.qb = unit_q;
-              plan.step = twin ? 2 * kN : kN;
-              plan.j = seg.j;
-              plan.last = whole;
-              plan.part = (2 * static_cast<int>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0)) * p.srows;
-              plan.by_row = 0;
-              plan.head = seg.head;
-#pragma unroll 1
-              for (int sd = 0; sd < 2; ++sd) {
-                typename Plan::Side& v = plan.side[sd];
-                const int tok0 = twin ? 0 : sd * p.tq;
-                v.nt = twin ? (T + 1 - (sd ^ ph)) >> 1 : seg.side_tiles(sd, p.tq);
-                v.first = (seg.lt0 + (twin ? sd ^ ph : 0)) * kN;
-                v.tokens = max(min(seg.ntok - tok0, p.tq), 0);
-                v.row0 = seg.t0 + tok0;
-                seg.sees(p, tok0, v, plan.lo_min);
-              }
-              if constexpr (PART) {
-                if (p.grouped) {  // a unit that is whole leaves its result by row, for the join
-                  const int half = seg.of_head ? 0 : 1;
-                  if (whole) plan.by_row = 1 + half;
-                  plan.last = 0;
-                  const size_t units = static_cast<size_t>(p.total) * p.g;
-                  int* cut = p.cut + (2 * half) * units + static_cast<size_t>(seg.t0) * p.g + seg.j;
-                  if (seg.lt0 == 0) cut[0] = whole ? -1 : static_cast<int>(blockIdx.x);
-                  if (seg.lt0 > 0 && seg.lt1 == seg.ti) cut[units] = static_cast<int>(blockIdx.x);
-                }
-              }
-              if (seg.lt0 == 0 && !whole) {
-                d_head = 1;
-                d_tok0 = seg.t0;
-                d_ntok = seg.ntok;
-                d_j = seg.j;
-              } else if (seg.lt0 > 0) {
-                d_end = seg.lt1 == seg.ti;
-              }
-            }
-            mbar_arrive(BAR(C::SEG_FULL + kn % kSegs));
-          }
-          __syncwarp();
-          ++kn;
-          if (!more) break;
-          if (twin) twins += T;
-          twin_q = twin ? twin_q ^ 1 : 0;
           // (twins of single tokens read rows that nobody else reads)
           const uint64_t pol = PART && twin ? pol_once : pol_keep;
           // query rows of a side (twins: of both)
@@ -417,7 +385,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
               ++qn[0];
           };
-          load_q(0);
+          // (the first unit's rows before anything else; later ones wait for the unit
+          // ahead, whose end waits for this announcement)
+          const bool q_early = kn == 0 && more;
+          if (q_early) load_q(0);
+          if (!hold(C::SEG_EMPTY + kn % kSegs, (kn / kSegs) ^ 1)) break;
+          Plan& plan = *seg_at(kn);
+          if (lane < 2 && more) {  // (a side each)
+            typename Plan::Side& v = plan.side[lane];
+            const int tok0 = twin ? 0 : lane * p.tq;
+            v.nt = twin ? (T + 1 - (lane ^ ph)) >> 1 : seg.side_tiles(lane, p.tq);
+            v.first = (seg.lt0 + (twin ? lane ^ ph : 0)) * kN;
+            v.tokens = max(min(seg.ntok - tok0, p.tq), 0);
+            v.row0 = seg.t0 + tok0;
+            seg.sees(p, tok0, v, plan.lo_min);  // (lo_min: the same from both)
+          }
+          const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
+          if (lane == 0) {
+            plan.T = T;
+            plan.twin = twin;
+            plan.qb = unit_q;
+            plan.step = twin ? 2 * kN : kN;
+            plan.j = seg.j;
+            plan.last = whole;
+            plan.part = (2 * static_cast<int>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0)) * p.srows;
+            plan.by_row = 0;
+            plan.head = seg.head;
+            if constexpr (PART) {
+              if (more && p.grouped) {  // a whole unit leaves its result by row, for the join
+                const int half = seg.of_head ? 0 : 1;
+                if (whole) plan.by_row = 1 + half;
+                plan.last = 0;
+                const size_t units = static_cast<size_t>(p.total) * p.g;
+                int* cut = p.cut + (2 * half) * units + static_cast<size_t>(seg.t0) * p.g + seg.j;
+                if (seg.lt0 == 0) cut[0] = whole ? -1 : static_cast<int>(blockIdx.x);
+                if (seg.lt0 > 0 && seg.lt1 == seg.ti) cut[units] = static_cast<int>(blockIdx.x);
+              }
+            }
+          }
+          __syncwarp();
+          mbar_arrive_if(BAR(C::SEG_FULL + kn % kSegs), lane == 0);
+          if (more && seg.lt0 == 0 && !whole) {
+            d_head = 1;
+            d_tok0 = seg.t0;
+            d_ntok = seg.ntok;
+            d_j = seg.j;
+          } else if (more && seg.lt0 > 0) {
+            d_end = seg.lt1 == seg.ti;
+          }
+          ++kn;
+          if (!more) break;
+          if (twin) twins += T;
+          twin_q = twin ? twin_q ^ 1 : 0;
+          if (!q_early) load_q(0);
           // K and V of the tiles by turns: the order the products need them
           for (int lt = seg.lt0; lt < seg.lt1 && ok; ++lt) {
             // the pool or cache row of this lane's box, for the tile's K and V

@@ -15,6 +15,20 @@
 // results of units that no run's end cuts lie by row, the others by CTA.  With
 // units that one sequence fills the prefix is the head of the unit's span: the
 // tiles read are the same and nothing has to be joined.
+//
+// Measured (graph replay, bf16, d = 128; floors at the measured copy and GEMM
+// rates).  64 single tokens over windows of 4,096, h = 64, g = 8, 64-row blocks:
+// 170 us, 6,250 GB/s (157): HBM, then 4 us of start and the join.  A prompt of
+// 8,192 in a window of 2,048: 352 us (254): 17 tiles a unit of 32 tokens where 16
+// are seen, 4 us from one unit to the next (three tiles' time), the clock under
+// load.  32 mixed sequences, 7,506 tokens, window 1,000: 124 us (38): units of six
+// tiles, join.  64 single tokens behind a prefix of 8,192: 62 us (22): 512 units
+// of five tiles and the prefix's long ones beside them.  16 chunks of 50 to 400
+// tokens behind 6,000: 211 us (147).
+//
+// Boxes of 64 positions (or a block): with 128, a few sinks cost a whole tile and
+// a window begins up to 127 positions early; with 16, a tile is 64 copies.
+// Contiguous windows begin at any row.
 #include "chunk_kernel.cuh"
 
 namespace gqa {
@@ -307,7 +321,8 @@ __global__ void __launch_bounds__(kGroupThreads) group_join_kernel(const ChunkPa
       static_cast<long long>(blockIdx.x) * (kGroupThreads / 32) + (threadIdx.x >> 5);
   const long long tj = id / pairs;
   const int a_first = 2 * static_cast<int>(id - tj * pairs);
-  const int t = static_cast<int>(tj / p.g), j = static_cast<int>(tj - static_cast<long long>(t) * p.g);
+  const int t = static_cast<int>(tj / p.g);
+  const int j = static_cast<int>(tj - static_cast<long long>(t) * p.g);
   const int T = PartWalk::head_tokens(p);
   if (t >= T) return;  // (uniform across the warp, as all below)
   const int i = packed_sequence(p.cu, p.b, t);
@@ -409,15 +424,29 @@ template <typename T16, int DV>
 cudaError_t PartWalk::join(cudaLaunchConfig_t& cfg, const ChunkParams& p, int num_sms) {
   if (!p.grouped) return launch_join<T16, DV>(cfg, p, num_sms);
   const long long warps = static_cast<long long>(p.total) * p.g * ((p.r + 1) / 2);
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + kGroupThreads / 32 - 1) / (kGroupThreads / 32)));
+  constexpr int kWarps = kGroupThreads / 32;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps));
   cfg.blockDim = dim3(kGroupThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, group_join_kernel<T16, DV>, p, num_sms);
 }
 
 // Are the prefix's units to be shared by the sequences?  (tq: tokens of a side)
-bool prefix_grouped(int b, int total, int tq) {
+// Shared, a row's two results are written, read back and joined; not shared,
+// every sequence reads the prefix for its own rows.  Measured, n tokens a
+// sequence, us shared / not: 16 sequences behind 6,000 (tq = 32) n = 1 21 / 52, n =
+// 31 58 / 64, n = 64 116 / 85; 64 behind 8,192 (tq = 16) n = 1 57 / 222, n = 15 228
+// / 237, n = 32 441 / 334; 4 behind 3,000 (tq = 18) n = 17 22 / 34; 16 behind 700 n =
+// 1 18 / 21, n = 4 24 / 21.5, n = 31 36 / 32: with few positions in common the join
+// costs more than their tiles.
+bool prefix_few(int b, int total, int tq) {
   return b > 1 && total < static_cast<long long>(b) * tq;
+}
+constexpr int kLongPrefix = 2048;
+
+bool prefix_grouped(int b, int total, int tq, int prefix_len) {
+  return prefix_few(b, total, tq) && prefix_len > 0 &&
+         (prefix_len >= kLongPrefix || total <= 2ll * b);
 }
 
 int part_run(const ChunkCall& x, void* stream) {
@@ -448,7 +477,7 @@ int prefix_run(ChunkCall& x, int prefix_len, void* stream) {
   x.head = x.base_min = prefix_len;
   x.head_seq = 0;
   if (x.g > 0 && x.h > 0 && x.h / x.g >= 1 && x.h / x.g <= kM)
-    x.grouped = prefix_len > 0 && prefix_grouped(x.b, x.total, kM / (x.h / x.g));
+    x.grouped = prefix_grouped(x.b, x.total, kM / (x.h / x.g), prefix_len);
   return part_run(x, stream);
 }
 
@@ -519,7 +548,7 @@ int gqa_chunk_attn_prefix_workspace(int b, int total, int h, int g, int d_k, int
   const int tq = kM / (h / g);
   const long long most = std::min<long long>(total, static_cast<long long>(b) * tq - 1);
   size_t n = chunk_plan(total, h, g, d_v, num_sms).bytes;
-  if (prefix_grouped(b, static_cast<int>(most), tq))
+  if (prefix_few(b, static_cast<int>(most), tq))
     n = std::max(n, chunk_plan(static_cast<int>(most), h, g, d_v, num_sms, true).bytes);
   *bytes = static_cast<long long>(n);
   return GQA_OK;

@@ -631,8 +631,9 @@ int gqa_chunk_attn_window_paged(const void* q, const void* k_pool, const void* v
  * anything; the prefix and the rows prefix_len <= p < L_i hold finite values.
  * Otherwise as gqa_chunk_attn; cap (paged: max_blocks * block_size) up to
  * 2^31 - 256.  Where sequences bring few tokens each (total below b times 128 /
- * (h / g)) the prefix is read once for many of them, with three kernels; else
- * once for each, with the call's two kernels of gqa_chunk_attn.
+ * (h / g); at most 2 b behind a prefix of less than 2,048) the prefix is attended
+ * once for many of them and joined with each one's own positions, else once for
+ * each.
  *
  * gqa_chunk_attn_prefix_paged - the same over a paged cache: the prefix is
  * found through row 0 of the block table.  Entries of whole blocks of the
