@@ -1,6 +1,6 @@
 // chunk_kernel.cuh - attention of packed chunks of new tokens (prompts,
-// prompt chunks, single tokens, mixed) over a contiguous or paged 16-bit
-// cache, on the tcgen05 tensor cores.
+// prompt chunks, single tokens, mixed) over a part of a contiguous or paged
+// 16-bit cache, on the tcgen05 tensor cores.
 //
 // A unit is a block of query rows of one (sequence, KV head): the r = h / g
 // query heads of a group share K and V, so rows are packed token-major (row
@@ -60,19 +60,12 @@
 // Rows that no token of the sequence sees: masked out of S, their V rows zeroed in
 // shared memory.
 //
-// Two users: chunk_attn.cu (causal, the whole cache) and chunk_part.cu (a window
-// and the first positions, or a prefix that the batch shares: PART), which differ
-// in the split of the work, where a tile's boxes lie and the masks.
-//
-// Bound by the tensor cores where units are long: a causal prompt of 8,192 tokens,
-// h = 64, g = 8, d = 128, bf16: 649 to 653 us, 1,690 TFLOP/s, in a short graph
-// replay, 704 to 718 us, 1,530 to 1,560, among other passes, as the clock falls
-// under the power limit.  What the pipe still waits for is a side's own chain
-// of S, softmax and hand-over, which is a little longer than the other side's
-// products.  Short units are bound by their fixed cost (query rows in, first
-// logits, output): 130 to 141 us for 32 mixed sequences of 5,957 tokens, 33.8
-// us for 48 packed short prompts with 64-wide heads, 17.8 us for eight chunks
-// of 4 to 12 tokens.
+// Used by chunk_part.cu, whose PartWalk gives the units, where their rows lie and
+// what their tokens see.  chunk_attn.cu has a kernel of its own for causal chunks
+// over the whole cache, with the same products and the same roles, but units
+// looked at by each role for itself: on this kernel a causal prompt of 8,192 took
+// 731 us where that takes 710, packed short prompts 36.4 (34.3).  Figures of this
+// one: chunk_part.cu.
 #pragma once
 
 #include <cuda.h>
@@ -147,7 +140,7 @@ struct ChunkParams {
   int srows;
   unsigned int* status;
   long long budget;
-  // a part of the cache (PART): tokens see their last `window` positions and
+  // the part of the cache: tokens see their last `window` positions and
   // the first `head` ones, which are read from sequence head_seq (-1: each
   // from its own); positions below base_min belong to the head alone
   int window, head, head_seq, base_min;
@@ -190,7 +183,7 @@ struct SegPlan {
     int first;   // position of the first one
     int tokens;  // tokens with rows
     int row0;    // packed row of the first
-    // (PART) token k sees [0, min(head, hi)) and [max(lo + k, lo_min), hi + k) of
+    // token k sees [0, min(head, hi)) and [max(lo + k, lo_min), hi + k) of
     // the span; every token [0, all_head) and [all_lo, all_hi)
     int lo, hi, all_head, all_lo, all_hi;
   } side[2];
@@ -209,7 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = ChunkCfg<DK, DV>;
   using Seg = typename Walk::Seg;
   using Plan = SegPlan;
-  constexpr bool PART = Walk::kPart;
   constexpr bool kBf16 = Half16<T16>::kBf16;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t s_base = smem_u32(sm);
@@ -303,10 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ============================ TMA producer ============================
         Seg seg;
         const uint64_t pol_keep = policy_evict_last(), pol_once = policy_evict_first();
-        const int oob_row = PAGED  ? p.num_blocks * p.g * p.bsz
-                            : PART ? static_cast<int>(static_cast<long long>(p.b) * p.g * p.cap)
-                                   : 0;
-        const int box = PART ? (PAGED ? min(p.bsz, kGrain) : kGrain) : PAGED ? min(p.bsz, kN) : kN;
+        const int oob_row = PAGED ? p.num_blocks * p.g * p.bsz
+                                  : static_cast<int>(static_cast<long long>(p.b) * p.g * p.cap);
+        const int box = PAGED ? min(p.bsz, kGrain) : kGrain;
         const int sub = kN / box;  // boxes a tile and 64-column half
         const int sh = PAGED ? __ffs(p.bsz) - 1 : 0, mask = p.bsz - 1;  // (a power of two)
         uint32_t slot_n = 0, qn[2] = {0, 0}, edge_n = 0;
@@ -320,33 +311,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!more) seg.lt0 = seg.lt1 = 0;
           const int T = seg.lt1 - seg.lt0;
           const bool twin = seg.twin(p.tq);
-          // the sequence's table entries, 64 at a time ahead of their use: no load
-          // stands before a tile's copies
-          PageCursor pc;
-          if constexpr (PAGED && !PART)
-            if (more)
-              pc.start(p.table + static_cast<size_t>(seg.i) * p.max_blocks,
-                       static_cast<int>((static_cast<unsigned>(seg.L) + mask) >> sh),
-                       (seg.lt0 * kN) >> sh);
-          // PART: the position of this lane's box of tile lt (-1: none), and the
+          // The position of this lane's box of tile lt (-1: none), and the
           // table entry that holds it.  (One load a box, a tile ahead of its use:
           // a tile's boxes may lie in two places.)
           auto box_at = [&](int lt) -> int {
             const int v = lt * kN + lane * box;
-            if constexpr (PART) {
-              const bool in_head = v < seg.sb;
-              const int pos = in_head ? v : v + seg.shift;
-              return lane < sub && pos < (in_head ? seg.head : seg.L) ? pos : -1;
-            }
-            return lane < sub && v < seg.L ? v : -1;
+            const bool in_head = v < seg.sb;
+            const int pos = in_head ? v : v + seg.shift;
+            return lane < sub && pos < (in_head ? seg.head : seg.L) ? pos : -1;
           };
           auto source = [&](int lt) -> int {
-            if constexpr (PART)
-              if (p.head_seq >= 0 && lt * kN + lane * box < seg.sb) return p.head_seq;
-            return seg.i;
+            return p.head_seq >= 0 && lt * kN + lane * box < seg.sb ? p.head_seq : seg.i;
           };
           auto entry = [&](int lt) -> int {
-            if constexpr (PAGED && PART) {
+            if constexpr (PAGED) {
               const int pos = box_at(lt);
               if (pos >= 0)
                 return __ldg(p.table + static_cast<size_t>(source(lt)) * p.max_blocks +
@@ -362,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ph = twins & 1;  // the side of the twins' first tile
           const uint32_t unit_q = twin_q;
           // (twins of single tokens read rows that nobody else reads)
-          const uint64_t pol = PART && twin ? pol_once : pol_keep;
+          const uint64_t pol = twin ? pol_once : pol_keep;
           // query rows of a side (twins: of both)
           auto load_q = [&](int side) {
             const int qb = twin ? unit_q : side;
@@ -411,16 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             plan.part = (2 * static_cast<int>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0)) * p.srows;
             plan.by_row = 0;
             plan.head = seg.head;
-            if constexpr (PART) {
-              if (more && p.grouped) {  // a whole unit leaves its result by row, for the join
-                const int half = seg.of_head ? 0 : 1;
-                if (whole) plan.by_row = 1 + half;
-                plan.last = 0;
-                const size_t units = static_cast<size_t>(p.total) * p.g;
-                int* cut = p.cut + (2 * half) * units + static_cast<size_t>(seg.t0) * p.g + seg.j;
-                if (seg.lt0 == 0) cut[0] = whole ? -1 : static_cast<int>(blockIdx.x);
-                if (seg.lt0 > 0 && seg.lt1 == seg.ti) cut[units] = static_cast<int>(blockIdx.x);
-              }
+            if (more && p.grouped) {  // a whole unit leaves its result by row, for the join
+              const int half = seg.of_head ? 0 : 1;
+              if (whole) plan.by_row = 1 + half;
+              plan.last = 0;
+              const size_t units = static_cast<size_t>(p.total) * p.g;
+              int* cut = p.cut + (2 * half) * units + static_cast<size_t>(seg.t0) * p.g + seg.j;
+              if (seg.lt0 == 0) cut[0] = whole ? -1 : static_cast<int>(blockIdx.x);
+              if (seg.lt0 > 0 && seg.lt1 == seg.ti) cut[units] = static_cast<int>(blockIdx.x);
             }
           }
           __syncwarp();
@@ -444,14 +420,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = box_at(lt);
             row = oob_row;
             if constexpr (PAGED) {
-              if constexpr (!PART) ent = pc.get_lanes((lt * kN) >> sh);
               if (pos >= 0) {
                 if (ent >= 0 && ent < p.num_blocks)
                   row = (ent * p.g + seg.j) * p.bsz + (pos & mask);
                 else
                   atomicOr(p.status, GQA_DEV_BAD_BLOCK);
               }
-              if (PART && lt + 1 < seg.lt1) ent = entry(lt + 1);
+              if (lt + 1 < seg.lt1) ent = entry(lt + 1);
             } else if (pos >= 0) {
               row = pos + static_cast<int>(
                               (static_cast<long long>(source(lt)) * p.g + seg.j) * p.cap);
@@ -790,15 +765,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = my.nt, first = my.first, step = sp->step, see = my.hi + tok;
       const bool live = tok < my.tokens;
       const bool warp_live = (warp & 3) * 32 < my.tokens * p.r;  // (some row is)
-      // PART: this row sees [0, vis.head) and [vis.lo, vis.hi) of the unit's
+      // This row sees [0, vis.head) and [vis.lo, vis.hi) of the unit's
       // span; `side_vis`: what every row of the side sees
-      PartVisible vis = {0, 0, see}, side_vis = {0, 0, my.all_hi};
-      if constexpr (PART) {
-        side_vis = {my.all_head, my.all_lo, my.all_hi};
-        vis.lo = max(my.lo + tok, sp->lo_min);
-        vis.head = min(sp->head, see);
-        if (vis.lo <= vis.head) vis.lo = 0;
-      }
+      const PartVisible side_vis = {my.all_head, my.all_lo, my.all_hi};
+      PartVisible vis = {min(sp->head, see), max(my.lo + tok, sp->lo_min), see};
+      if (vis.lo <= vis.head) vis.lo = 0;
       if (sp->T == 0) break;
       // (lanes without a row hold anything: with their maximum at infinity they
       // have no say in when the others' is raised)
@@ -822,27 +793,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < kN; ++e) x[e] *= p.scale_log2;
         }
         const int base = first + t * step;
-        if constexpr (PART) {
-          if (!side_vis.all(base, kN)) {
-#pragma unroll
-            for (int c = 0; c < kN / 32; ++c) {
-              const int x0 = base + 32 * c;
-              if (side_vis.all(x0, 32)) continue;  // (uniform)
-              const uint32_t bits = vis.bits(x0);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
-            }
-          }
-        } else if (base + kN > side_vis.hi) {
-          // positions past this row's token, 32 at a time (those that the
-          // side's first token sees need no mask)
-          const int lim = see - 1 - base;
+        if (!side_vis.all(base, kN)) {
 #pragma unroll
           for (int c = 0; c < kN / 32; ++c) {
-            if (base + 32 * c + 32 <= side_vis.hi) continue;  // (uniform)
-            const int see = lim + 1 - 32 * c;
-            const uint32_t bits = see >= 32 ? ~0u : see <= 0 ? 0u : (1u << see) - 1u;
+            const int x0 = base + 32 * c;
+            if (side_vis.all(x0, 32)) continue;  // (uniform)
+            const uint32_t bits = vis.bits(x0);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(bits & (1u << e))) x[32 * c + e] = -INFINITY;
@@ -936,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = 1.f / l;
       float* pml = p.part_ml + 2 * (at + row);
       float* pdst = p.part_o + (at + row) * DV;
-      if (PART && by_row) {
+      if (by_row) {
         const size_t x = (by_row - 1) * static_cast<size_t>(p.total) * p.h + out_row;
         pml = p.row_ml + 2 * x;
         pdst = p.row_o + x * DV;
@@ -1231,8 +1187,7 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   CUtensorMap mq, mq1, mk, mv;
   const uint64_t rows = PAGED ? static_cast<uint64_t>(x.num_blocks) * x.g * x.bsz
                               : static_cast<uint64_t>(x.b) * x.g * x.cap;
-  constexpr int kBox = Walk::kPart ? kGrain : kN;
-  const uint32_t box_rows = (PAGED && x.bsz < kBox) ? x.bsz : kBox;
+  const uint32_t box_rows = (PAGED && x.bsz < kGrain) ? x.bsz : kGrain;
   const uint64_t qd[3] = {DK, static_cast<uint64_t>(x.h), static_cast<uint64_t>(x.total)};
   const uint64_t qs[2] = {DK * 2, static_cast<uint64_t>(x.h) * DK * 2};
   const uint32_t qb[3] = {64u, static_cast<uint32_t>(p.r), static_cast<uint32_t>(p.tq)};

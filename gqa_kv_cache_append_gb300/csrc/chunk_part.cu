@@ -1,6 +1,6 @@
 // chunk_part.cu - attention of packed chunks over a part of the cache (a sliding
 // window and the first positions) and over a prefix that the batch shares: the
-// kernel of chunk_kernel.cuh with another split of work.
+// kernel of chunk_kernel.cuh, and its split of work.
 //
 // Window.  A token at position P sees p <= P with p > P - window or p < sinks.
 // A unit of ntok tokens reads the span (part_device.cuh) of ceil(sinks / 64) *
@@ -84,7 +84,6 @@ constexpr unsigned kPartNear = 2;  // tiles
 
 struct PartWalk {
   using Seg = PartSeg;
-  static constexpr bool kPart = true;
 
   const ChunkParams& p;
   int n_head;    // tokens of the head's units (0: it has none)

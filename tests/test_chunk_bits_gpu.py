@@ -90,7 +90,8 @@ def test_random_cases():
             continue
         kw = dict(block=rng.choice([0, 0, 16, 64, 256]), dtype=rng.choice(["bf16", "f16"]))
         if rng.random() < 0.6:
-            kw.update(window=rng.choice([1, 30, 100, 300, 1000]), sinks=rng.choice([0, 1, 5, 64, 100]))
+            kw.update(window=rng.choice([1, 30, 100, 300, 1000]),
+                      sinks=rng.choice([0, 1, 5, 64, 100]))
             ls = [x + rng.choice([0, rng.randint(0, 100), rng.randint(0, 1500)]) for x in ns]
         else:
             kw["prefix"] = rng.choice([1, 40, 64, 100, 500, 1500])

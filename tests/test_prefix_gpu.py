@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 # new tokens, and positions between the prefix and them
 SHAPES = [
-    ([1], [0]), ([1, 1], [0, 5]), ([1] * 5, [0, 1, 63, 300, 1000]), ([0, 1, 1, 0, 2], [9, 0, 40, 3, 7]),
+    ([1], [0]), ([1, 1], [0, 5]), ([1] * 5, [0, 1, 63, 300, 1000]),
+    ([0, 1, 1, 0, 2], [9, 0, 40, 3, 7]),
     ([3, 1, 4], [130, 20, 0]), ([200, 1, 3], [5, 0, 40]), ([300], [20]), ([70, 90], [0, 400]),
 ]
 
