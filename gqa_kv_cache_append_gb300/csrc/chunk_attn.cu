@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(s_base + side * C::Q_BYTES + c * (kM * 128), &tm_q, BAR(C::Q_FULL + side),
                         64 * c, seg.j * p.r, seg.t0 + (seg.twin(p.tq) ? 0 : side * p.tq), pol);
         }
+        __syncwarp();
         ++qn[side];
       };
       auto load_kv = [&](bool is_v, int lt, int prow) {
@@ -492,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(dst + c * (kN * 128) + lane * box * 128, is_v ? &tm_v : &tm_k, bar, 64 * c,
                         row, pol);
         }
+        __syncwarp();
         if (edge) {
           ok = __all_sync(0xffffffffu, wait(C::V_EDGE, edge_n & 1));
           ++edge_n;
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              : "memory");
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::FULL + slot));
+            mbar_arrive_if(BAR(C::FULL + slot), lane == 0);
           }
         }
         ++slot_n;
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       r.nt[1] = __shfl_sync(0xffffffffu, seg.side_tiles(1, p.tq), 0);
       r.T = __shfl_sync(0xffffffffu, seg.lt1 - seg.lt0, 0);
       r.twin = __shfl_sync(0xffffffffu, seg.twin(p.tq) ? 1 : 0, 0) != 0;
-      if (elect_one()) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+      mbar_arrive_if(BAR(C::SEG_EMPTY + kn % kSegs), elect_one());
       ++kn;
       return r;
     };
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const ChunkSeg seg = *seg_at(kn);
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
+      mbar_arrive_if(BAR(C::SEG_EMPTY + kn % kSegs), lane == 0);
       if (seg.lt1 == seg.lt0) break;
       const int nt = seg.side_tiles(side, p.tq);
       const bool whole = seg.lt0 == 0 && seg.lt1 == seg.ti;
@@ -856,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::P_READY + side));
+        mbar_arrive_if(BAR(C::P_READY + side), lane == 0);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // complete too)
         ml_sm[side * kM + row] = make_float2(ms, l);
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::TWIN));
+        mbar_arrive_if(BAR(C::TWIN), lane == 0);
         ok = __all_sync(0xffffffffu, wait(C::TWIN, tn & 1));
         if (!ok) break;
         tc_fence_after();
@@ -941,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       if (twin) {  // both O and ml_sm are free again
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::TWIN + 1));
+        mbar_arrive_if(BAR(C::TWIN + 1), lane == 0);
         ok = __all_sync(0xffffffffu, wait(C::TWIN + 1, tn & 1));
         ++tn;
       }

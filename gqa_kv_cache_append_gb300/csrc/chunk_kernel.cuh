@@ -544,8 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.nt0 = __shfl_sync(0xffffffffu, sp->side[0].nt, 0);
         r.nt1 = r.T;  // (the later tokens: they see what the unit sees)
         __syncwarp();
-        if (elect_one()) mbar_arrive(BAR(C::SEG_EMPTY + kn % kSegs));
-        __syncwarp();
+        mbar_arrive_if(BAR(C::SEG_EMPTY + kn % kSegs), elect_one());
         ++kn;
         return r;
       };

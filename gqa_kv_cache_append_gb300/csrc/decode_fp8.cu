@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
             mma_commit(BAR(C::S_FULL + nb));
             if (t == T - 1) mma_commit(BAR(C::Q_EMPTY + qb));
           }
+          __syncwarp();
         } else {
           ok = __all_sync(0xffffffffu, wait(C::FULL_V + st, sph) &&
                                            wait(C::O_FREE + nb, nph ^ 1) &&
@@ -396,8 +397,8 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
             mma_commit(BAR(C::O_FULL + nb));
             mma_commit(BAR(C::EMPTY + st));
           }
+          __syncwarp();
         }
-        __syncwarp();
         if (nb ^= 1; nb == 0) nph ^= 1;
         if (++st == kRing) {
           st = 0;
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::Q_FULL + qb));
+      mbar_arrive_if(BAR(C::Q_FULL + qb), lane == 0);
       ++k;
     }
     __syncwarp();
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::O_FREE + nb));
+      mbar_arrive_if(BAR(C::O_FREE + nb), lane == 0);
       const float vf = vt * (1.f / 256.f);
       float al[HP], pt[HP];
       load_all(al, alpha_sm + nb * NR + h0);
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
           for (int e = 0; e < HP; ++e) x[hf][e] = fmaf(lo[hf][e], 1.f / kLo, x[hf][e]);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::S_FREE + nb));
+        mbar_arrive_if(BAR(C::S_FREE + nb), lane == 0);
         const float* qs = qs_sm + qb * NR + h0;
         if (all_seen) {
           // (uniform) every query row sees every position of the tile
@@ -749,12 +750,12 @@ __global__ void __launch_bounds__(F8Cfg<NR, DK, DV>::THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::P_READY + nb));
+        mbar_arrive_if(BAR(C::P_READY + nb), lane == 0);
         if (lt > seg.lt0) correct(n - 1, vm_last);
         if (lt == seg.lt1 - 1) correct(n, vm);
       }
       ++k;
-      if (lane == 0) mbar_arrive(BAR(C::Q_EMPTY + qb));
+      mbar_arrive_if(BAR(C::Q_EMPTY + qb), lane == 0);
       // ---- segment end: the row sums across the warpgroup, then the output
       // or a partial ----
       const uint32_t nb = (n - 1) & 1;

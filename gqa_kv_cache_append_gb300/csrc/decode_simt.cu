@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(SimtCfg<DT, DK, DV, RMAX>::THREADS, 1)
           }
         }
         named_bar_sync(1, kCompute);
-        if (ct == 0) mbar_arrive(empty0 + 8 * st);
+        mbar_arrive_if(empty0 + 8 * st, ct == 0);
       }
 
       // ---- segment end: reduce the position groups, write out: each

@@ -348,6 +348,7 @@ __global__ void __maxnreg__(NWG == 2 ? 168 : 200)
           tma_load_3d(qdst + qb * NP * 128, &tm_q, BAR(B_Q_FULL + qs), 64 * qb, sg.j * r,
                       sg.i * nq, pol_keep);
       }
+      __syncwarp();
       if (ok) last_q[qs] = static_cast<int>(kk);
     };
     bool waited = !early;
@@ -920,21 +921,26 @@ __global__ void __maxnreg__(NWG == 2 ? 168 : 200)
     // fold O of tile mt into the registers: o = o * alpha + O_tile
     auto correct = [&](uint32_t mt, const float* al) {
       const uint32_t nb = mt & 1;
-      const bool ok = mbar_wait(BAR(B_O_FULL + nb), (mt >> 1) & 1, abort_flag, status, budget);
+      // (loads of tensor memory are the whole warp's: made whatever a lane's wait
+      // said.  Where one gave up, the status is set and the values do not matter.)
+      mbar_wait(BAR(B_O_FULL + nb), (mt >> 1) & 1, abort_flag, status, budget);
+      __syncwarp();
+      tc_fence_after();
       float ov[OH][HP];
 #pragma unroll
       for (int hf = 0; hf < OH; ++hf) {
-        if (ok && (hf == 0 || vh > 2)) {
+        if (hf == 0 || vh > 2) {
           tmem_ld16(tO + (nb * OH + hf) * NP, ov[hf]);
         } else {
 #pragma unroll
           for (int e = 0; e < HP; ++e) ov[hf][e] = 0.f;
         }
       }
-      if (ok) tmem_wait_ld();
+      tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(B_O_FREE + nb));
+      __syncwarp();
 #pragma unroll
       for (int hf = 0; hf < OH; ++hf)
 #pragma unroll
@@ -971,30 +977,27 @@ __global__ void __maxnreg__(NWG == 2 ? 168 : 200)
         const uint32_t nb = n & 1;
         const int st = n % kStages;
         const int valid = min(TT, seg.L - lt * TT);
-        // ---- logits from TMEM (WIDE: both 128-position halves) ----
-        const bool ok = mbar_wait(BAR(B_S_FULL + nb), (n >> 1) & 1, abort_flag, status, budget);
+        // ---- logits from TMEM (WIDE: both 128-position halves; loaded by
+        // the whole warp, as in `correct`) ----
+        mbar_wait(BAR(B_S_FULL + nb), (n >> 1) & 1, abort_flag, status, budget);
+        __syncwarp();
+        tc_fence_after();
         float x[NH][HP];
-        if (ok) {
 #pragma unroll
-          for (int hf = 0; hf < NH; ++hf) {
+        for (int hf = 0; hf < NH; ++hf) {
 #pragma unroll
-            for (int c = 0; c < HP; c += 16) {
-              float tmp[16];
-              tmem_ld16(tS + (nb * NH + hf) * NP + c, tmp);
+          for (int c = 0; c < HP; c += 16) {
+            float tmp[16];
+            tmem_ld16(tS + (nb * NH + hf) * NP + c, tmp);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) x[hf][c + e] = tmp[e];
-            }
+            for (int e = 0; e < 16; ++e) x[hf][c + e] = tmp[e];
           }
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int hf = 0; hf < NH; ++hf)
-#pragma unroll
-            for (int e = 0; e < HP; ++e) x[hf][e] = 0.f;
         }
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_S_FREE + nb));
+        __syncwarp();
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
           const int pos = row + hf * kT;  // position within the tile
@@ -1135,6 +1138,7 @@ __global__ void __maxnreg__(NWG == 2 ? 168 : 200)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_P_READY + nb));
+        __syncwarp();
         // ---- fold O into the registers: the previous tile's, and at the
         // segment end this one's ----
         if (lt > seg.lt0) correct(n - 1, alpha_sm + ((n - 1) & 1) * NP);

@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(192, 1)
       const long long pend = tile1 < pos1 ? tile1 : pos1;
       const bool whole = (p == tile0 && pend == tile1);
       const int ab = sgi & 1;
-      const bool ok = mbar_wait(ACC_FULL(ab), (sgi >> 1) & 1, abort_flag, status, budget);
+      // (the whole warp's answer: so are the loads of tensor memory)
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(ACC_FULL(ab), (sgi >> 1) & 1, abort_flag,
+                                                        status, budget));
       // destination of column n of this tile's row: element offset and pitch
       __nv_bfloat16* dst;
       size_t pitch;
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(192, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ACC_FREE(ab));
+      mbar_arrive_if(ACC_FREE(ab), lane == 0);
       if (!whole) {
         long long c0, c1;
         unit_ctas(tile0, tile1, W, nc, c0, c1);

@@ -20,18 +20,6 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Arrival of one lane of a warp, as a predicated instruction: behind a branch the
-// compiler may let that lane run ahead of the others, past waits that are the
-// whole warp's.
-__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool arrives) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
-      "r"(arrives ? 1u : 0u)
-      : "memory");
-}
-
 // 16 bytes global -> shared without passing registers; the arrival of all of
 // this thread's earlier ones on an mbarrier (one of its count); their end
 __device__ __forceinline__ void async_copy16(uint32_t dst, const void* src) {
