@@ -400,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   ChunkPos* const run_end = reinterpret_cast<ChunkPos*>(sm + C::OFF_MISC + 16);
+  // (a warpgroup's four warps at the same instruction, as it has to be)
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == 9) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (blockIdx.x == 0) report_bad_packed(p.cu, p.lens, p.b, p.total, p.cap, p.status);
   } else if (warp == 11) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // the run's end, beside the TMA warp's look for its start
     ChunkWalk w;
     ChunkPos e;
@@ -415,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 10) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // ============================ TMA producer ============================
     ChunkWalk w;
     ChunkSeg seg;
@@ -544,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     // ============================ MMA issuer ==============================
     // The sides by turns: P.V of the side's last tile, then S of its next
     // (of the next unit's first at a unit's end).  One warp issues both sides'

@@ -60,3 +60,10 @@ def test_branches_of_one_lane_end_in_a_warp_barrier(name):
 def test_loads_of_tensor_memory_are_the_whole_warps(name):
     # one lane's answer to a bounded wait would split the warp before them
     assert not re.search(r"const bool ok = mbar_wait\(", text(name))
+
+
+@pytest.mark.parametrize("name", ["chunk_attn.cu", "chunk_kernel.cuh"])
+def test_a_warpgroup_splits_its_registers_at_one_instruction(name):
+    # all four warps of a warpgroup execute the same setmaxnreg
+    s = text(name)
+    assert s.count("setmaxnreg.dec") == 1 and s.count("setmaxnreg.inc") == 1
