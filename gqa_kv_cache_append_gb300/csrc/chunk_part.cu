@@ -86,14 +86,14 @@ struct PartWalk {
   using Seg = PartSeg;
 
   const ChunkParams& p;
-  int n_head;    // tokens of the head's units (0: it has none)
+  int n_head;    // packed rows of the head's units (0: it has none)
   int gran, head_pad;
   ChunkPos at, end;
   int t0, n, L;  // of sequence at.i
   bool more;
 
   __device__ explicit PartWalk(const ChunkParams& params) : p(params) {
-    n_head = head_tokens(p);
+    n_head = head_rows(p);
     gran = p.table != nullptr ? min(p.bsz, kGrain) : kGrain;
     head_pad = (p.head + gran - 1) & ~(gran - 1);
   }
@@ -111,9 +111,36 @@ struct PartWalk {
     bad = __reduce_or_sync(0xffffffffu, bad);
     if (bad && (threadIdx.x & 31) == 0) atomicOr(p.status, bad);
   }
-  // tokens that the head's units hold
-  __device__ static int head_tokens(const ChunkParams& p) {
-    return p.grouped ? min(max(__ldg(p.cu + p.b), 0), p.total) : 0;
+  // Rows that the head's units hold: up to the end of the last usable sequence.
+  // (The entries of cu behind an unusable one say nothing, cu[b] among them.)
+  // Warp-cooperative.
+  __device__ static int head_rows(const ChunkParams& p) {
+    if (!p.grouped) return 0;
+    int end = 0;
+    for (int i = threadIdx.x & 31; i < p.b; i += 32) {
+      const int a0 = __ldg(p.cu + i), a1 = __ldg(p.cu + i + 1);
+      if (a1 > a0 && !errors(a0, a1, __ldg(p.lens + i), p.total, p.cap, p.base_min))
+        end = max(end, a1);
+    }
+    return __reduce_max_sync(0xffffffffu, end);
+  }
+  // Does usable sequence i hold packed row t?
+  __device__ static bool holds(const ChunkParams& p, int i, int t) {
+    const int a0 = __ldg(p.cu + i), a1 = __ldg(p.cu + i + 1);
+    return a0 <= t && t < a1 && !errors(a0, a1, __ldg(p.lens + i), p.total, p.cap, p.base_min);
+  }
+  // The usable sequence that holds packed row t (p.b: none).  cu need not ascend
+  // around an unusable sequence: where the search by it misses, every sequence is
+  // looked at.  Warp-cooperative.
+  __device__ static int sequence_of(const ChunkParams& p, int t) {
+    const int i = packed_sequence(p.cu, p.b, t);
+    if (i < p.b && holds(p, i, t)) return i;
+    for (int base = 0; base < p.b; base += 32) {
+      const int k = base + (threadIdx.x & 31);
+      const unsigned hit = __ballot_sync(0xffffffffu, k < p.b && holds(p, k, t));
+      if (hit) return base + __ffs(hit) - 1;
+    }
+    return p.b;
   }
   template <typename T16, int DV>
   static cudaError_t join(cudaLaunchConfig_t& cfg, const ChunkParams& p, int num_sms);
@@ -322,13 +349,10 @@ __global__ void __launch_bounds__(kGroupThreads) group_join_kernel(const ChunkPa
   const int a_first = 2 * static_cast<int>(id - tj * pairs);
   const int t = static_cast<int>(tj / p.g);
   const int j = static_cast<int>(tj - static_cast<long long>(t) * p.g);
-  const int T = PartWalk::head_tokens(p);
-  if (t >= T) return;  // (uniform across the warp, as all below)
-  const int i = packed_sequence(p.cu, p.b, t);
+  if (t >= p.total) return;  // (uniform across the warp, as all below)
+  const int i = PartWalk::sequence_of(p, t);
   if (i >= p.b) return;
-  const int a0 = __ldg(p.cu + i), a1 = __ldg(p.cu + i + 1);
-  if (t < a0 || t >= a1 || PartWalk::errors(a0, a1, __ldg(p.lens + i), p.total, p.cap, p.base_min))
-    return;
+  const int a0 = __ldg(p.cu + i);
   // the units that hold the token: over the head, over its own positions
   const int w = 2 * p.tq;
   const int u0[2] = {t / w * w, a0 + (t - a0) / w * w};
