@@ -145,12 +145,13 @@ struct ChunkParams {
   // from its own); positions below base_min belong to the head alone
   int window, head, head_seq, base_min;
   unsigned unit_inv;   // 2^32 / (2 tq), rounded up
-  // the head is attended by units of its own, over the rows of all sequences,
-  // and every unit leaves partial results
-  bool grouped;
-  int* cut;            // [2][2][total * g]: a unit's first CTA (-1: not cut), its last
-  float* row_ml;       // [2][total * h][2] partial results of whole units
-  float* row_o;        // [2][total * h][d_v]
+  // the head may be attended by units of its own, over the rows of all
+  // sequences, when those are group_rows or fewer (0: never); every unit leaves
+  // partial results then
+  int group_rows;
+  int* cut;            // [2][2][group_rows * g]: a unit's first CTA (-1: not cut), its last
+  float* row_ml;       // [2][group_rows * h][2] partial results of whole units
+  float* row_o;        // [2][group_rows * h][d_v]
 };
 
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
@@ -190,8 +191,9 @@ struct SegPlan {
 };
 static_assert(sizeof(SegPlan) <= kSegBytes, "segment ring");
 
-// desc of CTA c: a unit cut at its run's end (head) or start (tail / middle)
-enum { D_HEAD = 0, D_TOK0 = 1, D_NTOK = 2, D_J = 3, D_END = 4 };
+// desc of CTA c: a unit cut at its run's end (head) or start (tail / middle); the
+// rows of the head's own units, the same from every CTA
+enum { D_HEAD = 0, D_TOK0 = 1, D_NTOK = 2, D_J = 3, D_END = 4, D_ROWS = 5 };
 
 template <typename T16, int DK, int DV, bool PAGED, class Walk>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -389,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             plan.part = (2 * static_cast<int>(blockIdx.x) + (seg.lt0 == 0 ? 1 : 0)) * p.srows;
             plan.by_row = 0;
             plan.head = seg.head;
-            if (more && p.grouped) {  // a whole unit leaves its result by row, for the join
+            if (more && w.n_head > 0) {  // a whole unit leaves its result by row, for the join
               const int half = seg.of_head ? 0 : 1;
               if (whole) plan.by_row = 1 + half;
               plan.last = 0;
-              const size_t units = static_cast<size_t>(p.total) * p.g;
+              const size_t units = static_cast<size_t>(p.group_rows) * p.g;
               int* cut = p.cut + (2 * half) * units + static_cast<size_t>(seg.t0) * p.g + seg.j;
               if (seg.lt0 == 0) cut[0] = whole ? -1 : static_cast<int>(blockIdx.x);
               if (seg.lt0 > 0 && seg.lt1 == seg.ti) cut[units] = static_cast<int>(blockIdx.x);
@@ -474,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           d[D_NTOK] = d_ntok;
           d[D_J] = d_j;
           d[D_END] = ok ? d_end : 1;
+          d[D_ROWS] = w.n_head;
         }
         if (ok && lane == 0) {  // no more edges
           *reinterpret_cast<int4*>(sm + C::OFF_EDGE + 16 * (edge_n % kEdges)) =
@@ -892,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* pml = p.part_ml + 2 * (at + row);
       float* pdst = p.part_o + (at + row) * DV;
       if (by_row) {
-        const size_t x = (by_row - 1) * static_cast<size_t>(p.total) * p.h + out_row;
+        const size_t x = (by_row - 1) * static_cast<size_t>(p.group_rows) * p.h + out_row;
         pml = p.row_ml + 2 * x;
         pdst = p.row_o + x * DV;
       }
@@ -971,15 +974,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // positions: M = max m, out = sum 2^(m - M) O / sum 2^(m - M) l, in the
 // pieces' order.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinRows = 32;  // at a time
 
-template <typename T16, int DV>
-__global__ void __launch_bounds__(kJoinThreads, 2)
-    chunk_join_kernel(const ChunkParams p, int nc) {
+// Rows [row0, row1) of side `side` of the unit whose first piece is CTA c's, by a
+// block of WARPS warps.
+template <typename T16, int DV, int WARPS>
+__device__ __forceinline__ void join_rows(const ChunkParams& p, int nc, int c, int side, int row0,
+                                          int row1) {
   constexpr int CPL = DV / 32;  // columns a lane
   constexpr int NP = 4;         // pieces at a time
-  pdl_wait_then_release();
-  const int c = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 d4 = __ldg(reinterpret_cast<const int4*>(p.desc + static_cast<size_t>(c) * kDescInts));
   // the CTA that holds the unit's last piece
@@ -993,11 +995,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   }
   if (!d4.x || last < 0) return;  // (none cut here)
   const int tok0 = d4.y, ntok = d4.z, j = d4.w;
-  for (int base = 0; base < kM; base += kJoinRows) {
+  for (int base = row0; base < row1; base += 2 * WARPS) {
     int row[2], orow[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int side = blockIdx.y, rr = base + 2 * warp + s, tok = rr / p.r;
+      const int rr = base + 2 * warp + s, tok = rr / p.r;
       const int t = side * p.tq + tok;
       row[s] = side * kM + rr;
       orow[s] = (tok < p.tq && t < ntok) ? t * p.h + (rr - tok * p.r) : -1;
@@ -1070,6 +1072,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   }
 }
 
+template <typename T16, int DV>
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    chunk_join_kernel(const ChunkParams p, int nc) {
+  pdl_wait_then_release();
+  join_rows<T16, DV, kJoinThreads / 32>(p, nc, blockIdx.x, blockIdx.y, 0, kM);
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -1084,7 +1093,7 @@ struct ChunkCall {
   long long ws_bytes;
   // a part of the cache, as in ChunkParams
   int window = 0, head = 0, head_seq = -1, base_min = 0;
-  bool grouped = false;
+  int group_rows = 0;
 };
 
 struct ChunkPlan {
@@ -1092,7 +1101,7 @@ struct ChunkPlan {
   size_t ml_at = 0, o_at = 0, cut_at = 0, row_ml_at = 0, row_o_at = 0, bytes = 0;
 };
 
-ChunkPlan chunk_plan(int total, int h, int g, int dv, int num_sms, bool grouped = false) {
+ChunkPlan chunk_plan(int total, int h, int g, int dv, int num_sms, int group_rows = 0) {
   ChunkPlan pl;
   const int r = h / g, tq = kM / r;
   pl.srows = total <= tq ? kM : 2 * kM;
@@ -1101,8 +1110,8 @@ ChunkPlan chunk_plan(int total, int h, int g, int dv, int num_sms, bool grouped 
   const size_t rows = 2 * static_cast<size_t>(num_sms) * pl.srows;
   pl.o_at = up(pl.ml_at + rows * 2 * sizeof(float));
   pl.bytes = up(pl.o_at + rows * dv * sizeof(float));
-  if (grouped) {
-    const size_t t = total;
+  if (group_rows > 0) {
+    const size_t t = group_rows;
     pl.cut_at = pl.bytes;
     pl.row_ml_at = up(pl.cut_at + 4 * t * g * sizeof(int));
     pl.row_o_at = up(pl.row_ml_at + 4 * t * h * sizeof(float));
@@ -1178,7 +1187,7 @@ cudaError_t launch_chunk(const ChunkCall& x, const ChunkPlan& pl, int num_sms,
   p.head = x.head;
   p.head_seq = x.head_seq;
   p.base_min = x.base_min;
-  p.grouped = x.grouped;
+  p.group_rows = x.group_rows;
   p.cut = reinterpret_cast<int*>(ws + pl.cut_at);
   p.row_ml = reinterpret_cast<float*>(ws + pl.row_ml_at);
   p.row_o = reinterpret_cast<float*>(ws + pl.row_o_at);

@@ -34,6 +34,29 @@
 namespace gqa {
 namespace {
 
+// Are the prefix's units to be shared by the sequences?  (b sequences with `rows`
+// packed rows in all; tq: tokens of a side.)  Shared, a row's two results are
+// written, read back and joined; not shared, every sequence reads the prefix for its
+// own rows.  Measured, n tokens a sequence, us shared / not: 16 sequences behind
+// 6,000 (tq = 32) n = 1 21 / 52, n = 31 58 / 64, n = 64 116 / 85; 64 behind 8,192 (tq
+// = 16) n = 1 57 / 222, n = 15 228 / 237, n = 32 441 / 334; 4 behind 3,000 (tq = 18)
+// n = 17 22 / 34; 16 behind 700 n = 1 18 / 21, n = 4 24 / 21.5, n = 31 36 / 32: with few
+// positions in common the join costs more than their tiles.
+constexpr int kLongPrefix = 2048;
+
+__host__ __device__ __forceinline__ bool prefix_grouped(int b, int rows, int tq, int prefix_len) {
+  return b > 1 && prefix_len > 0 && rows < static_cast<long long>(b) * tq &&
+         (prefix_len >= kLongPrefix || rows <= 2ll * b);
+}
+
+// The most rows of up to b sequences that it says yes to, of at most `total` (0:
+// none).
+int group_rows(int b, int total, int tq, int prefix_len) {
+  if (b < 2 || tq < 2 || prefix_len < 1) return 0;
+  const long long few = std::min<long long>(total, static_cast<long long>(b) * tq - 1);
+  return static_cast<int>(prefix_len >= kLongPrefix ? few : std::min(few, 2ll * b));
+}
+
 struct PartSeg {
   int i, j;        // sequence, KV head
   int t0;          // packed row of the unit's first token
@@ -111,18 +134,23 @@ struct PartWalk {
     bad = __reduce_or_sync(0xffffffffu, bad);
     if (bad && (threadIdx.x & 31) == 0) atomicOr(p.status, bad);
   }
-  // Rows that the head's units hold: up to the end of the last usable sequence.
-  // (The entries of cu behind an unusable one say nothing, cu[b] among them.)
-  // Warp-cooperative.
+  // Rows that units of the head's own hold (0: it has none): up to the end of the
+  // last usable sequence.  (The entries of cu behind an unusable one say nothing,
+  // cu[b] among them.)  Decided by the tokens that are there, not by the call's
+  // `total` and b, which may leave room for more.  Warp-cooperative.
   __device__ static int head_rows(const ChunkParams& p) {
-    if (!p.grouped) return 0;
-    int end = 0;
+    if (p.group_rows == 0) return 0;
+    int end = 0, count = 0;
     for (int i = threadIdx.x & 31; i < p.b; i += 32) {
       const int a0 = __ldg(p.cu + i), a1 = __ldg(p.cu + i + 1);
-      if (a1 > a0 && !errors(a0, a1, __ldg(p.lens + i), p.total, p.cap, p.base_min))
+      if (a1 > a0 && !errors(a0, a1, __ldg(p.lens + i), p.total, p.cap, p.base_min)) {
         end = max(end, a1);
+        ++count;
+      }
     }
-    return __reduce_max_sync(0xffffffffu, end);
+    end = __reduce_max_sync(0xffffffffu, end);
+    count = __reduce_add_sync(0xffffffffu, count);
+    return prefix_grouped(count, end, p.tq, p.head) ? end : 0;
   }
   // Does usable sequence i hold packed row t?
   __device__ static bool holds(const ChunkParams& p, int i, int t) {
@@ -175,7 +203,7 @@ struct PartWalk {
   };
   __device__ Shape shape(int k, int nn, int Lk) const {
     Shape s;
-    const unsigned pad = p.grouped ? 0 : head_pad;
+    const unsigned pad = n_head > 0 ? 0 : head_pad;
     s.nu = units(nn);
     s.tw = nn - (s.nu - 1) * 2 * p.tq <= p.tq;
     s.A = Lk - nn - p.base_min + (p.head_seq >= 0 ? pad : 0);
@@ -201,7 +229,7 @@ struct PartWalk {
     s.pos0 = Lk - nn + first;
     s.ntok = min(nn - first, 2 * p.tq);
     s.L = Lk;
-    s.head = p.grouped && k >= 0 ? 0 : p.head;
+    s.head = n_head > 0 && k >= 0 ? 0 : p.head;
     const int lo = max(p.base_min, s.pos0 - p.window + 1);
     const int lo_all = max(p.base_min, Lk - nn - p.window + 1);
     const PartSpan t = part_span(lo, lo_all, s.head, gran, p.table != nullptr,
@@ -330,26 +358,15 @@ struct PartWalk {
   }
 };
 
-// Joins, for every row, the partial results over the head and over the
-// sequence's own positions, each whole (by row) or in pieces (by CTA).  A warp
-// takes two query heads of a token's group, four pieces of both with their
-// loads side by side.
-constexpr int kGroupThreads = 256;
-
+// Joins, for a row of two query heads of a token's group, the partial results over the
+// head and over the sequence's own positions, each whole (by row) or in pieces (by
+// CTA), by a warp, four pieces of both heads with their loads side by side.
 template <typename T16, int DV>
-__global__ void __launch_bounds__(kGroupThreads) group_join_kernel(const ChunkParams p, int nc) {
+__device__ __forceinline__ void join_group(const ChunkParams& p, int nc, int t, int j,
+                                           int a_first) {
   constexpr int CPL = DV / 32;
   constexpr int NP = 4;
-  pdl_wait_then_release();
   const int lane = threadIdx.x & 31;
-  const int pairs = (p.r + 1) >> 1;
-  const long long id =
-      static_cast<long long>(blockIdx.x) * (kGroupThreads / 32) + (threadIdx.x >> 5);
-  const long long tj = id / pairs;
-  const int a_first = 2 * static_cast<int>(id - tj * pairs);
-  const int t = static_cast<int>(tj / p.g);
-  const int j = static_cast<int>(tj - static_cast<long long>(t) * p.g);
-  if (t >= p.total) return;  // (uniform across the warp, as all below)
   const int i = PartWalk::sequence_of(p, t);
   if (i >= p.b) return;
   const int a0 = __ldg(p.cu + i);
@@ -359,7 +376,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_join_kernel(const ChunkPa
   int first[2], cnt[2], row0[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const size_t units = static_cast<size_t>(p.total) * p.g;
+    const size_t units = static_cast<size_t>(p.group_rows) * p.g;
     const int* cut = p.cut + (2 * k) * units + static_cast<size_t>(u0[k]) * p.g + j;
     // (held within the launch's CTAs: where a wait gave up they may not have
     // been written)
@@ -388,7 +405,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_join_kernel(const ChunkPa
         const int x = own ? first[1] + (k0 + k - cnt[0]) : first[0] + k0 + k;  // its CTA
         const bool by_row = own ? first[1] < 0 : first[0] < 0;
         const size_t at =
-            by_row ? (own ? static_cast<size_t>(p.total) * p.h : 0) + orow + a
+            by_row ? (own ? static_cast<size_t>(p.group_rows) * p.h : 0) + orow + a
                    : static_cast<size_t>(2 * x + (x == (own ? first[1] : first[0]) ? 1 : 0)) *
                              p.srows +
                          (own ? row0[1] : row0[0]) + a;
@@ -443,33 +460,43 @@ __global__ void __launch_bounds__(kGroupThreads) group_join_kernel(const ChunkPa
   }
 }
 
+// What follows a launch whose head may have had units of its own: the rows of both
+// kinds if it had, else the units that a run's end cut, half a side to a block.
+constexpr int kGroupThreads = 256;
+
+template <typename T16, int DV>
+__global__ void __launch_bounds__(kGroupThreads) group_join_kernel(const ChunkParams p, int nc) {
+  pdl_wait_then_release();
+  constexpr int kWarps = kGroupThreads / 32;
+  // (held within what the workspace has room for)
+  const int rows = min(__ldg(p.desc + D_ROWS), p.group_rows);
+  if (rows <= 0) {
+    const int sides = p.srows / kM, c = blockIdx.x / (2 * sides), k = blockIdx.x % (2 * sides);
+    if (c < nc)
+      join_rows<T16, DV, kWarps>(p, nc, c, k >> 1, (k & 1) * (kM / 2), ((k & 1) + 1) * (kM / 2));
+    return;
+  }
+  const int pairs = (p.r + 1) >> 1;
+  const long long n = static_cast<long long>(rows) * p.g * pairs;
+  for (long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); id < n;
+       id += static_cast<long long>(gridDim.x) * kWarps) {
+    const long long tj = id / pairs;
+    const int t = static_cast<int>(tj / p.g);
+    join_group<T16, DV>(p, nc, t, static_cast<int>(tj - static_cast<long long>(t) * p.g),
+                        2 * static_cast<int>(id - tj * pairs));
+  }
+}
+
 template <typename T16, int DV>
 cudaError_t PartWalk::join(cudaLaunchConfig_t& cfg, const ChunkParams& p, int num_sms) {
-  if (!p.grouped) return launch_join<T16, DV>(cfg, p, num_sms);
-  const long long warps = static_cast<long long>(p.total) * p.g * ((p.r + 1) / 2);
+  if (p.group_rows == 0) return launch_join<T16, DV>(cfg, p, num_sms);
+  const long long warps = static_cast<long long>(p.group_rows) * p.g * ((p.r + 1) / 2);
   constexpr int kWarps = kGroupThreads / 32;
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps));
+  const long long most = std::min<long long>((warps + kWarps - 1) / kWarps, 8ll * num_sms);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<long long>(most, 2ll * (p.srows / kM) * num_sms)));
   cfg.blockDim = dim3(kGroupThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, group_join_kernel<T16, DV>, p, num_sms);
-}
-
-// Are the prefix's units to be shared by the sequences?  (tq: tokens of a side)
-// Shared, a row's two results are written, read back and joined; not shared,
-// every sequence reads the prefix for its own rows.  Measured, n tokens a
-// sequence, us shared / not: 16 sequences behind 6,000 (tq = 32) n = 1 21 / 52, n =
-// 31 58 / 64, n = 64 116 / 85; 64 behind 8,192 (tq = 16) n = 1 57 / 222, n = 15 228
-// / 237, n = 32 441 / 334; 4 behind 3,000 (tq = 18) n = 17 22 / 34; 16 behind 700 n =
-// 1 18 / 21, n = 4 24 / 21.5, n = 31 36 / 32: with few positions in common the join
-// costs more than their tiles.
-bool prefix_few(int b, int total, int tq) {
-  return b > 1 && total < static_cast<long long>(b) * tq;
-}
-constexpr int kLongPrefix = 2048;
-
-bool prefix_grouped(int b, int total, int tq, int prefix_len) {
-  return prefix_few(b, total, tq) && prefix_len > 0 &&
-         (prefix_len >= kLongPrefix || total <= 2ll * b);
 }
 
 int part_run(const ChunkCall& x, void* stream) {
@@ -478,7 +505,7 @@ int part_run(const ChunkCall& x, void* stream) {
   int num_sms = 0;
   unsigned int* status = nullptr;
   if (int e = device_query(&num_sms, &status)) return e;
-  const ChunkPlan pl = chunk_plan(x.total, x.h, x.g, x.dv, num_sms, x.grouped);
+  const ChunkPlan pl = chunk_plan(x.total, x.h, x.g, x.dv, num_sms, x.group_rows);
   if (x.ws_bytes < static_cast<long long>(pl.bytes)) return GQA_ERR_SCRATCH_LIMIT;
   if (x.total == 0) return GQA_OK;
   const cudaError_t e =
@@ -500,7 +527,7 @@ int prefix_run(ChunkCall& x, int prefix_len, void* stream) {
   x.head = x.base_min = prefix_len;
   x.head_seq = 0;
   if (x.g > 0 && x.h > 0 && x.h / x.g >= 1 && x.h / x.g <= kM)
-    x.grouped = prefix_grouped(x.b, x.total, kM / (x.h / x.g), prefix_len);
+    x.group_rows = group_rows(x.b, x.total, kM / (x.h / x.g), prefix_len);
   return part_run(x, stream);
 }
 
@@ -567,13 +594,9 @@ int gqa_chunk_attn_prefix_workspace(int b, int total, int h, int g, int d_k, int
     unsigned int* status = nullptr;
     if (int e = device_query(&num_sms, &status)) return e;
   }
-  // (of any number of rows up to `total`: the most that are still grouped)
-  const int tq = kM / (h / g);
-  const long long most = std::min<long long>(total, static_cast<long long>(b) * tq - 1);
-  size_t n = chunk_plan(total, h, g, d_v, num_sms).bytes;
-  if (prefix_few(b, static_cast<int>(most), tq))
-    n = std::max(n, chunk_plan(static_cast<int>(most), h, g, d_v, num_sms, true).bytes);
-  *bytes = static_cast<long long>(n);
+  // (behind a long prefix, which may share most rows)
+  const int rows = group_rows(b, total, kM / (h / g), kLongPrefix);
+  *bytes = static_cast<long long>(chunk_plan(total, h, g, d_v, num_sms, rows).bytes);
   return GQA_OK;
 }
 

@@ -47,3 +47,41 @@ def test_a_bad_block_takes_its_own_sequence_alone(prefix):
     c.table[1, (prefix + 40) // 16] = -1
     c.run()
     c.check(status=B.GQA_DEV_BAD_BLOCK, rows=[0, 3, 4, 5])
+
+
+@pytest.mark.parametrize("block", [0, 64])
+@pytest.mark.parametrize("prefix", [200, 2500])
+@pytest.mark.parametrize("ns", [[1] * 6, [2, 0, 1, 3, 1], [9, 3, 17]])
+def test_room_for_more_rows_changes_nothing(ns, prefix, block):
+    """Bits depend on the tokens that are there, not on `total` (a captured step
+    has room for more rows)."""
+    c = Part(ns, [prefix + 40 * i + n for i, n in enumerate(ns)], 8, 2, prefix=prefix, block=block,
+             pad=32 * len(ns) + 1)
+    c.run()
+    c.check()
+    padded = c.out.clone()
+    for total in (c.t, c.t + 3, 2 * len(ns) + 1):
+        if total < c.t:
+            continue
+        c.out.fill_(5.0)
+        c.run(total=total)
+        c.check()
+        assert torch.equal(c.out, padded)
+
+
+@pytest.mark.parametrize("prefix", [200, 2500])
+@pytest.mark.parametrize("ns", [[1, 1, 1], [20, 40, 30], [1], [33, 40]])
+def test_room_for_more_sequences_changes_nothing(ns, prefix):
+    """... nor on how many empty sequences a batch has."""
+    more = ns + [0] * 61
+    c = Part(more, [prefix + 70 * i + n for i, n in enumerate(ns)] + [0] * 61, 8, 2, prefix=prefix,
+             block=16)
+    c.run()
+    c.check()
+    many = c.out.clone()
+    c.out.fill_(5.0)
+    c.b = len(ns)
+    c.run(workspace=torch.empty(binding().gqa_chunk_attn_prefix_workspace(
+        c.b, c.total, c.h, c.g, c.dk, c.dv), dtype=torch.uint8, device="cuda"))
+    c.check()
+    assert torch.equal(c.out, many)
