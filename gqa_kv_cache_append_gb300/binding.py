@@ -208,6 +208,12 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _i32(x) -> int:
+    """A number of positions as the library's 32-bit integer: held within its
+    range, beyond every length there can be (ctypes would drop the upper bits)."""
+    return max(-0x80000000, min(int(x), 0x7FFFFFFF))
+
+
 def _check(fn: str, code: int) -> None:
     if code != GQA_OK:
         raise GqaError(fn, code)
@@ -751,7 +757,7 @@ def gqa_chunk_attn_window(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k
     among them) and the first `sinks` of its sequence.  workspace: as for
     gqa_chunk_attn."""
     _chunk("gqa_chunk_attn_window", q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v,
-           scale, (int(window), int(sinks)), out, total, cap, dtype, workspace, stream,
+           scale, (_i32(window), _i32(sinks)), out, total, cap, dtype, workspace, stream,
            gqa_chunk_attn_workspace)
 
 
@@ -761,7 +767,7 @@ def gqa_chunk_attn_window_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_l
     """gqa_chunk_attn_window over a paged cache; table entries of blocks that
     hold no position that is seen are not looked at."""
     _chunk_paged("gqa_chunk_attn_window_paged", q, k_pool, v_pool, block_table, cu_tokens,
-                 seq_lens, b, h, g, d_k, d_v, scale, (int(window), int(sinks)), out, total,
+                 seq_lens, b, h, g, d_k, d_v, scale, (_i32(window), _i32(sinks)), out, total,
                  dtype, workspace, stream, gqa_chunk_attn_workspace)
 
 
@@ -782,7 +788,7 @@ def gqa_chunk_attn_prefix(q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k
     tensor of gqa_chunk_attn_prefix_workspace bytes (by default one is made
     per call)."""
     _chunk("gqa_chunk_attn_prefix", q, k_cache, v_cache, cu_tokens, seq_lens, b, h, g, d_k, d_v,
-           scale, (int(prefix_len),), out, total, cap, dtype, workspace, stream,
+           scale, (_i32(prefix_len),), out, total, cap, dtype, workspace, stream,
            gqa_chunk_attn_prefix_workspace, b)
 
 
@@ -792,7 +798,7 @@ def gqa_chunk_attn_prefix_paged(q, k_pool, v_pool, block_table, cu_tokens, seq_l
     """gqa_chunk_attn_prefix over a paged cache: the prefix is found through
     row 0 of the block table."""
     _chunk_paged("gqa_chunk_attn_prefix_paged", q, k_pool, v_pool, block_table, cu_tokens,
-                 seq_lens, b, h, g, d_k, d_v, scale, (int(prefix_len),), out, total, dtype,
+                 seq_lens, b, h, g, d_k, d_v, scale, (_i32(prefix_len),), out, total, dtype,
                  workspace, stream, gqa_chunk_attn_prefix_workspace, b)
 
 
@@ -842,7 +848,7 @@ def gqa_decode_attn_fp8_window_paged(q, k_pool, v_pool, k_scale, v_scale, block_
     of blocks that hold none of them are not looked at.  workspace: as for
     gqa_decode_attn_fp8_paged."""
     _decode_fp8("gqa_decode_attn_fp8_window_paged", q, k_pool, v_pool, k_scale, v_scale,
-                block_table, seq_lens, b, h, g, d_k, d_v, scale, (int(window), int(sinks)), out,
+                block_table, seq_lens, b, h, g, d_k, d_v, scale, (_i32(window), _i32(sinks)), out,
                 n, dtype, workspace, stream)
 
 
