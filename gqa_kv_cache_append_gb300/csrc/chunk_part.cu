@@ -36,25 +36,37 @@ namespace {
 
 // Are the prefix's units to be shared by the sequences?  (b sequences with `rows`
 // packed rows in all; tq: tokens of a side.)  Shared, a row's two results are
-// written, read back and joined; not shared, every sequence reads the prefix for its
-// own rows.  Measured, n tokens a sequence, us shared / not: 16 sequences behind
-// 6,000 (tq = 32) n = 1 21 / 52, n = 31 58 / 64, n = 64 116 / 85; 64 behind 8,192 (tq
-// = 16) n = 1 57 / 222, n = 15 228 / 237, n = 32 441 / 334; 4 behind 3,000 (tq = 18)
-// n = 17 22 / 34; 16 behind 700 n = 1 18 / 21, n = 4 24 / 21.5, n = 31 36 / 32: with few
-// positions in common the join costs more than their tiles.
-constexpr int kLongPrefix = 2048;
-
-__host__ __device__ __forceinline__ bool prefix_grouped(int b, int rows, int tq, int prefix_len) {
-  return b > 1 && prefix_len > 0 && rows < static_cast<long long>(b) * tq &&
-         (prefix_len >= kLongPrefix || rows <= 2ll * b);
+// written, read back and joined, which grows with the rows; not shared, every
+// sequence reads the prefix for its own rows, which grows with the prefix.  With
+// fewer than 64 units (a sequence and KV head each) those are cut among the SMs
+// anyway, and their tiles cost no time that a few rows' join would not.
+// Measured, us shared / not, n tokens a sequence:
+//   16 sequences, h = 32, g = 8 (tq = 32): behind 700 n = 1 18.0 / 20.0, 4 21.6 /
+//     21.2, 31 37.3 / 27.1; 1,400 n = 8 25.0 / 26.9, 16 31.4 / 29.7; 2,500 n = 16
+//     35.2 / 36.5, 31 48.2 / 41.8; 6,000 n = 31 63.2 / 68.9
+//   64, h = 64, g = 8 (16): 350 n = 1 37.0 / 40.2, 2 44.1 / 40.4; 1,400 n = 4 62.0 /
+//     66.4, 8 79.1 / 69.1; 3,500 n = 8 104 / 124, 15 151 / 141; 8,192 n = 15 228 / 282
+//   12, h = 64, g = 8: 350 n = 1 16.1 / 16.1, 2 17.5 / 17.1
+//   128, h = 8, g = 2 (32): 350 n = 1 29.1 / 27.9; 700 n = 1 28.4 / 31.9
+//   32, h = 8, g = 1 (16), so 32 units: 3,000 n = 1 21.4 / 18.8, 8 23.8 / 24.4; 6,000
+//     n = 1 24.8 / 23.4, 15 28.1 / 32.1
+//   4, h = 28, g = 4 (18), 16 units: 700 n = 1 14.5 / 13.6, 17 18.8 / 18.2; 1,400 n = 8
+//     18.5 / 19.3; 6,000 n = 1 19.3 / 17.9, 17 26.9 / 29.1
+//   2, h = 32, g = 8, 16 units: 20,000 n = 1 28.8 / 30.9
+__host__ __device__ __forceinline__ bool prefix_grouped(int b, int rows, int tq, int g,
+                                                        int prefix_len) {
+  const long long room = static_cast<long long>(b) * tq;  // rows that fill a side for each
+  if (b < 2 || prefix_len < 1 || rows >= room) return false;
+  const float units = static_cast<float>(b) * static_cast<float>(g);
+  const float reads = units * static_cast<float>(prefix_len);  // positions, not shared
+  if (units < 64.f) return 8ll * rows >= 3 * room ? prefix_len >= 1024 : reads >= 160000.f;
+  return 4096ll * rows <= room * prefix_len && reads >= 80000.f;
 }
 
-// The most rows of up to b sequences that it says yes to, of at most `total` (0:
-// none).
+// Rows that may share at most, of up to b sequences and `total` rows (0: none).
 int group_rows(int b, int total, int tq, int prefix_len) {
-  if (b < 2 || tq < 2 || prefix_len < 1) return 0;
-  const long long few = std::min<long long>(total, static_cast<long long>(b) * tq - 1);
-  return static_cast<int>(prefix_len >= kLongPrefix ? few : std::min(few, 2ll * b));
+  if (b < 2 || prefix_len < 1) return 0;
+  return static_cast<int>(std::min<long long>(total, static_cast<long long>(b) * tq - 1));
 }
 
 struct PartSeg {
@@ -150,7 +162,7 @@ struct PartWalk {
     }
     end = __reduce_max_sync(0xffffffffu, end);
     count = __reduce_add_sync(0xffffffffu, count);
-    return prefix_grouped(count, end, p.tq, p.head) ? end : 0;
+    return prefix_grouped(count, end, p.tq, p.g, p.head) ? end : 0;
   }
   // Does usable sequence i hold packed row t?
   __device__ static bool holds(const ChunkParams& p, int i, int t) {
@@ -593,8 +605,7 @@ int gqa_chunk_attn_prefix_workspace(int b, int total, int h, int g, int d_k, int
     unsigned int* status = nullptr;
     if (int e = device_query(&num_sms, &status)) return e;
   }
-  // (behind a long prefix, which may share most rows)
-  const int rows = group_rows(b, total, kM / (h / g), kLongPrefix);
+  const int rows = group_rows(b, total, kM / (h / g), 1);
   *bytes = static_cast<long long>(chunk_plan(total, h, g, d_v, num_sms, rows).bytes);
   return GQA_OK;
 }

@@ -630,9 +630,9 @@ int gqa_chunk_attn_window_paged(const void* q, const void* k_pool, const void* v
  * Rows p < prefix_len of sequences other than 0 and rows p >= L_i may hold
  * anything; the prefix and the rows prefix_len <= p < L_i hold finite values.
  * Otherwise as gqa_chunk_attn; cap (paged: max_blocks * block_size) up to
- * 2^31 - 256.  Where sequences bring few tokens each (the tokens that are there
- * below 128 / (h / g) times the sequences that bring some; at most twice them
- * behind a prefix of less than 2,048) the prefix is attended once for many of them
+ * 2^31 - 256.  Where sequences bring few tokens each, measured by the prefix (fewer
+ * than 128 / (h / g) on average, and fewer the shorter the prefix; some thousand
+ * positions of it at least) the prefix is attended once for many of them
  * and joined with each one's own positions, else once for each.  Room for more
  * rows or sequences (a total above cu_tokens[b], sequences without tokens) changes
  * neither that nor any bit.
