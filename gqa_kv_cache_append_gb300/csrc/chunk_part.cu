@@ -510,29 +510,37 @@ cudaError_t PartWalk::join(cudaLaunchConfig_t& cfg, const ChunkParams& p, int nu
   return cudaLaunchKernelEx(&cfg, group_join_kernel<T16, DV>, p, num_sms);
 }
 
-int part_run(const ChunkCall& x, void* stream) {
+template <typename T16, int DK, int DV, bool PAGED>
+struct PartLaunch {
+  static cudaError_t run(const PartCall& x, const PartPlan& pl, int num_sms, unsigned int* status,
+                         cudaStream_t st) {
+    return launch_chunk<T16, DK, DV, PAGED, PartWalk>(x, pl, num_sms, status, st);
+  }
+};
+
+int part_run(const PartCall& x, void* stream) {
   if (int e = chunk_check(x)) return e;
   if (x.cap > 0x7FFFFF00) return GQA_ERR_SHAPE;  // (indices of a span stay within 31 bits)
   int num_sms = 0;
   unsigned int* status = nullptr;
   if (int e = device_query(&num_sms, &status)) return e;
-  const ChunkPlan pl = chunk_plan(x.total, x.h, x.g, x.dv, num_sms, x.group_rows);
+  const PartPlan pl = part_plan(x.total, x.h, x.g, x.dv, num_sms, x.group_rows);
   if (x.ws_bytes < static_cast<long long>(pl.bytes)) return GQA_ERR_SCRATCH_LIMIT;
   if (x.total == 0) return GQA_OK;
   const cudaError_t e =
-      launch_chunk_types<PartWalk>(x, pl, num_sms, status, static_cast<cudaStream_t>(stream));
+      chunk_dispatch<PartLaunch>(x, pl, num_sms, status, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 // (cap: positions that the cache can hold)
-int window_run(ChunkCall& x, int window, int sinks, void* stream) {
+int window_run(PartCall& x, int window, int sinks, void* stream) {
   if (window < 1 || sinks < 0) return GQA_ERR_SHAPE;
   x.window = std::min(window, std::max(x.cap, 1));
   x.head = std::min(sinks, std::max(x.cap, 0));
   return part_run(x, stream);
 }
 
-int prefix_run(ChunkCall& x, int prefix_len, void* stream) {
+int prefix_run(PartCall& x, int prefix_len, void* stream) {
   if (prefix_len < 0 || (x.cap >= 1 && prefix_len > x.cap)) return GQA_ERR_SHAPE;
   x.window = std::max(x.cap, 1);
   x.head = x.base_min = prefix_len;
@@ -554,8 +562,10 @@ int gqa_chunk_attn_window(const void* q, const void* k_cache, const void* v_cach
                           int h, int g, int d_k, int d_v, float scale, int window, int sinks,
                           void* out, int cap, int dtype, void* workspace,
                           long long workspace_bytes, void* stream) {
-  ChunkCall x = {q, k_cache, v_cache, cu_tokens, seq_lens, nullptr, b, total, h, g, d_k,
-                 d_v, scale, out, cap, 0, 0, 0, dtype, workspace, workspace_bytes};
+  PartCall x;
+  static_cast<ChunkCall&>(x) = {q, k_cache, v_cache, cu_tokens, seq_lens, nullptr, b, total, h, g,
+                                d_k, d_v, scale, out, cap, 0, 0, 0, dtype, workspace,
+                                workspace_bytes};
   return window_run(x, window, sinks, stream);
 }
 
@@ -566,9 +576,10 @@ int gqa_chunk_attn_window_paged(const void* q, const void* k_pool, const void* v
                                 int block_size, int max_blocks, int num_blocks, int dtype,
                                 void* workspace, long long workspace_bytes, void* stream) {
   if (int e = paged_args_check(block_table, g, block_size, max_blocks, num_blocks)) return e;
-  ChunkCall x = {q, k_pool, v_pool, cu_tokens, seq_lens, block_table, b, total, h, g, d_k,
-                 d_v, scale, out, max_blocks * block_size, block_size, max_blocks,
-                 num_blocks, dtype, workspace, workspace_bytes};
+  PartCall x;
+  static_cast<ChunkCall&>(x) = {q, k_pool, v_pool, cu_tokens, seq_lens, block_table, b, total, h, g,
+                                d_k, d_v, scale, out, max_blocks * block_size, block_size,
+                                max_blocks, num_blocks, dtype, workspace, workspace_bytes};
   return window_run(x, window, sinks, stream);
 }
 
@@ -577,8 +588,10 @@ int gqa_chunk_attn_prefix(const void* q, const void* k_cache, const void* v_cach
                           int h, int g, int d_k, int d_v, float scale, int prefix_len, void* out,
                           int cap, int dtype, void* workspace, long long workspace_bytes,
                           void* stream) {
-  ChunkCall x = {q, k_cache, v_cache, cu_tokens, seq_lens, nullptr, b, total, h, g, d_k,
-                 d_v, scale, out, cap, 0, 0, 0, dtype, workspace, workspace_bytes};
+  PartCall x;
+  static_cast<ChunkCall&>(x) = {q, k_cache, v_cache, cu_tokens, seq_lens, nullptr, b, total, h, g,
+                                d_k, d_v, scale, out, cap, 0, 0, 0, dtype, workspace,
+                                workspace_bytes};
   return prefix_run(x, prefix_len, stream);
 }
 
@@ -589,9 +602,10 @@ int gqa_chunk_attn_prefix_paged(const void* q, const void* k_pool, const void* v
                                 int max_blocks, int num_blocks, int dtype, void* workspace,
                                 long long workspace_bytes, void* stream) {
   if (int e = paged_args_check(block_table, g, block_size, max_blocks, num_blocks)) return e;
-  ChunkCall x = {q, k_pool, v_pool, cu_tokens, seq_lens, block_table, b, total, h, g, d_k,
-                 d_v, scale, out, max_blocks * block_size, block_size, max_blocks,
-                 num_blocks, dtype, workspace, workspace_bytes};
+  PartCall x;
+  static_cast<ChunkCall&>(x) = {q, k_pool, v_pool, cu_tokens, seq_lens, block_table, b, total, h, g,
+                                d_k, d_v, scale, out, max_blocks * block_size, block_size,
+                                max_blocks, num_blocks, dtype, workspace, workspace_bytes};
   return prefix_run(x, prefix_len, stream);
 }
 
@@ -606,7 +620,7 @@ int gqa_chunk_attn_prefix_workspace(int b, int total, int h, int g, int d_k, int
     if (int e = device_query(&num_sms, &status)) return e;
   }
   const int rows = group_rows(b, total, kM / (h / g), 1);
-  *bytes = static_cast<long long>(chunk_plan(total, h, g, d_v, num_sms, rows).bytes);
+  *bytes = static_cast<long long>(part_plan(total, h, g, d_v, num_sms, rows).bytes);
   return GQA_OK;
 }
 
