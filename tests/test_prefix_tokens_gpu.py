@@ -156,3 +156,33 @@ def test_shared_head_groups(h, g):
     want = c.t if h // g < 128 else 0  # (a token's rows fill a side)
     assert shared_rows(c) == (want if 128 // (h // g) > 1 else 0)
     c.check()
+
+
+def test_rows_ahead_of_the_first_sequence():
+    """cu_tokens need not begin at zero."""
+    c = Part([3, 1, 2], [2507, 2540, 2560], 64, 32, 64, 64, prefix=2500, block=16)
+    c.cu[0] = 1  # sequence 0 has two new tokens then, at the same positions
+    assert shared_rows(c) == 6
+    c.check(rows=slice(1, 6))
+    assert (c.out[0] == 5.0).all()
+
+
+def test_one_graph_takes_both_forms():
+    """A captured call whose tokens change between replays: not shared, shared, not
+    shared."""
+    c = Part([90, 100, 80], [2700, 2650, 2600], 64, 32, 64, 64, prefix=2500, block=32)
+    n = binding().gqa_chunk_attn_prefix_workspace(c.b, c.total, c.h, c.g, c.dk, c.dv)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    c.run(workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(workspace=ws)
+    many = c.ns
+    for ns in (many, [1, 2, 1], many, [0, 4, 30], [1, 0, 0]):
+        c.ns, c.t = list(ns), sum(ns)
+        c.cu.copy_(torch.tensor([0, ns[0], ns[0] + ns[1], sum(ns)], dtype=torch.int32))
+        c.out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(ws[:32].view(torch.int32)[5]) == (sum(ns) if 1 < sum(ns) < 40 else 0)
+        c.check()
