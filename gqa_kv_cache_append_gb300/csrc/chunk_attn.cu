@@ -46,14 +46,13 @@
 // Rows >= L_i: masked out of S, their V rows zeroed in shared memory.
 //
 // Bound by the tensor cores where units are long: a prompt of 8,192 tokens,
-// h = 64, g = 8, d = 128, bf16: 649 to 653 us, 1,690 TFLOP/s, in a short graph
-// replay, 704 to 718 us, 1,530 to 1,560, among other passes, as the clock falls
-// under the power limit.  What the pipe still waits for is a side's own chain
-// of S, softmax and hand-over, which is a little longer than the other side's
-// products.  Short units are bound by their fixed cost (query rows in, first
-// logits, output): 130 to 141 us for 32 mixed sequences of 5,957 tokens, 33.8
-// us for 48 packed short prompts with 64-wide heads, 17.8 us for eight chunks
-// of 4 to 12 tokens.
+// h = 64, g = 8, d = 128, bf16: 649 to 657 us, 1,680 TFLOP/s, in a short graph replay,
+// 684 to 709 us over several boxes, 1,550 to 1,610, among other passes, as the clock
+// falls under the power limit.  What the pipe still waits for is a side's own chain of
+// S, softmax and hand-over, which is a little longer than the other side's products.  Short units are bound by their
+// fixed cost (query rows in, first logits, output): 135 to 145 us for 32 mixed
+// sequences of 5,957 tokens, 34.8 us for 48 packed short prompts with 64-wide heads,
+// 18.1 us for eight chunks of 4 to 12 tokens.
 #include "chunk_common.cuh"
 
 namespace gqa {

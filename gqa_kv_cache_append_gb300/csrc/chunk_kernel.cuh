@@ -60,11 +60,13 @@
 // Rows that no token of the sequence sees: masked out of S, their V rows zeroed in
 // shared memory.
 //
-// Used by chunk_part.cu, whose PartWalk gives the units, where their rows lie and
-// what their tokens see.  chunk_attn.cu has a kernel of its own for causal chunks
-// over the whole cache, with the same products and the same roles, but units
-// looked at by each role for itself: on this kernel a causal prompt of 8,192 took
-// 731 us where that takes 710, packed short prompts 36.4 (34.3).  Figures of this
+// Used by chunk_part.cu alone, whose PartWalk (the one Walk there is; it stands
+// behind the kernel, with its joins) gives the units, where their rows lie and what
+// their tokens see.  chunk_attn.cu has a kernel of its own for causal chunks over the
+// whole cache, with the same products and the same roles, but units looked at by each
+// role for itself: on this kernel, without what is not needed there, a causal prompt of
+// 8,192 took 731 us where that took 715, 32 mixed sequences 138.6 (134.8), packed
+// short prompts 36.4 (34.6).  What both share is in chunk_common.cuh.  Figures of this
 // one: chunk_part.cu.
 #pragma once
 

@@ -4,8 +4,10 @@
 //
 // Window.  A token at position P sees p <= P with p > P - window or p < sinks.
 // A unit of ntok tokens reads the span (part_device.cuh) of ceil(sinks / 64) *
-// 64 + window + ntok - 1 positions at most, not the P + 1 of the causal form;
-// its first and last tiles are masked row by row, the others are seen whole.
+// 64 + window + ntok - 1 positions at most, not the P + 1 of the causal form (up to
+// 63 more where a paged window's first box, 64 positions or a block, begins before
+// it; the split of work leaves those out); its first and last tiles are masked row
+// by row, the others are seen whole.
 //
 // Prefix.  Positions below prefix_len are the same rows for every sequence.
 // Where sequences bring few tokens, the prefix is attended by units of its own
@@ -16,15 +18,15 @@
 // units that one sequence fills the prefix is the head of the unit's span: the
 // tiles read are the same and nothing has to be joined.
 //
-// Measured (graph replay, bf16, d = 128; floors at the measured copy and GEMM
-// rates).  64 single tokens over windows of 4,096, h = 64, g = 8, 64-row blocks:
-// 170 us, 6,250 GB/s (157): HBM, then 4 us of start and the join.  A prompt of
-// 8,192 in a window of 2,048: 352 us (254): 17 tiles a unit of 32 tokens where 16
-// are seen, 4 us from one unit to the next (three tiles' time), the clock under
-// load.  32 mixed sequences, 7,506 tokens, window 1,000: 124 us (38): units of six
-// tiles, join.  64 single tokens behind a prefix of 8,192: 62 us (22): 512 units
-// of five tiles and the prefix's long ones beside them.  16 chunks of 50 to 400
-// tokens behind 6,000: 211 us (147).
+// Measured (graph replay, bf16, d = 128, over several boxes; floors at the measured
+// copy and GEMM rates).  64 single tokens over windows of 4,096, h = 64, g = 8, 64-row
+// blocks: 168 to 170 us, 6,250 GB/s (157): HBM, then 4 us of start and the join.  A
+// prompt of 8,192 in a window of 2,048: 350 to 371 us (254): 17 tiles a unit of 32
+// tokens where 16 are seen, 4 us from one unit to the next (three tiles' time), the
+// clock under load.  32 mixed sequences, 7,506 tokens, window 1,000: 121 to 125 us
+// (38): units of six tiles, join.  64 single tokens behind a prefix of 8,192: 57 us
+// (22): 512 units of five tiles and the prefix's long ones beside them.  16 chunks of
+// 50 to 400 tokens behind 6,000: 211 to 224 us (147).
 //
 // Boxes of 64 positions (or a block): with 128, a few sinks cost a whole tile and
 // a window begins up to 127 positions early; with 16, a tile is 64 copies.

@@ -595,7 +595,10 @@ int gqa_chunk_attn_workspace(int total, int h, int g, int d_k, int d_v, int num_
  * gqa_chunk_attn_workspace gives), errors and supported shapes as for
  * gqa_chunk_attn; cap (paged: max_blocks * block_size) up to 2^31 - 256.
  * Only rows that some new token of the sequence sees are used: rows p >= L_i
- * and rows sinks <= p <= L_i - n_i - window may hold anything.
+ * and rows sinks <= p <= L_i - n_i - window may hold anything.  The others hold
+ * finite values (a NaN reaches the tokens that see it; an infinity or NaN that one
+ * new token sees may reach the sequence's other new tokens, past whose window it lies
+ * or who come before it).
  *
  * gqa_chunk_attn_window_paged - the same over a paged cache.  Entries of blocks
  * that hold no row that is used are not looked at (an engine may have given
