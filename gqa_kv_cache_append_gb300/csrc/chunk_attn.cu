@@ -47,7 +47,7 @@
 //
 // Bound by the tensor cores where units are long: a prompt of 8,192 tokens,
 // h = 64, g = 8, d = 128, bf16: 649 to 657 us, 1,680 TFLOP/s, in a short graph replay,
-// 684 to 709 us over several boxes, 1,550 to 1,610, among other passes, as the clock
+// 684 to 709 us over several GPUs, 1,550 to 1,610, among other passes, as the clock
 // falls under the power limit.  What the pipe still waits for is a side's own chain of
 // S, softmax and hand-over, which is a little longer than the other side's products.  Short units are bound by their
 // fixed cost (query rows in, first logits, output): 135 to 145 us for 32 mixed

@@ -18,7 +18,7 @@
 // units that one sequence fills the prefix is the head of the unit's span: the
 // tiles read are the same and nothing has to be joined.
 //
-// Measured (graph replay, bf16, d = 128, over several boxes; floors at the measured
+// Measured (graph replay, bf16, d = 128, over several GPUs; floors at the measured
 // copy and GEMM rates).  64 single tokens over windows of 4,096, h = 64, g = 8, 64-row
 // blocks: 168 to 170 us, 6,250 GB/s (157): HBM, then 4 us of start and the join.  A
 // prompt of 8,192 in a window of 2,048: 350 to 371 us (254): 17 tiles a unit of 32
